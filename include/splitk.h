@@ -87,8 +87,15 @@ enum splitk_status {
        mapped into the device address space. */
     SPLITK_ERR_NOT_MAPPED = -12,
     /* splitk_gemm_bf16_noalloc(): the stream is capturing a CUDA graph. */
-    SPLITK_ERR_CAPTURE = -13
+    SPLITK_ERR_CAPTURE = -13,
+    /* A type code, an epsilon or a count outside its range. */
+    SPLITK_ERR_INVALID_ARGUMENT = -14
 };
+
+/* Element types, where an argument may have one of several. */
+#define SPLITK_DTYPE_BF16 0
+#define SPLITK_DTYPE_F32 1
+#define SPLITK_DTYPE_F16 2
 
 /* Flags of splitk_gemm_bf16_planned(). */
 #define SPLITK_FLAG_NO_PDL 0x1u
@@ -449,6 +456,91 @@ SPLITK_API int splitk_gemm_bf16_zerocopy(const void *a, const void *b_host, void
 SPLITK_API int splitk_gemm_bf16_noalloc(const void *a, const void *b, void *c,
                                         int M, int N, int K, int L, int split_k,
                                         splitk_stream_t stream);
+
+/*
+ * ---- Around the projection: 8-bit codes and log probabilities ----
+ *
+ * A decode step around these calls: splitk_rmsnorm_i8() adds a projection's
+ * output to the residual stream and leaves the normed activations as 8-bit
+ * codes with a scale per token, splitk_gemm_i8() multiplies them with weights
+ * held as codes with a scale per channel, and after the last projection
+ * splitk_logprobs() reads the vocabulary's logits.
+ *
+ * These calls own no memory and keep nothing between calls.  They launch in
+ * the stream's programmatic-dependent-launch chain and read nothing before
+ * the work ahead of them in the stream has completed, so any operand may be
+ * written by the kernel before.  Rows are at 64-bit offsets.  Buffers must not
+ * overlap, except as said.
+ */
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit codes, for M rows
+ * (tokens) of D features:
+ *     y = x[m] + residual[m]                   (f32)
+ *     residual_out[m] = y                      (rounded to its type)
+ *     n = y * weight / sqrt(mean(y^2) + eps)   (f32, of the unrounded y)
+ *     scale[m] = max(max|n| / 127, 2^-126)
+ *     q[m] = n / scale[m] rounded to nearest even, -127..127
+ *   x             bf16, rows x_stride elements apart (x_stride >= D)
+ *   residual      [M][D] bf16 or f32 (residual_type), or NULL with
+ *                 residual_out NULL: y = x and no sum is written.
+ *   residual_out  [M][D] of the same type; may be `residual` itself
+ *   weight        [D] bf16 or f32 (weight_type)
+ *   eps           > 0
+ *   q             [M][D] 8-bit codes;  scale  [M] f32
+ * A row that holds a NaN or an infinity, or whose sum of squares passes the
+ * f32 range, has scale NaN; its codes then mean nothing.
+ */
+SPLITK_API int splitk_rmsnorm_i8(const void *x, long long x_stride, const void *residual,
+                                 void *residual_out, int residual_type, const void *weight,
+                                 int weight_type, float eps, void *q, float *scale, int M,
+                                 int D, splitk_stream_t stream);
+
+/*
+ * The codes and scales alone (n = x above): activations that follow no norm,
+ * or weights (a row is then a channel).
+ */
+SPLITK_API int splitk_quantize_i8(const void *x, long long x_stride, void *q, float *scale,
+                                  int M, int D, splitk_stream_t stream);
+
+/*
+ * Matrix product of 8-bit codes with a scale per channel and per token:
+ *     C[l][m][n] = round( a_scale[l][n] * b_scale[l][m]
+ *                         * sum_k A[l][n][k] * B[l][m][k]  + bias[l][n] )
+ *   a_q      [L][N][K] weight codes (-128..127), 16-byte aligned
+ *   a_scale  [L][N] f32
+ *   b_q      [L][M][K] token codes, 16-byte aligned;  b_scale  [L][M] f32
+ *   bias     [L][N] bf16, or NULL
+ *   c        [L][M][N] bf16 or f32 (c_type)
+ * K must be a multiple of 16.  The products are exact and summed in f32, so
+ * the sum is exact while its partial sums stay below 2^24 in magnitude (any
+ * codes at all up to K = 1024); it is rounded once more, by the output's type.
+ */
+SPLITK_API int splitk_gemm_i8(const void *a_q, const float *a_scale, const void *b_q,
+                              const float *b_scale, const void *bias, void *c, int c_type,
+                              int M, int N, int K, int L, splitk_stream_t stream);
+
+/*
+ * Log probabilities of M rows of V logits (V <= 2^22):
+ *     logprob[m] = x[m][tokens[m]] - log(sum exp(x[m]))
+ *     entropy[m] = -sum p log p
+ *     top_ids[m], top_logprobs[m]: the top_k most probable tokens in order,
+ *     equal logits by the lowest index
+ *   logits  bf16, f16 or f32 (logits_type), rows `stride` elements apart
+ *           (stride >= V), any alignment of their type
+ *   tokens  [M], or NULL with logprob NULL.  A token outside 0..V-1 has
+ *           logprob NaN.
+ *   top_k   0..32, at most V; 0: no alternatives, their pointers are unused
+ * Masked logits are -inf (log probability -inf) or the type's lowest value.
+ * A row whose every logit is -inf has no probabilities: its log
+ * probabilities are -inf, its entropy 0, its alternatives 0, 1, 2, ...  A NaN
+ * or +inf in a row makes its log probabilities and entropy NaN; its
+ * alternatives are then some tokens of the row.
+ */
+SPLITK_API int splitk_logprobs(const void *logits, int logits_type, long long stride,
+                               const long long *tokens, float *logprob, float *entropy,
+                               int top_k, long long *top_ids, float *top_logprobs, int M,
+                               int V, splitk_stream_t stream);
 
 /*
  * Diagnostic record of the first bounded wait that ran out on the current

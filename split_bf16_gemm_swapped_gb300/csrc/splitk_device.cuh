@@ -121,6 +121,17 @@ __device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t a, u
                : "memory");
 }
 
+// A word of a cluster peer's shared memory (address from mapa).
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  return __uint_as_float(ld_cluster_u32(cluster_addr));
+}
+
 // ---------------------------------------------------------------- PDL
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

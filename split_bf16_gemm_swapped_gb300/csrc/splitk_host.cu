@@ -851,7 +851,8 @@ int current_device(DeviceState** out, int* dev_out) {
     }
     if (major != 10 || minor != 3) return SPLITK_ERR_UNSUPPORTED_DEVICE;
     if (!encode_fn()) return SPLITK_ERR_CUDA;
-    if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess) {
+    if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess ||
+        prepare_logprobs() != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
@@ -1205,6 +1206,15 @@ void* mapped_device_pointer(const void* host) {
 }
 
 }  // namespace
+
+int require_device(DeviceSize* out) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* st = nullptr;
+  const int rc = current_device(&st, nullptr);
+  if (rc == SPLITK_OK && out) *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin};
+  return rc;
+}
+
 }  // namespace splitk
 
 using namespace splitk;
@@ -1654,6 +1664,7 @@ SPLITK_API const char* splitk_strerror(int code) {
     case SPLITK_ERR_BAD_PLAN: return "plan does not match the shape";
     case SPLITK_ERR_SCRATCH: return "the call needs more scratch than the allocation-free array holds";
     case SPLITK_ERR_NOT_MAPPED: return "host buffer is not page-locked and mapped into the device address space";
+    case SPLITK_ERR_INVALID_ARGUMENT: return "an argument is outside its range (a type code, an epsilon, a count)";
     case SPLITK_ERR_CAPTURE: return "the allocation-free entry point cannot run inside a CUDA graph capture";
     default: return "unknown status code";
   }

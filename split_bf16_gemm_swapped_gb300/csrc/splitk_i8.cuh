@@ -1,0 +1,60 @@
+// 8-bit integer codes on the f16 tensor path.
+//
+// GB300's tensor cores have no fast 8-bit integer rate, but f16 holds every
+// whole number up to 2048 exactly, the product of two codes is exact in the
+// f32 accumulator, and so is a sum of them while its magnitude stays below
+// 2^24 (any K up to 1024 whatever the codes; the partial sums of quantised
+// activations and weights are far below it).  Past 2^24 the sum is rounded as
+// f32 additions are.
+#pragma once
+
+#include <stdint.h>
+
+#include "splitk_device.cuh"
+
+namespace splitk {
+namespace dev {
+
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four codes (the bytes of `w`) as two words of two f16, in order.  With the
+// sign bit flipped a byte is code + 128; under the byte 0x64 it reads as the
+// f16 1024 + (code + 128), and subtracting 1152 leaves the code, exactly.
+__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = f16x2_sub(prmt(u, 0x64646464u, 0x4140u), 0x64806480u);
+  hi = f16x2_sub(prmt(u, 0x64646464u, 0x4342u), 0x64806480u);
+}
+
+}  // namespace dev
+
+// The operands of one product (splitk_gemm_i8).
+struct I8Params {
+  const int8_t* a;          // weight codes [L][N][K]
+  const int8_t* b;          // token codes [L][M][K]
+  const float* a_scale;     // [L][N]
+  const float* b_scale;     // [L][M]
+  const uint16_t* bias;     // bf16 [L][N], or null
+  void* c;                  // bf16 or f32 [L][M][N]
+  bool c_f32;
+  int M, N, K, L;
+};
+
+// The sum `v` of output (l, m, n) with its scales and bias, stored: one
+// rounding, from f32.
+__device__ __forceinline__ void store_i8_result(const I8Params& p, int l, int m, int n, float v) {
+  v = v * p.b_scale[(long long)l * p.M + m] * p.a_scale[(long long)l * p.N + n];
+  if (p.bias != nullptr) v += __uint_as_float((uint32_t)p.bias[(long long)l * p.N + n] << 16);
+  const long long at = ((long long)l * p.M + m) * p.N + n;
+  if (p.c_f32) {
+    static_cast<float*>(p.c)[at] = v;
+  } else {
+    static_cast<uint16_t*>(p.c)[at] = (uint16_t)(dev::pack_bf16x2(v, 0.0f) & 0xFFFFu);
+  }
+}
+
+}  // namespace splitk

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "splitk.h"
+
 namespace splitk {
 
 // Tile constants.  The weight tile is 128 rows (tcgen05 MMA M for one CTA);
@@ -160,5 +162,48 @@ cudaError_t launch_persistent(const LaunchArgs& la, const CUtensorMap& b_map,
 cudaError_t max_active_clusters_persistent(int mma_n, unsigned cluster_x, size_t smem, int* out);
 cudaError_t prepare_persistent(int max_dynamic_smem);
 cudaError_t read_and_clear_fault_persistent(int* out_words);
+
+// Defined in splitk_host.cu: whether the current device can run this
+// library (SPLITK_OK or SPLITK_ERR_UNSUPPORTED_DEVICE / SPLITK_ERR_CUDA),
+// and its size.
+struct DeviceSize {
+  int num_sms;
+  size_t smem_per_sm;
+  size_t smem_optin;
+};
+int require_device(DeviceSize* out);
+
+// Defined in splitk_logprobs.cu.
+cudaError_t prepare_logprobs();
+
+// The status of a launch, with CUDA's own error record cleared.
+inline int launched(cudaError_t e) {
+  if (e == cudaSuccess) return SPLITK_OK;
+  cudaGetLastError();
+  return SPLITK_ERR_CUDA;
+}
+
+// One kernel in the stream's programmatic-dependent-launch chain, in clusters
+// of `cluster_x` CTAs.  The kernel waits (griddepcontrol.wait) before it
+// reads or writes global memory that other kernels write.
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, unsigned cluster_x,
+                           cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster_x;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster_x > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace splitk

@@ -1,0 +1,446 @@
+// Log probabilities of a vocabulary's logits: splitk_logprobs().
+//
+// For a row x of V logits, with m = max x:
+//   S = sum exp(x - m),  T = sum exp(x - m) (x - m)
+//   logprob(i) = x[i] - m - log S,   entropy = log S - T / S
+// and the k largest logits, equal ones by the lowest index.
+//
+// One pass reads the row.  A warp takes 256 consecutive logits (a group) at a
+// time and keeps a running maximum with S and T rescaled when it grows; the
+// group's maximum, needed for that anyway, is also written down.  The k best
+// groups by (maximum, lowest index) hold the k best logits: a logit of any
+// other group has those k groups' maxima before it.  So only k groups are
+// read a second time, whatever the logits are.
+//
+// A cluster of CTAs shares a row when there are few rows; the first CTA then
+// reads the others' sums and maxima from their shared memory.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "splitk.h"
+#include "splitk_device.cuh"
+#include "splitk_internal.h"
+
+namespace splitk {
+
+namespace {
+
+constexpr int kThreadsLp = 512;
+constexpr int kWarpsLp = kThreadsLp / 32;
+constexpr int kGroup = 256;                 // logits of a group
+constexpr int kMaxTop = 32;
+constexpr int kMaxVocab = 1 << 22;
+constexpr int kFewCandidates = 128;         // candidates ranked by counting; more are drawn one by one
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kFarBelow = -1000.0f;       // in powers of two: exp is 0, and so is exp times it
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+struct LogprobParams {
+  const void* x;             // [rows][stride]
+  long long stride;
+  const long long* tokens;   // [rows], or null
+  float* logprob;            // [rows], or null
+  float* entropy;            // [rows]
+  long long* top_ids;        // [rows][k], or null
+  float* top_logprobs;       // [rows][k], or null
+  int rows, V, k;
+};
+
+// kType: 1 bf16, 2 f32, 3 f16 (the codes of splitk.h plus one).
+template <int kType>
+struct Logit;
+template <>
+struct Logit<1> {
+  static constexpr int kPerLoad = 8;
+  using T = uint16_t;
+  __device__ static float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  __device__ static void unpack(const uint4& w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+__device__ __forceinline__ float f16_one(uint16_t v) {
+  float f;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v));
+  return f;
+}
+template <>
+struct Logit<3> {
+  static constexpr int kPerLoad = 8;
+  using T = uint16_t;
+  __device__ static float one(uint16_t v) { return f16_one(v); }
+  __device__ static void unpack(const uint4& w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = f16_one((uint16_t)(u[i] & 0xFFFFu));
+      f[2 * i + 1] = f16_one((uint16_t)(u[i] >> 16));
+    }
+  }
+};
+template <>
+struct Logit<2> {
+  static constexpr int kPerLoad = 4;
+  using T = float;
+  __device__ static float one(float v) { return v; }
+  __device__ static void unpack(const uint4& w, float* f) {
+    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+  }
+};
+
+__device__ __forceinline__ float exp2_approx(float v) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// A number that orders as the logit does (-0 as 0); 0 stands below every
+// logit, and a NaN above.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+
+// A row as 16-byte words: position p counts from the aligned address at or
+// before the row's first logit, so logit i stands at p = i + shift.  A word
+// that reaches over either end is read one logit at a time, and what is not
+// of the row reads as -inf.
+template <int kType>
+struct Row {
+  using E = Logit<kType>;
+  const typename E::T* x;
+  int shift, V;
+  __device__ Row(const LogprobParams& p, int row)
+      : x(static_cast<const typename E::T*>(p.x) + (long long)row * p.stride), V(p.V) {
+    shift = (int)(((uintptr_t)x & 15u) / sizeof(typename E::T));
+  }
+  __device__ int groups() const { return (shift + V + kGroup - 1) / kGroup; }
+  // word of positions [p, p + kPerLoad)
+  __device__ __forceinline__ void load(int p, float* f) const {
+    const int i = p - shift;
+    if (i >= 0 && i + E::kPerLoad <= V) {
+      const uint4 w = *reinterpret_cast<const uint4*>(x + i);
+      E::unpack(w, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E::kPerLoad; ++j) {
+        f[j] = i + j >= 0 && i + j < V ? E::one(x[i + j]) : -INFINITY;
+      }
+    }
+  }
+  // a lane's eight logits of group `g`: positions at(g, lane, j)
+  __device__ static int at(int g, int lane, int j) {
+    return g * kGroup + (j / E::kPerLoad) * 32 * E::kPerLoad + lane * E::kPerLoad + j % E::kPerLoad;
+  }
+  __device__ __forceinline__ void load_group(int g, int lane, float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; j += E::kPerLoad) load(at(g, lane, j), f + j);
+  }
+};
+
+// Sums relative to a maximum; in powers of two (d = (x - m) log2 e).
+struct Sums {
+  float m, s, t;
+  // the same sums relative to `to` >= m
+  __device__ __forceinline__ void rebase(float to) {
+    if (m == -INFINITY) {                  // nothing but masked logits so far: s and t are 0 (or NaN)
+      m = to;
+      return;
+    }
+    const float d = fminf((to - m) * kLog2e, -kFarBelow), f = exp2_approx(-d);
+    t = f * (t - d * s);
+    s *= f;
+    m = to;
+  }
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t w = __shfl_xor_sync(kFull, v, o);
+    v = w > v ? w : v;
+  }
+  return v;
+}
+
+// Adds the sums of `n` parts at `parts` (in order), relative to their largest
+// maximum.
+__device__ __forceinline__ Sums join(const Sums* parts, int n) {
+  float m = -INFINITY;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, parts[i].m);
+  Sums all{m, 0.0f, 0.0f};
+  for (int i = 0; i < n; ++i) {
+    Sums q = parts[i];
+    q.rebase(m);
+    all.s += q.s;
+    all.t += q.t;
+  }
+  return all;
+}
+
+// One warp: the `want` best of the n maxima in `best` (0 where taken), as
+// group numbers in order, into `sel`.  Lane l holds the maximum of the l-th
+// 32nd of the groups, so equal maxima go by the lowest group.
+__device__ __forceinline__ void select_groups(uint32_t* best, int n, int want, int lane, int* sel, uint32_t* last) {
+  const int span = ((n + 1023) / 1024) * 32;
+  uint32_t mine = 0;
+  for (int i = 0; i < span; ++i) {
+    const int g = lane * span + i;
+    if (g < n) mine = max(mine, best[g]);
+  }
+  for (int r = 0; r < want; ++r) {
+    const uint32_t top = __reduce_max_sync(kFull, mine);
+    const int owner = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+    bool found = false;
+    uint32_t rest = 0;
+    for (int i = 0; i < span; i += 32) {
+      const int g = owner * span + i + lane;
+      uint32_t v = g < n ? best[g] : 0u;
+      if (!found) {
+        const uint32_t hit = __ballot_sync(kFull, g < n && v == top);
+        if (hit != 0) {
+          found = true;
+          if (lane == __ffs(hit) - 1) {
+            best[g] = 0;
+            sel[r] = g;
+            v = 0;
+          }
+        }
+      }
+      rest = max(rest, __reduce_max_sync(kFull, v));
+    }
+    if (lane == owner) mine = rest;
+    if (r == want - 1 && lane == 0) *last = top;
+    __syncwarp();
+  }
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParams p, int split) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Sums s_warp[kWarpsLp];
+  __shared__ Sums s_cta;
+  __shared__ int s_sel[kMaxTop];
+  __shared__ uint32_t s_last;
+  __shared__ int s_count;
+  __shared__ uint64_t s_round[kWarpsLp];
+  dev::griddep_launch_dependents();
+  dev::griddep_wait();
+
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const int rank = split > 1 ? (int)dev::cluster_ctarank() : 0;
+  const int row_index = (int)blockIdx.x / split;
+  const Row<kType> row(p, row_index);
+  const int n = row.groups();
+  const int g0 = (int)((long long)n * rank / split), g1 = (int)((long long)n * (rank + 1) / split);
+  uint32_t* s_best = reinterpret_cast<uint32_t*>(smem);              // [n] the groups' maxima
+  uint64_t* s_cand = reinterpret_cast<uint64_t*>(smem + (((size_t)n * 4u + 15u) & ~(size_t)15u));
+
+  Sums a{-INFINITY, 0.0f, 0.0f};
+  for (int g = g0 + warp; g < g1; g += kWarpsLp) {
+    float f[8];
+    row.load_group(g, lane, f);
+    float m = f[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
+    m = warp_max(m);
+    if (lane == 0) s_best[g] = order_of(m);
+    if (m > a.m) a.rebase(m);
+    const float base = a.m == -INFINITY ? 0.0f : a.m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = max_nan((f[j] - base) * kLog2e, kFarBelow);
+      const float e = exp2_approx(d);
+      a.s += e;
+      a.t = fmaf(e, d, a.t);
+    }
+  }
+  a.s = warp_sum(a.s);
+  a.t = warp_sum(a.t);
+  if (lane == 0) s_warp[warp] = a;
+  if (threadIdx.x == 0) s_count = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) s_cta = join(s_warp, kWarpsLp);
+  if (split > 1) {
+    // the first CTA takes the others' sums and maxima from their shared memory
+    dev::cluster_arrive_release();
+    dev::cluster_wait_acquire();
+    if (rank == 0) {
+      if ((int)threadIdx.x < split && threadIdx.x > 0) {
+        const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), threadIdx.x);
+        s_warp[threadIdx.x] = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
+      }
+      if (threadIdx.x == 0) s_warp[0] = s_cta;
+      if (p.k > 0) {
+        for (int r = 1; r < split; ++r) {
+          const int lo = (int)((long long)n * r / split), hi = (int)((long long)n * (r + 1) / split);
+          for (int g = lo + (int)threadIdx.x; g < hi; g += kThreadsLp) {
+            s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
+          }
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) s_cta = join(s_warp, split);
+    }
+    dev::cluster_arrive_release();
+    dev::cluster_wait_acquire();
+    if (rank != 0) return;
+  }
+  __syncthreads();
+  const Sums all = s_cta;
+  // a row whose every logit is masked: no probabilities (log 0), entropy 0
+  const float log_s = all.s == 0.0f ? 0.0f : logf(all.s);
+  const float base = all.m == -INFINITY && all.s == 0.0f ? 0.0f : all.m;
+  if (threadIdx.x == 0) {
+    p.entropy[row_index] = all.s == 0.0f ? 0.0f : log_s - kLn2 * (all.t / all.s);
+    if (p.tokens != nullptr) {
+      const long long t = p.tokens[row_index];
+      p.logprob[row_index] =
+          t >= 0 && t < (long long)p.V ? (Logit<kType>::one(row.x[t]) - base) - log_s : __uint_as_float(0x7FC00000u);
+    }
+  }
+  if (p.k == 0) return;
+
+  const int want = min(p.k, n);
+  if (warp == 0) select_groups(s_best, n, want, lane, s_sel, &s_last);
+  __syncthreads();
+  // the chosen groups again: every logit that the last of them does not exclude
+  const uint32_t last = s_last;
+  const bool all_in = n <= p.k;            // fewer groups than alternatives: none excludes anything
+  for (int i = warp; i < want; i += kWarpsLp) {
+    float f[8];
+    row.load_group(s_sel[i], lane, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int id = Row<kType>::at(s_sel[i], lane, j) - row.shift;
+      const uint32_t o = order_of(f[j]);
+      if (id >= 0 && id < p.V && (all_in || o >= last)) {
+        s_cand[atomicAdd(&s_count, 1)] = ((uint64_t)o << 32) | (uint32_t)~id;
+      }
+    }
+  }
+  __syncthreads();
+  // Their order is by (logit, lowest index), each one's place in it the
+  // number before it, so how they came into the list does not matter.
+  const int count = s_count;
+  long long* ids = p.top_ids + (long long)row_index * p.k;
+  float* tops = p.top_logprobs + (long long)row_index * p.k;
+  if (count <= kFewCandidates) {
+    if ((int)threadIdx.x < count) {
+      const uint64_t c = s_cand[threadIdx.x];
+      int before = 0;
+      for (int i = 0; i < count; ++i) before += s_cand[i] > c ? 1 : 0;
+      if (before < p.k) {
+        ids[before] = (long long)(uint32_t)~(uint32_t)c;
+        tops[before] = (value_of((uint32_t)(c >> 32)) - base) - log_s;
+      }
+    }
+    return;
+  }
+  for (int r = 0; r < p.k; ++r) {           // many equal logits (a masked row): one at a time
+    uint64_t mine = 0;
+    for (int i = (int)threadIdx.x; i < count; i += kThreadsLp) mine = s_cand[i] > mine ? s_cand[i] : mine;
+    const uint64_t w = warp_max64(mine);
+    if (lane == 0) s_round[warp] = w;
+    __syncthreads();
+    uint64_t top = s_round[0];
+#pragma unroll
+    for (int i = 1; i < kWarpsLp; ++i) top = s_round[i] > top ? s_round[i] : top;
+    if (mine == top) {
+      for (int i = (int)threadIdx.x; i < count; i += kThreadsLp) {
+        if (s_cand[i] == top) s_cand[i] = 0;
+      }
+      ids[r] = (long long)(uint32_t)~(uint32_t)top;
+      tops[r] = (value_of((uint32_t)(top >> 32)) - base) - log_s;
+    }
+    __syncthreads();
+  }
+}
+
+// Shared memory: the groups' maxima (one more group than the row fills when
+// it starts inside a word) and the candidates of k groups.
+size_t logprob_smem(int V, int k) {
+  const size_t n = ((size_t)V + 7u + kGroup - 1u) / kGroup;
+  return ((n * 4u + 15u) & ~(size_t)15u) + (size_t)k * kGroup * sizeof(uint64_t);
+}
+
+template <int kType>
+cudaError_t launch_logprobs(const LogprobParams& p, int split, cudaStream_t stream) {
+  return launch_chained(logprobs_kernel<kType>, dim3((unsigned)p.rows * (unsigned)split), dim3(kThreadsLp),
+                        logprob_smem(p.V, p.k), (unsigned)split, stream, p, split);
+}
+
+inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
+
+}  // namespace
+
+cudaError_t prepare_logprobs() {
+  const int most = (int)logprob_smem(kMaxVocab, kMaxTop);
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(logprobs_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(logprobs_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+  return cudaFuncSetAttribute(logprobs_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
+}  // namespace splitk
+
+using namespace splitk;
+
+extern "C" {
+
+SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long stride, const long long* tokens,
+                               float* logprob, float* entropy, int top_k, long long* top_ids, float* top_logprobs,
+                               int M, int V, splitk_stream_t stream) {
+  if (!logits || !entropy || (tokens != nullptr) != (logprob != nullptr)) return SPLITK_ERR_NULL;
+  if (top_k > 0 && (!top_ids || !top_logprobs)) return SPLITK_ERR_NULL;
+  if (logits_type != SPLITK_DTYPE_BF16 && logits_type != SPLITK_DTYPE_F32 && logits_type != SPLITK_DTYPE_F16) {
+    return SPLITK_ERR_INVALID_ARGUMENT;
+  }
+  if (M < 1 || V < 1 || V > kMaxVocab || stride < V || M > (1 << 27)) return SPLITK_ERR_INVALID_SHAPE;
+  if (top_k < 0 || top_k > kMaxTop || top_k > V) return SPLITK_ERR_INVALID_ARGUMENT;
+  if (!aligned(logits, logits_type == SPLITK_DTYPE_F32 ? 4u : 2u) || !aligned(tokens, 8) || !aligned(logprob, 4) ||
+      !aligned(entropy, 4) || (top_k > 0 && (!aligned(top_ids, 8) || !aligned(top_logprobs, 4)))) {
+    return SPLITK_ERR_MISALIGNED;
+  }
+  DeviceSize dev;
+  int rc = require_device(&dev);
+  if (rc != SPLITK_OK) return rc;
+  const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
+  // CTAs sharing a row: as many as two CTAs an SM leave, with 16 groups (one
+  // a warp) for each at least.
+  int split = 1;
+  while (split < 8 && (long long)M * split * 2 <= 2ll * dev.num_sms && V / (split * 2) >= kGroup * kWarpsLp) split *= 2;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, s)
+                        : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, s)
+                                                          : launch_logprobs<3>(p, split, s);
+  return launched(e);
+}
+
+}  // extern "C"

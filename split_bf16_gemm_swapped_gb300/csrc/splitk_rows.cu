@@ -1,0 +1,353 @@
+// Activations to 8-bit codes, a row (token) at a time: splitk_rmsnorm_i8()
+// and splitk_quantize_i8().
+//
+//   y = x + r                                   (f32; r' = y in r's type)
+//   n = y * w / sqrt(mean(y^2) + eps)           (quantise alone: n = x)
+//   s = max(max|n| / 127, 2^-126);  q = rne(n / s)
+//
+// max|n| = max|y w| / rms, so one joint reduction of (sum y^2, max|y w|) over
+// the row gives both statistics, and the row's values z = y w stay in
+// registers between reading and coding: every byte is read and written once.
+// Sums and statistics are f32; the codes are rounded once, by adding
+// 1.5 * 2^23 in the multiplication that scales them (the sum's low byte is
+// then the two's complement code, rounded to nearest even).
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "splitk.h"
+#include "splitk_device.cuh"
+#include "splitk_internal.h"
+
+namespace splitk {
+
+namespace {
+
+constexpr float kMinScale = 1.17549435e-38f;   // 2^-126, the smallest normal f32
+constexpr float kMaxF32 = 3.40282347e38f;
+constexpr int kMaxRowThreads = 1024;
+constexpr int kVec = 8;                        // elements of one 16-byte load of bf16
+
+struct RowParams {
+  const uint16_t* x;        // bf16 [rows][x_stride]
+  long long x_stride;
+  const void* residual;     // bf16 or f32 [rows][width], or null
+  void* residual_out;
+  const void* weight;       // bf16 or f32 [width]
+  float eps;
+  int8_t* q;                // [rows][width]
+  float* scale;             // [rows]
+  int rows, width;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float bf16_one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// max that keeps a NaN of either operand (a row holding one must not come
+// out as finite codes).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// f32 rounded to the nearest whole number (|v * m| <= 127), in the low byte.
+__device__ __forceinline__ uint32_t code_of(float v, float m) { return __float_as_uint(fmaf(v, m, 12582912.0f)); }
+
+__device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return dev::prmt(dev::prmt(a, b, 0x0040u), dev::prmt(c, d, 0x0040u), 0x5410u);
+}
+
+// Eight consecutive elements from 16-byte aligned memory of type kType
+// (1 bf16, 2 f32).
+template <int kType>
+__device__ __forceinline__ void load8(const void* p, long long at, float (&v)[kVec]) {
+  if (kType == 1) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+template <int kType>
+__device__ __forceinline__ float load1(const void* p, long long at) {
+  return kType == 1 ? bf16_one(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+}
+
+template <int kType>
+__device__ __forceinline__ void store1(void* p, long long at, float v) {
+  if (kType == 1) {
+    static_cast<uint16_t*>(p)[at] = (uint16_t)(dev::pack_bf16x2(v, 0.0f) & 0xFFFFu);
+  } else {
+    static_cast<float*>(p)[at] = v;
+  }
+}
+
+// The row's sum and maximum, in every thread of the row.  A row is one warp
+// (blockDim.x = 32, blockDim.y rows a CTA) or the whole CTA.
+__device__ __forceinline__ void reduce_row(float& sum, float& amax) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  }
+  if (blockDim.x == 32) return;
+  __shared__ float s_sum[32], s_max[32];
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+  if (lane == 0) s_sum[warp] = sum, s_max[warp] = amax;
+  __syncthreads();
+  sum = lane < warps ? s_sum[lane] : 0.0f;
+  amax = lane < warps ? s_max[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  }
+}
+
+// The row's scale, and the factors from z = y w to codes: z * first * mult.
+// `first` is 1 unless the scale is so near its floor that one factor would
+// pass f32 (a row of zeros, say).  A row that holds a NaN or an infinity (or
+// whose sum of squares passes f32) has no codes: its scale is NaN, and so is
+// every product that uses it.
+__device__ __forceinline__ float row_scale(bool norm, float sum, float amax, int width, float eps, float* first,
+                                           float* mult) {
+  const float rinv = norm ? 1.0f / sqrtf(sum / (float)width + eps) : 1.0f;
+  float s = fmaxf(amax * rinv / 127.0f, kMinScale);
+  if (!(sum <= kMaxF32) || !(amax <= kMaxF32)) s = __uint_as_float(0x7FC00000u);
+  const float m = rinv / s;
+  *first = m > kMaxF32 ? rinv : 1.0f;
+  *mult = m > kMaxF32 ? 1.0f / s : m;
+  return s;
+}
+
+// kRes: 0 no residual, 1 bf16, 2 f32.  kW: 0 no norm (quantise alone), 1 bf16
+// weight, 2 f32 weight.  kVecs: 8-element vectors a thread holds.  kWide:
+// every row and the weight are read and written in 16-byte vectors; else one
+// element at a time, lane by lane.
+template <int kRes, int kW, int kVecs, bool kWide>
+__global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p) {
+  dev::griddep_launch_dependents();
+  dev::griddep_wait();
+  const int row = (int)(blockIdx.x * blockDim.y + threadIdx.y);
+  if (row >= p.rows) return;             // whole warps: blockDim.y > 1 only with one warp a row
+  const int tid = (int)threadIdx.x, step = (int)blockDim.x;
+  const uint16_t* x = p.x + (long long)row * p.x_stride;
+  const long long base = (long long)row * p.width;
+  float z[kVecs][kVec];
+  float sum = 0.0f, amax = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    if (kWide) {
+      const int e = (v * step + tid) * kVec;
+      if (e >= p.width) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) z[v][j] = 0.0f;
+        continue;
+      }
+      load8<1>(x, e, z[v]);
+      if (kRes != 0) {
+        float r[kVec];
+        load8<kRes == 0 ? 1 : kRes>(p.residual, base + e, r);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) z[v][j] += r[j];
+        if (kRes == 1) {
+          uint4 o;
+          o.x = dev::pack_bf16x2(z[v][0], z[v][1]), o.y = dev::pack_bf16x2(z[v][2], z[v][3]);
+          o.z = dev::pack_bf16x2(z[v][4], z[v][5]), o.w = dev::pack_bf16x2(z[v][6], z[v][7]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.residual_out) + base + e) = o;
+        } else {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.residual_out) + base + e);
+          o[0] = make_float4(z[v][0], z[v][1], z[v][2], z[v][3]);
+          o[1] = make_float4(z[v][4], z[v][5], z[v][6], z[v][7]);
+        }
+      }
+      if (kW != 0) {
+        float w[kVec];
+        load8<kW == 0 ? 1 : kW>(p.weight, e, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          sum = fmaf(z[v][j], z[v][j], sum);
+          z[v][j] *= w[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const int e = (v * kVec + j) * step + tid;
+        z[v][j] = 0.0f;
+        if (e >= p.width) continue;
+        float y = bf16_one(x[e]);
+        if (kRes != 0) {
+          y += load1<kRes == 0 ? 1 : kRes>(p.residual, base + e);
+          store1<kRes == 0 ? 1 : kRes>(p.residual_out, base + e, y);
+        }
+        if (kW != 0) {
+          sum = fmaf(y, y, sum);
+          y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
+        }
+        z[v][j] = y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) amax = max_nan(amax, fabsf(z[v][j]));
+  }
+  reduce_row(sum, amax);
+  float first, mult;
+  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
+  if (tid == 0) p.scale[row] = s;
+  if (first != 1.0f) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) z[v][j] *= first;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    if (kWide) {
+      const int e = (v * step + tid) * kVec;
+      if (e >= p.width) continue;
+      uint2 o;
+      o.x = pack_codes(code_of(z[v][0], mult), code_of(z[v][1], mult), code_of(z[v][2], mult), code_of(z[v][3], mult));
+      o.y = pack_codes(code_of(z[v][4], mult), code_of(z[v][5], mult), code_of(z[v][6], mult), code_of(z[v][7], mult));
+      *reinterpret_cast<uint2*>(p.q + base + e) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const int e = (v * kVec + j) * step + tid;
+        if (e < p.width) p.q[base + e] = (int8_t)(code_of(z[v][j], mult) & 0xFFu);
+      }
+    }
+  }
+}
+
+// Rows wider than a CTA's registers hold: the row is read twice, an element
+// at a time.  The first pass writes nothing, so the residual may be updated
+// in place: each thread's second pass reads an element before it writes it.
+template <int kRes, int kW>
+__global__ void __launch_bounds__(kMaxRowThreads) long_rows_kernel(const RowParams p) {
+  dev::griddep_launch_dependents();
+  dev::griddep_wait();
+  const int row = (int)blockIdx.x;
+  const uint16_t* x = p.x + (long long)row * p.x_stride;
+  const long long base = (long long)row * p.width;
+  float sum = 0.0f, amax = 0.0f;
+  for (int e = (int)threadIdx.x; e < p.width; e += (int)blockDim.x) {
+    float y = bf16_one(x[e]);
+    if (kRes != 0) y += load1<kRes == 0 ? 1 : kRes>(p.residual, base + e);
+    if (kW != 0) {
+      sum = fmaf(y, y, sum);
+      y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
+    }
+    amax = max_nan(amax, fabsf(y));
+  }
+  reduce_row(sum, amax);
+  float first, mult;
+  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
+  if (threadIdx.x == 0) p.scale[row] = s;
+  for (int e = (int)threadIdx.x; e < p.width; e += (int)blockDim.x) {
+    float y = bf16_one(x[e]);
+    if (kRes != 0) {
+      y += load1<kRes == 0 ? 1 : kRes>(p.residual, base + e);
+      store1<kRes == 0 ? 1 : kRes>(p.residual_out, base + e, y);
+    }
+    if (kW != 0) y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
+    p.q[base + e] = (int8_t)(code_of(y * first, mult) & 0xFFu);
+  }
+}
+
+template <int kRes, int kW, int kVecs>
+cudaError_t launch_vecs(const RowParams& p, bool wide, dim3 grid, dim3 block, cudaStream_t stream) {
+  return wide ? launch_chained(rows_kernel<kRes, kW, kVecs, true>, grid, block, 0, 1, stream, p)
+              : launch_chained(rows_kernel<kRes, kW, kVecs, false>, grid, block, 0, 1, stream, p);
+}
+
+template <int kRes, int kW>
+cudaError_t launch_rows(const RowParams& p, bool wide, cudaStream_t stream) {
+  const int vecs = (p.width + kVec - 1) / kVec;
+  if (vecs > 4 * kMaxRowThreads) {
+    return launch_chained(long_rows_kernel<kRes, kW>, dim3((unsigned)p.rows), dim3(kMaxRowThreads), 0, 1, stream, p);
+  }
+  if (vecs <= 4 * 32) {                  // a warp a row, four rows a CTA
+    const dim3 block(32, 4), grid((unsigned)((p.rows + 3) / 4));
+    if (vecs <= 32) return launch_vecs<kRes, kW, 1>(p, wide, grid, block, stream);
+    if (vecs <= 64) return launch_vecs<kRes, kW, 2>(p, wide, grid, block, stream);
+    return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
+  }
+  const dim3 grid((unsigned)p.rows);
+  const dim3 block((unsigned)(((vecs + 3) / 4 + 31) & ~31));
+  return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
+}
+
+template <int kRes>
+cudaError_t launch_weight(const RowParams& p, int weight_type, bool wide, cudaStream_t stream) {
+  if (weight_type == SPLITK_DTYPE_F32) return launch_rows<kRes, 2>(p, wide, stream);
+  return launch_rows<kRes, 1>(p, wide, stream);
+}
+
+inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
+
+// The checks both entry points share.
+int check_rows(const void* x, long long x_stride, const void* q, const float* scale, int M, int D) {
+  if (!x || !q || !scale) return SPLITK_ERR_NULL;
+  if (M < 1 || D < 1 || x_stride < D || D > (1 << 30)) return SPLITK_ERR_INVALID_SHAPE;
+  if (!aligned(x, 2) || !aligned(scale, 4)) return SPLITK_ERR_MISALIGNED;
+  return SPLITK_OK;
+}
+
+}  // namespace
+
+}  // namespace splitk
+
+using namespace splitk;
+
+extern "C" {
+
+SPLITK_API int splitk_rmsnorm_i8(const void* x, long long x_stride, const void* residual, void* residual_out,
+                                 int residual_type, const void* weight, int weight_type, float eps, void* q,
+                                 float* scale, int M, int D, splitk_stream_t stream) {
+  int rc = check_rows(x, x_stride, q, scale, M, D);
+  if (rc != SPLITK_OK) return rc;
+  if (!weight || (residual != nullptr) != (residual_out != nullptr)) return SPLITK_ERR_NULL;
+  if (!(eps > 0.0f) || !(eps <= 3.4e38f)) return SPLITK_ERR_INVALID_ARGUMENT;
+  if (weight_type != SPLITK_DTYPE_BF16 && weight_type != SPLITK_DTYPE_F32) return SPLITK_ERR_INVALID_ARGUMENT;
+  if (residual && residual_type != SPLITK_DTYPE_BF16 && residual_type != SPLITK_DTYPE_F32) {
+    return SPLITK_ERR_INVALID_ARGUMENT;
+  }
+  const uintptr_t r_size = residual_type == SPLITK_DTYPE_F32 ? 4u : 2u;
+  const uintptr_t w_size = weight_type == SPLITK_DTYPE_F32 ? 4u : 2u;
+  if (!aligned(weight, w_size)) return SPLITK_ERR_MISALIGNED;
+  if (residual && (!aligned(residual, r_size) || !aligned(residual_out, r_size))) return SPLITK_ERR_MISALIGNED;
+  rc = require_device(nullptr);
+  if (rc != SPLITK_OK) return rc;
+  const RowParams p{static_cast<const uint16_t*>(x), x_stride, residual, residual_out, weight, eps,
+                    static_cast<int8_t*>(q), scale, M, D};
+  const bool wide = D % kVec == 0 && x_stride % kVec == 0 && aligned(x, 16) && aligned(weight, 16) && aligned(q, 8) &&
+                    aligned(residual, 16) && aligned(residual_out, 16);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = !residual                               ? launch_weight<0>(p, weight_type, wide, s)
+                        : residual_type == SPLITK_DTYPE_F32 ? launch_weight<2>(p, weight_type, wide, s)
+                                                                : launch_weight<1>(p, weight_type, wide, s);
+  return launched(e);
+}
+
+SPLITK_API int splitk_quantize_i8(const void* x, long long x_stride, void* q, float* scale, int M, int D,
+                                  splitk_stream_t stream) {
+  int rc = check_rows(x, x_stride, q, scale, M, D);
+  if (rc != SPLITK_OK) return rc;
+  rc = require_device(nullptr);
+  if (rc != SPLITK_OK) return rc;
+  const RowParams p{static_cast<const uint16_t*>(x), x_stride, nullptr, nullptr, nullptr, 0.0f,
+                    static_cast<int8_t*>(q), scale, M, D};
+  const bool wide = D % kVec == 0 && x_stride % kVec == 0 && aligned(x, 16) && aligned(q, 8);
+  return launched(launch_rows<0, 0>(p, wide, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
