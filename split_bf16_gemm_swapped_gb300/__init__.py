@@ -539,187 +539,6 @@ def splitk_gemm_bf16_zerocopy(a, b_host, c_host, split_k: int = 0, stream=None):
     return c_host
 
 
-# ---------------------------------------------------------------- 8-bit codes, log probabilities
-DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
-
-
-def _dtype_code(t, name, *allowed):
-    """The library's code of t's type, one of `allowed` (torch type names)."""
-    kind = str(t.dtype)[6:]
-    if kind not in allowed:
-        raise TypeError(f"{name} must be {' or '.join(allowed)}, not {kind}")
-    return {"bfloat16": DTYPE_BF16, "float32": DTYPE_F32, "float16": DTYPE_F16}[kind]
-
-
-def _same_device(device, **ts):
-    """Every tensor given is a CUDA tensor on `device`."""
-    for name, t in ts.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, the operands' device")
-    if device.type != "cuda":
-        raise ValueError("operands must be CUDA tensors")
-
-
-def _given(t, name, shape, dtype, device):
-    """t if it is a contiguous tensor of this shape and type, or a new one."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    _same_device(device, **{name: t})
-    return t
-
-
-def _rows(t, name):
-    """(rows, width, row stride) of a tensor read as rows along its last
-    dimension: [M, D] with contiguous rows any distance apart, or a contiguous
-    [L, M, D]."""
-    if t.dim() not in (2, 3) or (t.dim() == 3 and not t.is_contiguous()) or t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} is [M, D] with contiguous rows, or a contiguous [L, M, D]")
-    width = t.shape[-1]
-    if t.dim() == 3:
-        return t.shape[0] * t.shape[1], width, width
-    rows = t.shape[0]
-    return rows, width, (t.stride(0) if rows > 1 else width)
-
-
-def _call(fn, device, stream, where, *args):
-    """One library call on `device` (made current) and `stream` (the current
-    one when None)."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
-    _check(rc, where)
-
-
-def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=None, residual_out=None,
-                      stream=None):
-    """Residual addition, RMS norm and 8-bit codes with a scale per row:
-    y = x + residual, n = y * weight / sqrt(mean(y^2) + eps), codes
-    q = round(n / scale) with scale = max|n| / 127.
-
-    x [M, D] (rows any distance apart) or contiguous [L, M, D], bfloat16;
-    residual contiguous of x's shape, bfloat16 or float32; weight [D],
-    bfloat16 or float32.  Returns (q int8, scale float32 [M] or [L, M],
-    residual_out): the sum y in the residual's type, None without a residual.
-    residual_out may be the residual itself (updated in place)."""
-    import torch
-    M, D, stride = _rows(x, "x")
-    _dtype_code(x, "x", "bfloat16")
-    w_code = _dtype_code(weight, "weight", "bfloat16", "float32")
-    if tuple(weight.shape) != (D,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous tensor of shape ({D},)")
-    device, shape = x.device, tuple(x.shape)
-    _same_device(device, weight=weight, residual=residual)
-    r_code, r_in, r_out = DTYPE_BF16, None, None
-    if residual is not None:
-        r_code = _dtype_code(residual, "residual", "bfloat16", "float32")
-        r_in = _given(residual, "residual", shape, residual.dtype, device).data_ptr()
-        residual_out = _given(residual_out, "residual_out", shape, residual.dtype, device)
-        r_out = residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    q = _given(q, "q", shape, torch.int8, device)
-    scale = _given(scale, "scale", shape[:-1], torch.float32, device)
-    _call(load_library().splitk_rmsnorm_i8, device, stream, "splitk_rmsnorm_i8",
-          x.data_ptr(), stride, r_in, r_out, r_code, weight.data_ptr(), w_code, eps, q.data_ptr(),
-          scale.data_ptr(), M, D)
-    return q, scale, residual_out
-
-
-def splitk_quantize_i8(x, q=None, scale=None, stream=None):
-    """8-bit codes with a scale per row, scale = max|x| / 127: activations
-    (a row is a token) or weights (a row is a channel).  x as in
-    splitk_rmsnorm_i8; returns (q int8, scale float32)."""
-    import torch
-    M, D, stride = _rows(x, "x")
-    _dtype_code(x, "x", "bfloat16")
-    device, shape = x.device, tuple(x.shape)
-    _same_device(device)
-    q = _given(q, "q", shape, torch.int8, device)
-    scale = _given(scale, "scale", shape[:-1], torch.float32, device)
-    _call(load_library().splitk_quantize_i8, device, stream, "splitk_quantize_i8",
-          x.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), M, D)
-    return q, scale
-
-
-def splitk_gemm_i8(a_q, a_scale, b_q, b_scale, c=None, bias=None, out_dtype=None, stream=None):
-    """c = (b_q @ a_q^T) * b_scale * a_scale + bias: 8-bit codes with a scale
-    per channel (a_scale [L, N] or [N]) and per token (b_scale [L, M] or [M]).
-
-    a_q [L, N, K] or [N, K] and b_q [L, M, K] or [M, K] int8, contiguous, K a
-    multiple of 16; bias [L, N] or [N] bfloat16.  Returns c [L, M, N] or
-    [M, N]: bfloat16, or float32 where out_dtype or the c given says so."""
-    import torch
-    if a_q.dtype != torch.int8 or b_q.dtype != torch.int8:
-        raise TypeError("a_q and b_q must be int8")
-    if a_scale.dtype != torch.float32 or b_scale.dtype != torch.float32:
-        raise TypeError("a_scale and b_scale must be float32")
-    if a_q.dim() not in (2, 3) or b_q.dim() != a_q.dim():
-        raise ValueError("a_q is [L, N, K] or [N, K]; b_q is [L, M, K] or [M, K]")
-    batch = tuple(a_q.shape[:-2])
-    (N, K), (M, Kb) = a_q.shape[-2:], b_q.shape[-2:]
-    if K != Kb or tuple(b_q.shape[:-2]) != batch or tuple(a_scale.shape) != (*batch, N) or \
-            tuple(b_scale.shape) != (*batch, M):
-        raise ValueError(f"shape mismatch: a_q{tuple(a_q.shape)} a_scale{tuple(a_scale.shape)} "
-                         f"b_q{tuple(b_q.shape)} b_scale{tuple(b_scale.shape)}")
-    if not (a_q.is_contiguous() and a_scale.is_contiguous() and b_q.is_contiguous() and b_scale.is_contiguous()):
-        raise ValueError("operands must be contiguous")
-    device = a_q.device
-    _same_device(device, a_scale=a_scale, b_q=b_q, b_scale=b_scale, bias=bias)
-    if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (*batch, N) or
-                             not bias.is_contiguous()):
-        raise ValueError(f"bias must be a contiguous bfloat16 tensor of shape {(*batch, N)}")
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if c is None else c.dtype
-    c = _given(c, "c", (*batch, M, N), out_dtype, device)
-    c_code = _dtype_code(c, "c", "bfloat16", "float32")
-    _call(load_library().splitk_gemm_i8, device, stream, "splitk_gemm_i8",
-          a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(),
-          None if bias is None else bias.data_ptr(), c.data_ptr(), c_code, M, N, K, batch[0] if batch else 1)
-    return c
-
-
-def splitk_logprobs(logits, tokens=None, top_k: int = 0, logprob=None, entropy=None, top_ids=None,
-                    top_logprobs=None, stream=None):
-    """Log probabilities of the given tokens, the entropy of each row and its
-    top_k most probable tokens (0..32; equal logits by the lowest index).
-
-    logits [M, V] (rows any distance apart) or contiguous [L, M, V], bfloat16,
-    float16 or float32; tokens int64 [M] or [L, M], contiguous.  Returns
-    (logprob, entropy, top_ids int64 [..., top_k], top_logprobs), float32 but
-    the ids; logprob is None without tokens, the alternatives with top_k = 0."""
-    import torch
-    M, V, stride = _rows(logits, "logits")
-    code = _dtype_code(logits, "logits", "bfloat16", "float16", "float32")
-    device, shape = logits.device, tuple(logits.shape[:-1])
-    _same_device(device, tokens=tokens)
-    t_ptr = l_ptr = i_ptr = p_ptr = None
-    if tokens is not None:
-        if tokens.dtype != torch.int64 or tuple(tokens.shape) != shape or not tokens.is_contiguous():
-            raise ValueError(f"tokens must be a contiguous int64 tensor of shape {shape}")
-        logprob = _given(logprob, "logprob", shape, torch.float32, device)
-        t_ptr, l_ptr = tokens.data_ptr(), logprob.data_ptr()
-    elif logprob is not None:
-        raise ValueError("logprob needs tokens")
-    entropy = _given(entropy, "entropy", shape, torch.float32, device)
-    if top_k:
-        top_ids = _given(top_ids, "top_ids", (*shape, top_k), torch.int64, device)
-        top_logprobs = _given(top_logprobs, "top_logprobs", (*shape, top_k), torch.float32, device)
-        i_ptr, p_ptr = top_ids.data_ptr(), top_logprobs.data_ptr()
-    elif top_ids is not None or top_logprobs is not None:
-        raise ValueError("the alternatives' outputs need top_k > 0")
-    _call(load_library().splitk_logprobs, device, stream, "splitk_logprobs",
-          logits.data_ptr(), code, stride, t_ptr, l_ptr, entropy.data_ptr(), top_k, i_ptr, p_ptr, M, V)
-    return logprob, entropy, top_ids, top_logprobs
-
-
 # ---------------------------------------------------------------- status
 def splitk_get_fault() -> dict:
     f = Fault()
@@ -777,3 +596,16 @@ def splitk_strerror(code: int) -> str:
 
 def splitk_version() -> int:
     return int(load_library().splitk_version())
+
+
+# ---------------------------------------------------------------- 8-bit codes, log probabilities
+_OPERATORS = ("splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs")
+
+
+def __getattr__(name):
+    """The operators around the projection, loaded (with PyTorch) on first use."""
+    if name in _OPERATORS:
+        from . import operators
+        globals().update({n: getattr(operators, n) for n in _OPERATORS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -29,7 +29,8 @@ ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 # Translation units of the CUDA library; compiled in parallel, linked once.
 SPLITK_SOURCES = ["splitk_kernel.cu", "splitk_persistent.cu", "splitk_copy.cu", "splitk_host.cu",
-                  "splitk_rows.cu", "splitk_i8_stream.cu", "splitk_logprobs.cu"]
+                  "splitk_rows.cu", "splitk_i8.cu", "splitk_i8_stream.cu", "splitk_i8_tile.cu",
+                  "splitk_logprobs.cu"]
 SPLITK_HEADERS = ["splitk_device.cuh", "splitk_internal.h", "splitk_kernel_common.cuh", "splitk_i8.cuh"]
 
 

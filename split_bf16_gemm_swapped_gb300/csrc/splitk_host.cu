@@ -852,7 +852,7 @@ int current_device(DeviceState** out, int* dev_out) {
     if (major != 10 || minor != 3) return SPLITK_ERR_UNSUPPORTED_DEVICE;
     if (!encode_fn()) return SPLITK_ERR_CUDA;
     if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess ||
-        prepare_logprobs() != cudaSuccess) {
+        prepare_logprobs() != cudaSuccess || prepare_i8_tile(optin) != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
@@ -1215,6 +1215,20 @@ int require_device(DeviceSize* out) {
   return rc;
 }
 
+bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)L};
+  cuuint64_t strides[2] = {(cuuint64_t)K, (cuuint64_t)K * (cuuint64_t)rows};
+  cuuint32_t box[3] = {(cuuint32_t)kCtaK, (cuuint32_t)box_rows, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+
 }  // namespace splitk
 
 using namespace splitk;
@@ -1572,12 +1586,14 @@ SPLITK_API int splitk_get_fault(splitk_fault_t* out) {
       cudaGetLastError();
       return SPLITK_ERR_UNSUPPORTED_DEVICE;
     }
-    int words_p[kFaultWords] = {0};
-    if (read_and_clear_fault(words) != cudaSuccess || read_and_clear_fault_persistent(words_p) != cudaSuccess) {
+    int words_p[kFaultWords] = {0}, words_i[kFaultWords] = {0};
+    if (read_and_clear_fault(words) != cudaSuccess || read_and_clear_fault_persistent(words_p) != cudaSuccess ||
+        read_and_clear_fault_i8(words_i) != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
     if (words[0] == 0) std::memcpy(words, words_p, sizeof(words));
+    if (words[0] == 0) std::memcpy(words, words_i, sizeof(words));
   }
   if (out) {
     out->code = words[0];

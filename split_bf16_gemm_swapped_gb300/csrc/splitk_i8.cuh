@@ -8,6 +8,7 @@
 // f32 additions are.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "splitk_device.cuh"
@@ -43,6 +44,17 @@ struct I8Params {
   bool c_f32;
   int M, N, K, L;
 };
+
+// How a product runs: `tokens` token columns a CTA; the tile kernel's cluster
+// size and ring depth.
+struct I8Plan {
+  bool tile;                // tcgen05 (splitk_i8_tile.cu), else streamed (splitk_i8_stream.cu)
+  int tokens;
+  int split;
+  int stages;
+};
+cudaError_t launch_i8_stream(const I8Params& p, const I8Plan& plan, cudaStream_t stream);
+cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, unsigned long long wait_limit_ns, cudaStream_t stream);
 
 // The sum `v` of output (l, m, n) with its scales and bias, stored: one
 // rounding, from f32.

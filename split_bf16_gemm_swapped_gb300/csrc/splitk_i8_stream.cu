@@ -107,35 +107,14 @@ cudaError_t launch_stream(const I8Params& p, cudaStream_t stream) {
   return launch_chained(i8_stream_kernel<kTok>, grid, dim3(32 * kWarps), 0, 1, stream, p);
 }
 
-inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
-
 }  // namespace
 
-}  // namespace splitk
-
-using namespace splitk;
-
-extern "C" {
-
-SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void* b_q, const float* b_scale,
-                              const void* bias, void* c, int c_type, int M, int N, int K, int L,
-                              splitk_stream_t stream) {
-  if (!a_q || !a_scale || !b_q || !b_scale || !c) return SPLITK_ERR_NULL;
-  if (c_type != SPLITK_DTYPE_BF16 && c_type != SPLITK_DTYPE_F32) return SPLITK_ERR_INVALID_ARGUMENT;
-  if (M < 1 || N < 1 || K < 1 || L < 1 || K % 16 != 0 || L > 65535 || N > 65535 * 128 || M > 65535 * 32 ||
-      K > (1 << 30)) {
-    return SPLITK_ERR_INVALID_SHAPE;
+cudaError_t launch_i8_stream(const I8Params& p, const I8Plan& plan, cudaStream_t stream) {
+  switch (plan.tokens) {
+    case 8: return launch_stream<8>(p, stream);
+    case 16: return launch_stream<16>(p, stream);
+    default: return launch_stream<32>(p, stream);
   }
-  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(bias, 2) ||
-      !aligned(c, c_type == SPLITK_DTYPE_F32 ? 4u : 2u)) {
-    return SPLITK_ERR_MISALIGNED;
-  }
-  int rc = require_device(nullptr);
-  if (rc != SPLITK_OK) return rc;
-  const I8Params p{static_cast<const int8_t*>(a_q), static_cast<const int8_t*>(b_q), a_scale, b_scale,
-                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L};
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return launched(M <= 8 ? launch_stream<8>(p, s) : M <= 16 ? launch_stream<16>(p, s) : launch_stream<32>(p, s));
 }
 
-}  // extern "C"
+}  // namespace splitk

@@ -173,8 +173,18 @@ struct DeviceSize {
 };
 int require_device(DeviceSize* out);
 
+// Defined in splitk_host.cu: a map of [L][rows][K] bytes read in boxes of 128
+// bytes of K by `box_rows` rows, 128-byte swizzle, zeros past the ends; and
+// the bound on a kernel's waits.
+bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows);
+unsigned long long wait_limit_ns();
+
 // Defined in splitk_logprobs.cu.
 cudaError_t prepare_logprobs();
+
+// Defined in splitk_i8_tile.cu.
+cudaError_t prepare_i8_tile(int max_dynamic_smem);
+cudaError_t read_and_clear_fault_i8(int* out_words);
 
 // The status of a launch, with CUDA's own error record cleared.
 inline int launched(cudaError_t e) {
