@@ -128,6 +128,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   return v;
 }
 
+__device__ __forceinline__ void ld_cluster_f32x4(uint32_t cluster_addr, float (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(cluster_addr)
+               : "memory");
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
   return __uint_as_float(ld_cluster_u32(cluster_addr));
 }

@@ -822,6 +822,7 @@ struct DeviceState {
   int used = 0;
   std::unordered_map<AKey, int, AKeyHash> a_slots;
   std::unordered_map<BKey, CUtensorMap, BKeyHash> b_maps;
+  int i8_clusters[3] = {};         // see DeviceSize
   int max_clusters[9] = {};        // persistent kernel: clusters of 2, 4, 8 resident at once (0: unknown)
 };
 
@@ -852,7 +853,7 @@ int current_device(DeviceState** out, int* dev_out) {
     if (major != 10 || minor != 3) return SPLITK_ERR_UNSUPPORTED_DEVICE;
     if (!encode_fn()) return SPLITK_ERR_CUDA;
     if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess ||
-        prepare_logprobs() != cudaSuccess || prepare_i8_tile(optin) != cudaSuccess) {
+        prepare_logprobs() != cudaSuccess || prepare_i8_tile(optin, st.i8_clusters) != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
@@ -1211,7 +1212,10 @@ int require_device(DeviceSize* out) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   const int rc = current_device(&st, nullptr);
-  if (rc == SPLITK_OK && out) *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin};
+  if (rc == SPLITK_OK && out) {
+    *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin,
+                      {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2]}};
+  }
   return rc;
 }
 

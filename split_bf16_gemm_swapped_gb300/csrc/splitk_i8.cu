@@ -15,17 +15,49 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
 
-// Few tokens stream through registers; from 33 on the tensor core's rate for
-// f16 (mma.sync: 604 TFLOP/s measured) would bound the stream.  Tiles of up to
-// 128 tokens; K is split while that gives more SMs a tile, two K tiles a rank
-// at least.
-I8Plan plan_i8(int M, int N, int K, int L, const DeviceSize& dev) {
-  if (M <= 32) return I8Plan{false, M <= 8 ? 8 : M <= 16 ? 16 : 32, 1, 0};
-  I8Plan pl{true, M <= 64 ? 64 : 128, 1, 4};
-  const long long tiles = (long long)((M + pl.tokens - 1) / pl.tokens) * ((N + 127) / 128) * L;
+// What a launch of `tiles` tiles costs, in microseconds: rounds of as many
+// clusters as the device holds at once, each a CTA's K tiles and a fixed share
+// (set-up, first loads, epilogue; more when ranks exchange sums).  Measured on
+// GB300: a K tile of 256 tokens 0.53 (the MMAs), of up to 128 0.36 (shared
+// memory, conversion, and memory with all SMs at it); fixed 10.5 and 4.6, with a
+// split 3 more.
+double tile_us(long long tiles, int tokens, int k_tiles, int split, const int (&clusters)[3]) {
+  const int fit = clusters[split == 1 ? 0 : split == 2 ? 1 : 2];
+  if (tiles == 0) return 0.0;
+  if (fit <= 0 || split > k_tiles) return 1e30;
+  const double rounds = (double)((tiles + fit - 1) / fit);
+  const double each = (tokens == 256 ? 0.53 : 0.36) * ((k_tiles + split - 1) / split);
+  return rounds * (each + (tokens == 256 ? 10.5 : 4.6) + (split > 1 ? 3.0 : 0.0));
+}
+
+// The tile plan with the least estimated time: all tiles on `split` pairs, or
+// as many full rounds of whole tiles as there are and the rest split.
+double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out) {
   const int k_tiles = (K + 127) / 128;
-  while (pl.split < 8 && tiles * pl.split * 2 <= dev.num_sms && k_tiles / (pl.split * 2) >= 2) pl.split *= 2;
-  return pl;
+  double best = 1e30;
+  for (int tokens : {32, 64, 128, 256}) {
+    if (tokens < 256 && tokens < M && tokens < 128) continue;       // the smallest that holds M, or 128 or 256
+    if (tokens > 32 && tokens / 2 >= M) continue;
+    const long long tiles = (long long)((M + tokens - 1) / tokens) * ((N + 255) / 256) * L;
+    const long long fit = dev.i8_clusters[0];
+    const long long rounds = fit > 0 ? tiles / fit : 0;
+    for (int split : {1, 2, 4}) {
+      const double all = tile_us(tiles, tokens, k_tiles, split, dev.i8_clusters);
+      if (all < best) best = all, *out = I8Plan{tokens, 0, split};
+      const double rest = tile_us(rounds * fit, tokens, k_tiles, 1, dev.i8_clusters) +
+                          tile_us(tiles - rounds * fit, tokens, k_tiles, split, dev.i8_clusters);
+      if (split > 1 && rounds > 0 && rest < best) best = rest, *out = I8Plan{tokens, rounds * fit, split};
+    }
+  }
+  return best;
+}
+
+// Up to 16 tokens the weights stream through registers (no tile is filled that
+// far); up to 32 where that is estimated faster: its rate there is what the
+// legacy tensor path's conversions leave, 2.6 TB/s measured.
+bool streams(int M, int N, int K, int L, double tile_time) {
+  if (M <= 16) return true;
+  return M <= 32 && 2.0 + (double)N * K * L / 2.6e6 < tile_time;
 }
 
 }  // namespace
@@ -41,10 +73,11 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
                               splitk_stream_t stream) {
   if (!a_q || !a_scale || !b_q || !b_scale || !c) return SPLITK_ERR_NULL;
   if (c_type != SPLITK_DTYPE_BF16 && c_type != SPLITK_DTYPE_F32) return SPLITK_ERR_INVALID_ARGUMENT;
-  if (M < 1 || N < 1 || K < 1 || L < 1 || K % 16 != 0 || L > 65535 || N > 65535 * 16 || M > 65535 * 32 ||
-      K > (1 << 30)) {
+  if (M < 1 || N < 1 || K < 1 || L < 1 || K % 16 != 0 || L > 65535 || N > 65535 * 128 || K > (1 << 30)) {
     return SPLITK_ERR_INVALID_SHAPE;
   }
+  // tiles of 128 tokens by 256 weight rows, eight CTAs each at most
+  if (((long long)M + 127) / 128 * ((N + 255) / 256) * L > (1ll << 27)) return SPLITK_ERR_INVALID_SHAPE;
   if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(bias, 2) ||
       !aligned(c, c_type == SPLITK_DTYPE_F32 ? 4u : 2u)) {
     return SPLITK_ERR_MISALIGNED;
@@ -54,9 +87,10 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   if (rc != SPLITK_OK) return rc;
   const I8Params p{static_cast<const int8_t*>(a_q), static_cast<const int8_t*>(b_q), a_scale, b_scale,
                    static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L};
-  const I8Plan plan = plan_i8(M, N, K, L, dev);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return launched(plan.tile ? launch_i8_tile(p, plan, wait_limit_ns(), s) : launch_i8_stream(p, plan, s));
+  I8Plan plan{};
+  const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
+  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, s) : launch_i8_tile(p, plan, wait_limit_ns(), s));
 }
 
 }  // extern "C"

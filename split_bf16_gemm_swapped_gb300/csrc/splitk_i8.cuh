@@ -45,27 +45,43 @@ struct I8Params {
   int M, N, K, L;
 };
 
-// How a product runs: `tokens` token columns a CTA; the tile kernel's cluster
-// size and ring depth.
+// How the tcgen05 kernel runs: tiles of 256 weight rows by `tokens`, counted
+// tokens first, then rows, then batches; the first `whole` of them on one pair
+// of CTAs each, the others on `split` pairs that share K.
 struct I8Plan {
-  bool tile;                // tcgen05 (splitk_i8_tile.cu), else streamed (splitk_i8_stream.cu)
   int tokens;
+  long long whole;
   int split;
-  int stages;
 };
-cudaError_t launch_i8_stream(const I8Params& p, const I8Plan& plan, cudaStream_t stream);
+cudaError_t launch_i8_stream(const I8Params& p, cudaStream_t stream);
 cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, unsigned long long wait_limit_ns, cudaStream_t stream);
 
-// The sum `v` of output (l, m, n) with its scales and bias, stored: one
-// rounding, from f32.
-__device__ __forceinline__ void store_i8_result(const I8Params& p, int l, int m, int n, float v) {
-  v = v * p.b_scale[(long long)l * p.M + m] * p.a_scale[(long long)l * p.N + n];
-  if (p.bias != nullptr) v += __uint_as_float((uint32_t)p.bias[(long long)l * p.N + n] << 16);
+// What one weight row's outputs share; loaded once, before the first store
+// (which the compiler must take to alias it).
+struct I8Channel {
+  float scale, bias;
+  bool has_bias;
+  __device__ __forceinline__ I8Channel(const I8Params& p, int l, int n) : has_bias(p.bias != nullptr) {
+    const long long at = (long long)l * p.N + n;
+    scale = n < p.N ? p.a_scale[at] : 0.0f;
+    bias = n < p.N && has_bias ? __uint_as_float((uint32_t)p.bias[at] << 16) : 0.0f;
+  }
+  // the output of the sum `v`, in f32
+  __device__ __forceinline__ float result(float v, float token_scale) const {
+    v = v * token_scale * scale;
+    return has_bias ? v + bias : v;
+  }
+};
+
+// Output (l, m, n) from its sum `v`: one rounding, from f32.
+__device__ __forceinline__ void store_i8_result(const I8Params& p, int l, int m, int n, float v, float token_scale,
+                                                const I8Channel& channel) {
+  const float r = channel.result(v, token_scale);
   const long long at = ((long long)l * p.M + m) * p.N + n;
   if (p.c_f32) {
-    static_cast<float*>(p.c)[at] = v;
+    static_cast<float*>(p.c)[at] = r;
   } else {
-    static_cast<uint16_t*>(p.c)[at] = (uint16_t)(dev::pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    static_cast<uint16_t*>(p.c)[at] = (uint16_t)dev::pack_bf16x2(r, 0.0f);
   }
 }
 

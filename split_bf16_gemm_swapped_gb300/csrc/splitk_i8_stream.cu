@@ -27,6 +27,7 @@ namespace {
 constexpr int kRows = 16;            // weight rows a CTA
 constexpr int kWarps = 8;
 constexpr int kChunk = 64;           // codes of K a warp takes at a time
+constexpr int kAhead = 2;            // chunks whose loads a warp has in flight at once
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -36,17 +37,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The 16 codes at `row` + k, or zeros past the row's end (K is a multiple of
-// 16) or for a row that does not exist.
-__device__ __forceinline__ uint4 load16(const int8_t* row, int k, int K, bool there) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (there && k < K) v = *reinterpret_cast<const uint4*>(row + k);
-  return v;
-}
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
 // kTok: token columns of a CTA (8, 16 or 32).
 template <int kTok>
-__global__ void __launch_bounds__(32 * kWarps) i8_stream_kernel(const I8Params p) {
+__global__ void __launch_bounds__(32 * kWarps, 1) i8_stream_kernel(const I8Params p) {
   constexpr int kTiles = kTok / 8;
   __shared__ float s_part[kWarps][kRows][kTok + 1];
   dev::griddep_launch_dependents();
@@ -54,32 +49,50 @@ __global__ void __launch_bounds__(32 * kWarps) i8_stream_kernel(const I8Params p
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = (int)blockIdx.x * kRows, m0 = (int)blockIdx.y * kTok, l = (int)blockIdx.z;
-  const int8_t* a = p.a + ((long long)l * p.N + n0) * p.K;
-  const int8_t* b = p.b + ((long long)l * p.M + m0) * p.K;
+  // Rows and tokens past the end read the last one instead (their sums are not
+  // stored), and the last chunk's lanes past K read in front of it and count
+  // as zeros: no load hangs on a branch.
+  const int8_t* a[2];
+  const int8_t* b[kTiles];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) a[r] = p.a + ((long long)l * p.N + min(n0 + 8 * r + g, p.N - 1)) * p.K;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) b[i] = p.b + ((long long)l * p.M + min(m0 + 8 * i + g, p.M - 1)) * p.K;
 
   float acc[kTiles][4];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
 
-  const bool a_lo = n0 + g < p.N, a_hi = n0 + g + 8 < p.N;
-  for (int k0 = warp * kChunk; k0 < p.K; k0 += kWarps * kChunk) {
-    const int k = k0 + 16 * t;
-    const uint4 wa = load16(a + (long long)g * p.K, k, p.K, a_lo);
-    const uint4 wb = load16(a + (long long)(g + 8) * p.K, k, p.K, a_hi);
-    uint4 x[kTiles];
+  for (int k0 = warp * kChunk; k0 < p.K; k0 += kAhead * kWarps * kChunk) {
+    uint4 w[kAhead][2], x[kAhead][kTiles];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) x[i] = load16(b + (long long)(8 * i + g) * p.K, k, p.K, m0 + 8 * i + g < p.M);
-    const uint32_t la[4] = {wa.x, wa.y, wa.z, wa.w}, lb[4] = {wb.x, wb.y, wb.z, wb.w};
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = min(k0 + u * kWarps * kChunk + 16 * t, p.K - 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t f[4];
-      dev::i8x4_to_f16(la[j], f[0], f[2]);
-      dev::i8x4_to_f16(lb[j], f[1], f[3]);
+      for (int r = 0; r < 2; ++r) w[u][r] = *reinterpret_cast<const uint4*>(a[r] + at);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        uint32_t b0, b1;
-        dev::i8x4_to_f16(j == 0 ? x[i].x : j == 1 ? x[i].y : j == 2 ? x[i].z : x[i].w, b0, b1);
-        mma_f16(acc[i], f, b0, b1);
+      for (int i = 0; i < kTiles; ++i) x[u][i] = *reinterpret_cast<const uint4*>(b[i] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k0 + u * kWarps * kChunk + 16 * t >= p.K) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) x[u][i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q[4];
+        dev::i8x4_to_f16(word(w[u][0], j), q[0], q[2]);
+        dev::i8x4_to_f16(word(w[u][1], j), q[1], q[3]);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          uint32_t f0, f1;
+          dev::i8x4_to_f16(word(x[u][i], j), f0, f1);
+          mma_f16(acc[i], q, f0, f1);
+        }
       }
     }
   }
@@ -91,13 +104,15 @@ __global__ void __launch_bounds__(32 * kWarps) i8_stream_kernel(const I8Params p
     s_part[warp][g + 8][8 * i + 2 * t + 1] = acc[i][3];
   }
   __syncthreads();
-  for (int i = (int)threadIdx.x; i < kRows * kTok; i += 32 * kWarps) {
-    const int r = i % kRows, m = m0 + i / kRows, n = n0 + r;
-    if (m >= p.M || n >= p.N) continue;
+  const int live = min(kTok, p.M - m0), r = (int)threadIdx.x % kRows, n = n0 + r;
+  const I8Channel channel(p, l, n);
+  const float* scales = p.b_scale + (long long)l * p.M + m0;
+  for (int c = (int)threadIdx.x / kRows; c < live; c += 32 * kWarps / kRows) {
+    const float scale = scales[c];
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_part[w][r][i / kRows];
-    store_i8_result(p, l, m, n, v);
+    for (int w = 0; w < kWarps; ++w) v += s_part[w][r][c];
+    if (n < p.N) store_i8_result(p, l, m0 + c, n, v, scale, channel);
   }
 }
 
@@ -109,12 +124,10 @@ cudaError_t launch_stream(const I8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_i8_stream(const I8Params& p, const I8Plan& plan, cudaStream_t stream) {
-  switch (plan.tokens) {
-    case 8: return launch_stream<8>(p, stream);
-    case 16: return launch_stream<16>(p, stream);
-    default: return launch_stream<32>(p, stream);
-  }
+cudaError_t launch_i8_stream(const I8Params& p, cudaStream_t stream) {
+  if (p.M <= 8) return launch_stream<8>(p, stream);
+  if (p.M <= 16) return launch_stream<16>(p, stream);
+  return launch_stream<32>(p, stream);
 }
 
 }  // namespace splitk

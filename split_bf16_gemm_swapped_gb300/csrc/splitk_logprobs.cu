@@ -29,7 +29,8 @@ namespace {
 
 constexpr int kThreadsLp = 512;
 constexpr int kWarpsLp = kThreadsLp / 32;
-constexpr int kGroup = 256;                 // logits of a group
+constexpr int kGroup = 256;                 // logits of a group: eight of each lane
+constexpr int kAhead = 4;                   // groups whose loads a warp has in flight
 constexpr int kMaxTop = 32;
 constexpr int kMaxVocab = 1 << 22;
 constexpr int kFewCandidates = 128;         // candidates ranked by counting; more are drawn one by one
@@ -49,16 +50,31 @@ struct LogprobParams {
   int rows, V, k;
 };
 
-// kType: 1 bf16, 2 f32, 3 f16 (the codes of splitk.h plus one).
+// kType: 1 bf16, 2 f32, 3 f16.  A lane's eight logits of a group come in kLoads
+// 16-byte words; the largest of them is found on the packed values.
+__device__ __forceinline__ float f16_one(uint16_t v) {
+  float f;
+  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v));
+  return f;
+}
 template <int kType>
 struct Logit;
 template <>
 struct Logit<1> {
-  static constexpr int kPerLoad = 8;
+  static constexpr int kPerLoad = 8, kLoads = 1;
   using T = uint16_t;
   __device__ static float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-  __device__ static void unpack(const uint4& w, float* f) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  __device__ static uint32_t pair_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float max_of(const uint4 (&w)[1]) {
+    const uint32_t m = pair_max(pair_max(w[0].x, w[0].y), pair_max(w[0].z, w[0].w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  __device__ static void unpack(const uint4 (&w)[1], float (&f)[8]) {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(u[i] << 16);
@@ -66,33 +82,45 @@ struct Logit<1> {
     }
   }
 };
-__device__ __forceinline__ float f16_one(uint16_t v) {
-  float f;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v));
-  return f;
-}
 template <>
 struct Logit<3> {
-  static constexpr int kPerLoad = 8;
+  static constexpr int kPerLoad = 8, kLoads = 1;
   using T = uint16_t;
   __device__ static float one(uint16_t v) { return f16_one(v); }
-  __device__ static void unpack(const uint4& w, float* f) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  __device__ static uint32_t pair_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  __device__ static float max_of(const uint4 (&w)[1]) {
+    const uint32_t m = pair_max(pair_max(w[0].x, w[0].y), pair_max(w[0].z, w[0].w));
+    return fmaxf(f16_one((uint16_t)m), f16_one((uint16_t)(m >> 16)));
+  }
+  __device__ static void unpack(const uint4 (&w)[1], float (&f)[8]) {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[2 * i] = f16_one((uint16_t)(u[i] & 0xFFFFu));
+      f[2 * i] = f16_one((uint16_t)u[i]);
       f[2 * i + 1] = f16_one((uint16_t)(u[i] >> 16));
     }
   }
 };
 template <>
 struct Logit<2> {
-  static constexpr int kPerLoad = 4;
+  static constexpr int kPerLoad = 4, kLoads = 2;
   using T = float;
   __device__ static float one(float v) { return v; }
-  __device__ static void unpack(const uint4& w, float* f) {
-    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y);
-    f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+  __device__ static void unpack(const uint4 (&w)[2], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(w[i].x), f[4 * i + 1] = __uint_as_float(w[i].y);
+      f[4 * i + 2] = __uint_as_float(w[i].z), f[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+  }
+  __device__ static float max_of(const uint4 (&w)[2]) {
+    float f[8];
+    unpack(w, f);
+    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
   }
 };
 
@@ -118,9 +146,9 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 
 // A row as 16-byte words: position p counts from the aligned address at or
-// before the row's first logit, so logit i stands at p = i + shift.  A word
-// that reaches over either end is read one logit at a time, and what is not
-// of the row reads as -inf.
+// before the row's first logit, so logit i stands at p = i + shift.  Groups
+// that reach over either end are read one logit at a time, and what is not of
+// the row reads as -inf.
 template <int kType>
 struct Row {
   using E = Logit<kType>;
@@ -131,26 +159,30 @@ struct Row {
     shift = (int)(((uintptr_t)x & 15u) / sizeof(typename E::T));
   }
   __device__ int groups() const { return (shift + V + kGroup - 1) / kGroup; }
-  // word of positions [p, p + kPerLoad)
-  __device__ __forceinline__ void load(int p, float* f) const {
-    const int i = p - shift;
-    if (i >= 0 && i + E::kPerLoad <= V) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x + i);
-      E::unpack(w, f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E::kPerLoad; ++j) {
-        f[j] = i + j >= 0 && i + j < V ? E::one(x[i + j]) : -INFINITY;
-      }
-    }
-  }
-  // a lane's eight logits of group `g`: positions at(g, lane, j)
+  // whether groups [g, h) lie in the row
+  __device__ bool inside(int g, int h) const { return g * kGroup >= shift && h * kGroup <= shift + V; }
+  // position of the j-th of a lane's eight logits of group `g`
   __device__ static int at(int g, int lane, int j) {
     return g * kGroup + (j / E::kPerLoad) * 32 * E::kPerLoad + lane * E::kPerLoad + j % E::kPerLoad;
   }
-  __device__ __forceinline__ void load_group(int g, int lane, float (&f)[8]) const {
+  __device__ __forceinline__ void load_words(int g, int lane, uint4 (&w)[E::kLoads]) const {
 #pragma unroll
-    for (int j = 0; j < 8; j += E::kPerLoad) load(at(g, lane, j), f + j);
+    for (int i = 0; i < E::kLoads; ++i) {
+      w[i] = *reinterpret_cast<const uint4*>(x + (at(g, lane, i * E::kPerLoad) - shift));
+    }
+  }
+  __device__ __forceinline__ void load_group(int g, int lane, float (&f)[8]) const {
+    if (inside(g, g + 1)) {
+      uint4 w[E::kLoads];
+      load_words(g, lane, w);
+      E::unpack(w, f);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = at(g, lane, j) - shift;
+      f[j] = i >= 0 && i < V ? E::one(x[i]) : -INFINITY;
+    }
   }
 };
 
@@ -171,9 +203,9 @@ struct Sums {
 };
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+  float d;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -189,19 +221,24 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
   return v;
 }
 
-// Adds the sums of `n` parts at `parts` (in order), relative to their largest
-// maximum.
-__device__ __forceinline__ Sums join(const Sums* parts, int n) {
-  float m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, parts[i].m);
-  Sums all{m, 0.0f, 0.0f};
-  for (int i = 0; i < n; ++i) {
-    Sums q = parts[i];
-    q.rebase(m);
-    all.s += q.s;
-    all.t += q.t;
+// One warp: the parts its lanes hold, added relative to their largest maximum.
+__device__ __forceinline__ Sums join(Sums part) {
+  part.rebase(warp_max(part.m));
+  part.s = warp_sum(part.s);
+  part.t = warp_sum(part.t);
+  return part;
+}
+
+// Adds eight logits of each lane, whose warp's largest is at most a.m.
+__device__ __forceinline__ void add_logits(Sums& a, const float (&f)[8]) {
+  const float base = a.m == -INFINITY ? 0.0f : a.m;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float d = max_nan((f[j] - base) * kLog2e, kFarBelow);
+    const float e = exp2_approx(d);
+    a.s += e;
+    a.t = fmaf(e, d, a.t);
   }
-  return all;
 }
 
 // One warp: the `want` best of the n maxima in `best` (0 where taken), as
@@ -210,9 +247,9 @@ __device__ __forceinline__ Sums join(const Sums* parts, int n) {
 __device__ __forceinline__ void select_groups(uint32_t* best, int n, int want, int lane, int* sel, uint32_t* last) {
   const int span = ((n + 1023) / 1024) * 32;
   uint32_t mine = 0;
-  for (int i = 0; i < span; ++i) {
-    const int g = lane * span + i;
-    if (g < n) mine = max(mine, best[g]);
+  for (int i = 0; i < n; i += 32) {
+    const uint32_t top = __reduce_max_sync(kFull, i + lane < n ? best[i + lane] : 0u);
+    if (i / span == lane) mine = max(mine, top);
   }
   for (int r = 0; r < want; ++r) {
     const uint32_t top = __reduce_max_sync(kFull, mine);
@@ -263,22 +300,37 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
   uint64_t* s_cand = reinterpret_cast<uint64_t*>(smem + (((size_t)n * 4u + 15u) & ~(size_t)15u));
 
   Sums a{-INFINITY, 0.0f, 0.0f};
-  for (int g = g0 + warp; g < g1; g += kWarpsLp) {
-    float f[8];
-    row.load_group(g, lane, f);
-    float m = f[0];
+  for (int g = g0 + warp * kAhead; g < g1; g += kWarpsLp * kAhead) {
+    if (g + kAhead <= g1 && row.inside(g, g + kAhead)) {
+      uint4 w[kAhead][Logit<kType>::kLoads];
+      float top = -INFINITY;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
-    m = warp_max(m);
-    if (lane == 0) s_best[g] = order_of(m);
-    if (m > a.m) a.rebase(m);
-    const float base = a.m == -INFINITY ? 0.0f : a.m;
+      for (int i = 0; i < kAhead; ++i) row.load_words(g + i, lane, w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float d = max_nan((f[j] - base) * kLog2e, kFarBelow);
-      const float e = exp2_approx(d);
-      a.s += e;
-      a.t = fmaf(e, d, a.t);
+      for (int i = 0; i < kAhead; ++i) {
+        const float m = warp_max(Logit<kType>::max_of(w[i]));
+        if (lane == 0) s_best[g + i] = order_of(m);
+        top = fmaxf(top, m);
+      }
+      if (top > a.m) a.rebase(top);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        float f[8];
+        Logit<kType>::unpack(w[i], f);
+        add_logits(a, f);
+      }
+    } else {
+      for (int i = g; i < min(g + kAhead, g1); ++i) {
+        float f[8];
+        row.load_group(i, lane, f);
+        float m = f[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
+        m = warp_max(m);
+        if (lane == 0) s_best[i] = order_of(m);
+        if (m > a.m) a.rebase(m);
+        add_logits(a, f);
+      }
     }
   }
   a.s = warp_sum(a.s);
@@ -286,28 +338,35 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
   if (lane == 0) s_warp[warp] = a;
   if (threadIdx.x == 0) s_count = 0;
   __syncthreads();
-  if (threadIdx.x == 0) s_cta = join(s_warp, kWarpsLp);
+  const Sums none{-INFINITY, 0.0f, 0.0f};
+  if (warp == 0) {
+    const Sums all = join(lane < kWarpsLp ? s_warp[lane] : none);
+    if (lane == 0) s_cta = all;
+  }
   if (split > 1) {
     // the first CTA takes the others' sums and maxima from their shared memory
+    __syncwarp();
     dev::cluster_arrive_release();
     dev::cluster_wait_acquire();
     if (rank == 0) {
-      if ((int)threadIdx.x < split && threadIdx.x > 0) {
-        const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), threadIdx.x);
-        s_warp[threadIdx.x] = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
+      if (warp == 0) {
+        Sums part = none;
+        if (lane < split) {
+          const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), (uint32_t)lane);
+          part = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
+        }
+        part = join(part);
+        if (lane == 0) s_cta = part;
       }
-      if (threadIdx.x == 0) s_warp[0] = s_cta;
       if (p.k > 0) {
-        for (int r = 1; r < split; ++r) {
-          const int lo = (int)((long long)n * r / split), hi = (int)((long long)n * (r + 1) / split);
-          for (int g = lo + (int)threadIdx.x; g < hi; g += kThreadsLp) {
-            s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
-          }
+        for (int g = g1 + (int)threadIdx.x; g < n; g += kThreadsLp) {
+          // the rank whose run of groups holds g
+          const int r = (int)(((long long)(g + 1) * split - 1) / n);
+          s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
         }
       }
-      __syncthreads();
-      if (threadIdx.x == 0) s_cta = join(s_warp, split);
     }
+    __syncwarp();
     dev::cluster_arrive_release();
     dev::cluster_wait_acquire();
     if (rank != 0) return;

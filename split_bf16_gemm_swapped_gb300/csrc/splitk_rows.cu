@@ -270,7 +270,7 @@ cudaError_t launch_vecs(const RowParams& p, bool wide, dim3 grid, dim3 block, cu
 }
 
 template <int kRes, int kW>
-cudaError_t launch_rows(const RowParams& p, bool wide, cudaStream_t stream) {
+cudaError_t launch_rows(const RowParams& p, bool wide, int num_sms, cudaStream_t stream) {
   const int vecs = (p.width + kVec - 1) / kVec;
   if (vecs > 4 * kMaxRowThreads) {
     return launch_chained(long_rows_kernel<kRes, kW>, dim3((unsigned)p.rows), dim3(kMaxRowThreads), 0, 1, stream, p);
@@ -282,14 +282,22 @@ cudaError_t launch_rows(const RowParams& p, bool wide, cudaStream_t stream) {
     return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
   }
   const dim3 grid((unsigned)p.rows);
-  const dim3 block((unsigned)(((vecs + 3) / 4 + 31) & ~31));
+  // Few rows: one vector a thread, for the shortest chain of latencies (one row
+  // of 7168: 2.5 us, with four 3.3).  Many: several, so that a CTA's reduction
+  // costs less beside its loads (18432 x 7168 codes: 103 us with two, 128 with
+  // one, 112 with four; the norm's 2048 x 7168: 21.1 us with four, 22.1 with one).
+  int per = !wide || p.rows <= 2 * num_sms ? 1 : kW != 0 ? 4 : 2;
+  while (per < 4 && vecs > per * kMaxRowThreads) per *= 2;
+  const dim3 block((unsigned)(((vecs + per - 1) / per + 31) & ~31));
+  if (per == 1) return launch_vecs<kRes, kW, 1>(p, wide, grid, block, stream);
+  if (per == 2) return launch_vecs<kRes, kW, 2>(p, wide, grid, block, stream);
   return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
 }
 
 template <int kRes>
-cudaError_t launch_weight(const RowParams& p, int weight_type, bool wide, cudaStream_t stream) {
-  if (weight_type == SPLITK_DTYPE_F32) return launch_rows<kRes, 2>(p, wide, stream);
-  return launch_rows<kRes, 1>(p, wide, stream);
+cudaError_t launch_weight(const RowParams& p, int weight_type, bool wide, int num_sms, cudaStream_t stream) {
+  if (weight_type == SPLITK_DTYPE_F32) return launch_rows<kRes, 2>(p, wide, num_sms, stream);
+  return launch_rows<kRes, 1>(p, wide, num_sms, stream);
 }
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
@@ -325,16 +333,17 @@ SPLITK_API int splitk_rmsnorm_i8(const void* x, long long x_stride, const void* 
   const uintptr_t w_size = weight_type == SPLITK_DTYPE_F32 ? 4u : 2u;
   if (!aligned(weight, w_size)) return SPLITK_ERR_MISALIGNED;
   if (residual && (!aligned(residual, r_size) || !aligned(residual_out, r_size))) return SPLITK_ERR_MISALIGNED;
-  rc = require_device(nullptr);
+  DeviceSize dev;
+  rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const RowParams p{static_cast<const uint16_t*>(x), x_stride, residual, residual_out, weight, eps,
                     static_cast<int8_t*>(q), scale, M, D};
   const bool wide = D % kVec == 0 && x_stride % kVec == 0 && aligned(x, 16) && aligned(weight, 16) && aligned(q, 8) &&
                     aligned(residual, 16) && aligned(residual_out, 16);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = !residual                               ? launch_weight<0>(p, weight_type, wide, s)
-                        : residual_type == SPLITK_DTYPE_F32 ? launch_weight<2>(p, weight_type, wide, s)
-                                                                : launch_weight<1>(p, weight_type, wide, s);
+  const cudaError_t e = !residual                               ? launch_weight<0>(p, weight_type, wide, dev.num_sms, s)
+                        : residual_type == SPLITK_DTYPE_F32 ? launch_weight<2>(p, weight_type, wide, dev.num_sms, s)
+                                                                : launch_weight<1>(p, weight_type, wide, dev.num_sms, s);
   return launched(e);
 }
 
@@ -342,12 +351,13 @@ SPLITK_API int splitk_quantize_i8(const void* x, long long x_stride, void* q, fl
                                   splitk_stream_t stream) {
   int rc = check_rows(x, x_stride, q, scale, M, D);
   if (rc != SPLITK_OK) return rc;
-  rc = require_device(nullptr);
+  DeviceSize dev;
+  rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const RowParams p{static_cast<const uint16_t*>(x), x_stride, nullptr, nullptr, nullptr, 0.0f,
                     static_cast<int8_t*>(q), scale, M, D};
   const bool wide = D % kVec == 0 && x_stride % kVec == 0 && aligned(x, 16) && aligned(q, 8);
-  return launched(launch_rows<0, 0>(p, wide, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(launch_rows<0, 0>(p, wide, dev.num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
