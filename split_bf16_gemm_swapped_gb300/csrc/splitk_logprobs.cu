@@ -7,10 +7,11 @@
 //
 // One pass reads the row.  A warp takes 256 consecutive logits (a group) at a
 // time and keeps a running maximum with S and T rescaled when it grows; the
-// group's maximum, needed for that anyway, is also written down.  The k best
-// groups by (maximum, lowest index) hold the k best logits: a logit of any
-// other group has those k groups' maxima before it.  So only k groups are
-// read a second time, whatever the logits are.
+// group's maximum, needed for that anyway, is also written down.  If at least k
+// groups' maxima reach a bound, the k best logits are in groups whose maxima do
+// (a logit of any other group has k larger ones); and the k best groups by
+// (maximum, lowest index) hold them too.  So only some k groups are read a
+// second time, whatever the logits are.
 //
 // A cluster of CTAs shares a row when there are few rows; the first CTA then
 // reads the others' sums and maxima from their shared memory.
@@ -27,13 +28,12 @@ namespace splitk {
 
 namespace {
 
-constexpr int kThreadsLp = 512;
-constexpr int kWarpsLp = kThreadsLp / 32;
 constexpr int kGroup = 256;                 // logits of a group: eight of each lane
-constexpr int kAhead = 4;                   // groups whose loads a warp has in flight
 constexpr int kMaxTop = 32;
 constexpr int kMaxVocab = 1 << 22;
-constexpr int kFewCandidates = 128;         // candidates ranked by counting; more are drawn one by one
+constexpr int kMaxGroups = 64;              // groups read a second time
+constexpr int kMaxCandidates = 1024;        // logits of theirs that may be among the top
+constexpr int kFewCandidates = 128;         // that many are ranked by counting
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFarBelow = -1000.0f;       // in powers of two: exp is 0, and so is exp times it
@@ -51,7 +51,8 @@ struct LogprobParams {
 };
 
 // kType: 1 bf16, 2 f32, 3 f16.  A lane's eight logits of a group come in kLoads
-// 16-byte words; the largest of them is found on the packed values.
+// 16-byte words, kAhead groups at a time; the largest of them is found on the
+// packed values.
 __device__ __forceinline__ float f16_one(uint16_t v) {
   float f;
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v));
@@ -61,13 +62,21 @@ template <int kType>
 struct Logit;
 template <>
 struct Logit<1> {
-  static constexpr int kPerLoad = 8, kLoads = 1;
+  static constexpr int kPerLoad = 8, kLoads = 1, kAhead = 4;
+  static constexpr float kNear = 65536.0f;
+  __device__ static uint32_t pair_of(float v) { return dev::pack_bf16x2(v, v); }
   using T = uint16_t;
   __device__ static float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
   __device__ static uint32_t pair_max(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+  }
+  // the words with no logit under `low` (a pair); a NaN stays one
+  __device__ static void raise(uint4 (&w)[1], uint32_t low) {
+    uint32_t* u[4] = {&w[0].x, &w[0].y, &w[0].z, &w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(*u[i]) : "r"(low));
   }
   __device__ static float max_of(const uint4 (&w)[1]) {
     const uint32_t m = pair_max(pair_max(w[0].x, w[0].y), pair_max(w[0].z, w[0].w));
@@ -84,13 +93,25 @@ struct Logit<1> {
 };
 template <>
 struct Logit<3> {
-  static constexpr int kPerLoad = 8, kLoads = 1;
+  static constexpr int kPerLoad = 8, kLoads = 1, kAhead = 4;
+  static constexpr float kNear = 60000.0f;
+  __device__ static uint32_t pair_of(float v) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v), "f"(v));
+    return d;
+  }
   using T = uint16_t;
   __device__ static float one(uint16_t v) { return f16_one(v); }
   __device__ static uint32_t pair_max(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+  }
+  // the words with no logit under `low` (a pair); a NaN stays one
+  __device__ static void raise(uint4 (&w)[1], uint32_t low) {
+    uint32_t* u[4] = {&w[0].x, &w[0].y, &w[0].z, &w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(*u[i]) : "r"(low));
   }
   __device__ static float max_of(const uint4 (&w)[1]) {
     const uint32_t m = pair_max(pair_max(w[0].x, w[0].y), pair_max(w[0].z, w[0].w));
@@ -107,7 +128,7 @@ struct Logit<3> {
 };
 template <>
 struct Logit<2> {
-  static constexpr int kPerLoad = 4, kLoads = 2;
+  static constexpr int kPerLoad = 4, kLoads = 2, kAhead = 2;
   using T = float;
   __device__ static float one(float v) { return v; }
   __device__ static void unpack(const uint4 (&w)[2], float (&f)[8]) {
@@ -144,6 +165,10 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
 }
+
+// Logits of a row in their order: by value, then by the lowest index.
+__device__ __forceinline__ uint64_t key_of(uint32_t order, int id) { return ((uint64_t)order << 32) | (uint32_t)~id; }
+__device__ __forceinline__ long long id_of(uint64_t key) { return (long long)(uint32_t)~(uint32_t)key; }
 
 // A row as 16-byte words: position p counts from the aligned address at or
 // before the row's first logit, so logit i stands at p = i + shift.  Groups
@@ -230,37 +255,57 @@ __device__ __forceinline__ Sums join(Sums part) {
 }
 
 // Adds eight logits of each lane, whose warp's largest is at most a.m.
+// kClamp: logits may be so far below it that they are not finite beside it.
+template <bool kClamp>
 __device__ __forceinline__ void add_logits(Sums& a, const float (&f)[8]) {
   const float base = a.m == -INFINITY ? 0.0f : a.m;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float d = max_nan((f[j] - base) * kLog2e, kFarBelow);
+    const float d = kClamp ? max_nan((f[j] - base) * kLog2e, kFarBelow) : (f[j] - base) * kLog2e;
     const float e = exp2_approx(d);
     a.s += e;
     a.t = fmaf(e, d, a.t);
   }
 }
 
-// One warp: the `want` best of the n maxima in `best` (0 where taken), as
-// group numbers in order, into `sel`.  Lane l holds the maximum of the l-th
-// 32nd of the groups, so equal maxima go by the lowest group.
-__device__ __forceinline__ void select_groups(uint32_t* best, int n, int want, int lane, int* sel, uint32_t* last) {
+// The same from packed words.  Of 16-bit logits two at a time are raised to 800
+// under the maximum first (exp is 0 from 104 on), where the type resolves that;
+// elsewhere, and for 32-bit ones, each distance is clamped.
+template <int kType>
+__device__ __forceinline__ void add_words(Sums& a, uint4 (&w)[Logit<kType>::kLoads]) {
+  float f[8];
+  if constexpr (kType != 2) {
+    if (fabsf(a.m) < Logit<kType>::kNear) {
+      Logit<kType>::raise(w, Logit<kType>::pair_of(a.m - 800.0f));
+      Logit<kType>::unpack(w, f);
+      add_logits<false>(a, f);
+      return;
+    }
+  }
+  Logit<kType>::unpack(w, f);
+  add_logits<true>(a, f);
+}
+
+// One warp: the k best of the n maxima in `best` (0 where taken), by the lowest
+// group where equal, as group numbers into `sel`; the last one's maximum is the
+// result.  Lane l holds the maximum of the l-th 32nd of the groups.
+__device__ __forceinline__ uint32_t draw_groups(uint32_t* best, int n, int k, int lane, int* sel) {
   const int span = ((n + 1023) / 1024) * 32;
-  uint32_t mine = 0;
+  uint32_t mine = 0, last = 0;
   for (int i = 0; i < n; i += 32) {
     const uint32_t top = __reduce_max_sync(kFull, i + lane < n ? best[i + lane] : 0u);
     if (i / span == lane) mine = max(mine, top);
   }
-  for (int r = 0; r < want; ++r) {
-    const uint32_t top = __reduce_max_sync(kFull, mine);
-    const int owner = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+  for (int r = 0; r < k; ++r) {
+    last = __reduce_max_sync(kFull, mine);
+    const int owner = __ffs(__ballot_sync(kFull, mine == last)) - 1;
     bool found = false;
     uint32_t rest = 0;
     for (int i = 0; i < span; i += 32) {
       const int g = owner * span + i + lane;
       uint32_t v = g < n ? best[g] : 0u;
       if (!found) {
-        const uint32_t hit = __ballot_sync(kFull, g < n && v == top);
+        const uint32_t hit = __ballot_sync(kFull, g < n && v == last);
         if (hit != 0) {
           found = true;
           if (lane == __ffs(hit) - 1) {
@@ -273,20 +318,50 @@ __device__ __forceinline__ void select_groups(uint32_t* best, int n, int want, i
       rest = max(rest, __reduce_max_sync(kFull, v));
     }
     if (lane == owner) mine = rest;
-    if (r == want - 1 && lane == 0) *last = top;
     __syncwarp();
   }
+  return last;
 }
 
-template <int kType>
-__global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParams p, int split) {
+// A lower bound on the k-th largest logit: the k-th largest of 32 of the lanes'
+// values (logits of the row, all different ones), each warp's largest; 0 if
+// there are not that many.  CTA-wide; `some` holds 32 words.
+template <int kWarps>
+__device__ __forceinline__ uint32_t bound_top(uint32_t value, int k, int warp, int lane, uint32_t* some) {
+#pragma unroll
+  for (int i = 0; i < 32 / kWarps; ++i) {
+    const uint32_t top = __reduce_max_sync(kFull, value);
+    const int owner = __ffs(__ballot_sync(kFull, value == top)) - 1;
+    if (lane == owner) {
+      some[(32 / kWarps) * warp + i] = top;
+      value = 0;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t v = some[lane];
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t w = __shfl_sync(kFull, v, i);
+      before += w > v || (w == v && i < lane) ? 1 : 0;
+    }
+    __syncwarp();
+    if (before == k - 1) some[0] = v;
+  }
+  __syncthreads();
+  return some[0];
+}
+
+template <int kType, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) logprobs_kernel(const LogprobParams p, int split) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Sums s_warp[kWarpsLp];
+  __shared__ Sums s_warp[kWarps];
   __shared__ Sums s_cta;
-  __shared__ int s_sel[kMaxTop];
-  __shared__ uint32_t s_last;
-  __shared__ int s_count;
-  __shared__ uint64_t s_round[kWarpsLp];
+  __shared__ int s_sel[kMaxGroups];
+  __shared__ uint32_t s_some[32];
+  __shared__ int s_groups, s_count;
+  __shared__ uint64_t s_cand[kMaxCandidates], s_round[2][kWarps];
   dev::griddep_launch_dependents();
   dev::griddep_wait();
 
@@ -297,50 +372,52 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
   const int n = row.groups();
   const int g0 = (int)((long long)n * rank / split), g1 = (int)((long long)n * (rank + 1) / split);
   uint32_t* s_best = reinterpret_cast<uint32_t*>(smem);              // [n] the groups' maxima
-  uint64_t* s_cand = reinterpret_cast<uint64_t*>(smem + (((size_t)n * 4u + 15u) & ~(size_t)15u));
 
   Sums a{-INFINITY, 0.0f, 0.0f};
-  for (int g = g0 + warp * kAhead; g < g1; g += kWarpsLp * kAhead) {
-    if (g + kAhead <= g1 && row.inside(g, g + kAhead)) {
+  float lane_top = -INFINITY;
+  constexpr int kAhead = Logit<kType>::kAhead;
+  // (a short row: one group at a time, so that every warp has some)
+  const int ahead = g1 - g0 >= kWarps * kAhead ? kAhead : 1;
+  for (int g = g0 + warp * ahead; g < g1; g += kWarps * ahead) {
+    if (ahead == kAhead && g + kAhead <= g1 && row.inside(g, g + kAhead)) {
       uint4 w[kAhead][Logit<kType>::kLoads];
-      float top = -INFINITY;
+      float top = -INFINITY, mine = 0.0f;          // lane i writes down group g + i's maximum
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) row.load_words(g + i, lane, w[i]);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const float m = warp_max(Logit<kType>::max_of(w[i]));
-        if (lane == 0) s_best[g + i] = order_of(m);
+        const float of_lane = Logit<kType>::max_of(w[i]), m = warp_max(of_lane);
+        lane_top = fmaxf(lane_top, of_lane);
+        mine = lane == i ? m : mine;
         top = fmaxf(top, m);
       }
+      if (lane < kAhead) s_best[g + lane] = order_of(mine);
       if (top > a.m) a.rebase(top);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        float f[8];
-        Logit<kType>::unpack(w[i], f);
-        add_logits(a, f);
-      }
+      for (int i = 0; i < kAhead; ++i) add_words<kType>(a, w[i]);
     } else {
-      for (int i = g; i < min(g + kAhead, g1); ++i) {
+      for (int i = g; i < min(g + ahead, g1); ++i) {
         float f[8];
         row.load_group(i, lane, f);
         float m = f[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
+        lane_top = fmaxf(lane_top, m);
         m = warp_max(m);
         if (lane == 0) s_best[i] = order_of(m);
         if (m > a.m) a.rebase(m);
-        add_logits(a, f);
+        add_logits<true>(a, f);
       }
     }
   }
   a.s = warp_sum(a.s);
   a.t = warp_sum(a.t);
   if (lane == 0) s_warp[warp] = a;
-  if (threadIdx.x == 0) s_count = 0;
+  if (threadIdx.x == 0) s_groups = s_count = 0;
   __syncthreads();
   const Sums none{-INFINITY, 0.0f, 0.0f};
   if (warp == 0) {
-    const Sums all = join(lane < kWarpsLp ? s_warp[lane] : none);
+    const Sums all = join(lane < kWarps ? s_warp[lane] : none);
     if (lane == 0) s_cta = all;
   }
   if (split > 1) {
@@ -359,7 +436,7 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
         if (lane == 0) s_cta = part;
       }
       if (p.k > 0) {
-        for (int g = g1 + (int)threadIdx.x; g < n; g += kThreadsLp) {
+        for (int g = g1 + (int)threadIdx.x; g < n; g += 32 * kWarps) {
           // the rank whose run of groups holds g
           const int r = (int)(((long long)(g + 1) * split - 1) / n);
           s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
@@ -386,21 +463,45 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
   }
   if (p.k == 0) return;
 
-  const int want = min(p.k, n);
-  if (warp == 0) select_groups(s_best, n, want, lane, s_sel, &s_last);
+  // The groups to read again: those whose maximum reaches a bound that at
+  // least k of them reach; where too many do (equal maxima), the k best.
+  // The bound is of the lanes' largest logits, or, where other CTAs read a part
+  // of the row, of the groups'.
+  uint32_t mine = order_of(lane_top);
+  if (split > 1) {
+    mine = 0;
+    for (int g = n * warp / kWarps + lane; g < n * (warp + 1) / kWarps; g += 32) mine = max(mine, s_best[g]);
+  }
+  uint32_t bound = bound_top<kWarps>(mine, p.k, warp, lane, s_some);
+  for (int g = (int)threadIdx.x; g < n; g += 32 * kWarps) {
+    if (s_best[g] >= bound) {
+      const int at = atomicAdd(&s_groups, 1);
+      if (at < kMaxGroups) s_sel[at] = g;
+    }
+  }
   __syncthreads();
-  // the chosen groups again: every logit that the last of them does not exclude
-  const uint32_t last = s_last;
-  const bool all_in = n <= p.k;            // fewer groups than alternatives: none excludes anything
-  for (int i = warp; i < want; i += kWarpsLp) {
+  int groups = s_groups;
+  if (groups > kMaxGroups) {
+    groups = min(p.k, n);
+    if (warp == 0) {
+      const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
+      // fewer groups than alternatives: all of them, and every logit in them
+      if (lane == 0) s_some[0] = n <= p.k ? 0u : last;
+    }
+    __syncthreads();
+    bound = s_some[0];
+  }
+  // their logits that reach the bound (0: all)
+  const float least = bound == 0 ? -INFINITY : value_of(bound);
+  for (int i = warp; i < groups; i += kWarps) {
     float f[8];
     row.load_group(s_sel[i], lane, f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int id = Row<kType>::at(s_sel[i], lane, j) - row.shift;
-      const uint32_t o = order_of(f[j]);
-      if (id >= 0 && id < p.V && (all_in || o >= last)) {
-        s_cand[atomicAdd(&s_count, 1)] = ((uint64_t)o << 32) | (uint32_t)~id;
+      if (!(f[j] < least) && id >= 0 && id < p.V) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kMaxCandidates) s_cand[at] = key_of(order_of(f[j]), id);
       }
     }
   }
@@ -411,48 +512,66 @@ __global__ void __launch_bounds__(kThreadsLp) logprobs_kernel(const LogprobParam
   long long* ids = p.top_ids + (long long)row_index * p.k;
   float* tops = p.top_logprobs + (long long)row_index * p.k;
   if (count <= kFewCandidates) {
-    if ((int)threadIdx.x < count) {
-      const uint64_t c = s_cand[threadIdx.x];
+    for (int c = (int)threadIdx.x; c < count; c += 32 * kWarps) {
+      const uint64_t key = s_cand[c];
       int before = 0;
-      for (int i = 0; i < count; ++i) before += s_cand[i] > c ? 1 : 0;
+      for (int i = 0; i < count; ++i) before += s_cand[i] > key ? 1 : 0;
       if (before < p.k) {
-        ids[before] = (long long)(uint32_t)~(uint32_t)c;
-        tops[before] = (value_of((uint32_t)(c >> 32)) - base) - log_s;
+        ids[before] = id_of(key);
+        tops[before] = (value_of((uint32_t)(key >> 32)) - base) - log_s;
       }
     }
     return;
   }
-  for (int r = 0; r < p.k; ++r) {           // many equal logits (a masked row): one at a time
-    uint64_t mine = 0;
-    for (int i = (int)threadIdx.x; i < count; i += kThreadsLp) mine = s_cand[i] > mine ? s_cand[i] : mine;
-    const uint64_t w = warp_max64(mine);
-    if (lane == 0) s_round[warp] = w;
-    __syncthreads();
-    uint64_t top = s_round[0];
-#pragma unroll
-    for (int i = 1; i < kWarpsLp; ++i) top = s_round[i] > top ? s_round[i] : top;
-    if (mine == top) {
-      for (int i = (int)threadIdx.x; i < count; i += kThreadsLp) {
-        if (s_cand[i] == top) s_cand[i] = 0;
+  // More (a short row, many equal logits, a mask that leaves fewer than k): one
+  // alternative after another, from the list, or where that did not hold them
+  // from the groups again.
+  uint64_t last = ~0ull;
+  for (int r = 0; r < p.k; ++r) {
+    uint64_t best = 0;
+    if (count <= kMaxCandidates) {
+      for (int c = (int)threadIdx.x; c < count; c += 32 * kWarps) {
+        const uint64_t key = s_cand[c];
+        if (key < last && key > best) best = key;
       }
-      ids[r] = (long long)(uint32_t)~(uint32_t)top;
-      tops[r] = (value_of((uint32_t)(top >> 32)) - base) - log_s;
+    } else {
+      for (int i = warp; i < groups; i += kWarps) {
+        float f[8];
+        row.load_group(s_sel[i], lane, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int id = Row<kType>::at(s_sel[i], lane, j) - row.shift;
+          const uint64_t key = key_of(order_of(f[j]), id);
+          if (id >= 0 && id < p.V && key < last && key > best) best = key;
+        }
+      }
     }
+    best = warp_max64(best);
+    if (lane == 0) s_round[r & 1][warp] = best;
     __syncthreads();
+    last = s_round[r & 1][0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) last = s_round[r & 1][i] > last ? s_round[r & 1][i] : last;
+    if (threadIdx.x == 0) {
+      ids[r] = id_of(last);
+      tops[r] = (value_of((uint32_t)(last >> 32)) - base) - log_s;
+    }
   }
 }
 
 // Shared memory: the groups' maxima (one more group than the row fills when
-// it starts inside a word) and the candidates of k groups.
-size_t logprob_smem(int V, int k) {
-  const size_t n = ((size_t)V + 7u + kGroup - 1u) / kGroup;
-  return ((n * 4u + 15u) & ~(size_t)15u) + (size_t)k * kGroup * sizeof(uint64_t);
+// it starts inside a word).
+size_t logprob_smem(int V) { return ((size_t)V + 7u + kGroup - 1u) / kGroup * 4u; }
+
+template <int kType, int kWarps>
+cudaError_t launch_warps(const LogprobParams& p, int split, cudaStream_t stream) {
+  return launch_chained(logprobs_kernel<kType, kWarps>, dim3((unsigned)p.rows * (unsigned)split), dim3(32 * kWarps),
+                        logprob_smem(p.V), (unsigned)split, stream, p, split);
 }
 
 template <int kType>
-cudaError_t launch_logprobs(const LogprobParams& p, int split, cudaStream_t stream) {
-  return launch_chained(logprobs_kernel<kType>, dim3((unsigned)p.rows * (unsigned)split), dim3(kThreadsLp),
-                        logprob_smem(p.V, p.k), (unsigned)split, stream, p, split);
+cudaError_t launch_logprobs(const LogprobParams& p, int split, bool few_warps, cudaStream_t stream) {
+  return few_warps ? launch_warps<kType, 4>(p, split, stream) : launch_warps<kType, 16>(p, split, stream);
 }
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
@@ -460,11 +579,14 @@ inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 
 }  // namespace
 
 cudaError_t prepare_logprobs() {
-  const int most = (int)logprob_smem(kMaxVocab, kMaxTop);
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(logprobs_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(logprobs_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(logprobs_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  const int most = (int)logprob_smem(kMaxVocab);
+  cudaError_t e = cudaSuccess;
+  const auto set = [&](auto* kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  };
+  set(logprobs_kernel<1, 4>), set(logprobs_kernel<2, 4>), set(logprobs_kernel<3, 4>);
+  set(logprobs_kernel<1, 16>), set(logprobs_kernel<2, 16>), set(logprobs_kernel<3, 16>);
+  return e;
 }
 
 }  // namespace splitk
@@ -491,14 +613,19 @@ SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long st
   int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
-  // CTAs sharing a row: as many as two CTAs an SM leave, with 16 groups (one
+  // CTAs sharing a row: as many as three CTAs an SM leave, with 16 groups (one
   // a warp) for each at least.
   int split = 1;
-  while (split < 8 && (long long)M * split * 2 <= 2ll * dev.num_sms && V / (split * 2) >= kGroup * kWarpsLp) split *= 2;
+  while (split < 8 && (long long)M * split * 2 <= 3ll * dev.num_sms && V / (split * 2) >= 16 * kGroup) split *= 2;
+  // CTAs of four warps: for many short rows, so that more rows are at their
+  // different stages at once (4096 x 32000 bf16, top 20: 64 us, with sixteen warps
+  // 83; 1024 x 131072: 88 and 55), and for rows that would leave many of sixteen
+  // warps without a group.
+  const bool few_warps = split == 1 && (V <= 32 * kGroup || (M >= 6 * dev.num_sms && V <= 65536));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, s)
-                        : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, s)
-                                                          : launch_logprobs<3>(p, split, s);
+  const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, few_warps, s)
+                        : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, few_warps, s)
+                                                          : launch_logprobs<3>(p, split, few_warps, s);
   return launched(e);
 }
 

@@ -7,7 +7,8 @@
 //
 // max|n| = max|y w| / rms, so one joint reduction of (sum y^2, max|y w|) over
 // the row gives both statistics, and the row's values z = y w stay in
-// registers between reading and coding: every byte is read and written once.
+// registers between reading and coding: every byte is read and written once, and
+// memory is the bound.
 // Sums and statistics are f32; the codes are rounded once, by adding
 // 1.5 * 2^23 in the multiplication that scales them (the sum's low byte is
 // then the two's complement code, rounded to nearest even).
@@ -60,20 +61,23 @@ __device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t 
   return dev::prmt(dev::prmt(a, b, 0x0040u), dev::prmt(c, d, 0x0040u), 0x5410u);
 }
 
-// Eight consecutive elements from 16-byte aligned memory of type kType
-// (1 bf16, 2 f32).
+// Eight consecutive elements in 16-byte words of type kType (1 bf16, 2 f32).
 template <int kType>
-__device__ __forceinline__ void load8(const void* p, long long at, float (&v)[kVec]) {
-  if (kType == 1) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z), v[5] = bf16_hi(w.z), v[6] = bf16_lo(w.w), v[7] = bf16_hi(w.w);
-  } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Words {
+  uint4 w[kType];
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * (2 * kType));
+#pragma unroll
+    for (int i = 0; i < kType; ++i) w[i] = from[i];
   }
-}
+  __device__ __forceinline__ void unpack(float (&v)[kVec]) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      v[j] = kType == 2 ? __uint_as_float(u[j]) : j % 2 == 0 ? bf16_lo(u[j / 2]) : bf16_hi(u[j / 2]);
+    }
+  }
+};
 
 template <int kType>
 __device__ __forceinline__ float load1(const void* p, long long at) {
@@ -90,20 +94,21 @@ __device__ __forceinline__ void store1(void* p, long long at, float v) {
 }
 
 // The row's sum and maximum, in every thread of the row.  A row is one warp
-// (blockDim.x = 32, blockDim.y rows a CTA) or the whole CTA.
-__device__ __forceinline__ void reduce_row(float& sum, float& amax) {
+// (blockDim.x = 32, blockDim.y rows a CTA) or the whole CTA, which takes turns
+// between two buffers so that one barrier a row is enough.
+__device__ __forceinline__ void reduce_row(float& sum, float& amax, int turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
   }
   if (blockDim.x == 32) return;
-  __shared__ float s_sum[32], s_max[32];
+  __shared__ float s_sum[2][32], s_max[2][32];
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, warps = (int)blockDim.x >> 5;
-  if (lane == 0) s_sum[warp] = sum, s_max[warp] = amax;
+  if (lane == 0) s_sum[turn][warp] = sum, s_max[turn][warp] = amax;
   __syncthreads();
-  sum = lane < warps ? s_sum[lane] : 0.0f;
-  amax = lane < warps ? s_max[lane] : 0.0f;
+  sum = lane < warps ? s_sum[turn][lane] : 0.0f;
+  amax = lane < warps ? s_max[turn][lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -128,33 +133,44 @@ __device__ __forceinline__ float row_scale(bool norm, float sum, float amax, int
 }
 
 // kRes: 0 no residual, 1 bf16, 2 f32.  kW: 0 no norm (quantise alone), 1 bf16
-// weight, 2 f32 weight.  kVecs: 8-element vectors a thread holds.  kWide:
-// every row and the weight are read and written in 16-byte vectors; else one
-// element at a time, lane by lane.
-template <int kRes, int kW, int kVecs, bool kWide>
+// weight, 2 f32 weight.  kVecs: 8-element vectors a thread holds.
+//
+// Rows and weight in 16-byte vectors.  A CTA takes row after row; the next row's
+// words are on their way while this one is reduced and coded, so that loads are
+// in flight all the time (18432 x 7168 codes, a CTA a row: 103 us).
+template <int kRes, int kW, int kVecs>
 __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p) {
+  constexpr bool kNext = kVecs <= 2;     // registers for the next row's words
   dev::griddep_launch_dependents();
   dev::griddep_wait();
-  const int row = (int)(blockIdx.x * blockDim.y + threadIdx.y);
-  if (row >= p.rows) return;             // whole warps: blockDim.y > 1 only with one warp a row
-  const int tid = (int)threadIdx.x, step = (int)blockDim.x;
-  const uint16_t* x = p.x + (long long)row * p.x_stride;
-  const long long base = (long long)row * p.width;
-  float z[kVecs][kVec];
-  float sum = 0.0f, amax = 0.0f;
+  const int tid = (int)threadIdx.x, step = (int)blockDim.x, stride = (int)(gridDim.x * blockDim.y);
+  Words<1> xw[kVecs];
+  Words<kRes == 0 ? 1 : kRes> rw[kVecs];
+  const auto load = [&](int row) {
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    if (kWide) {
+    for (int v = 0; v < kVecs; ++v) {
       const int e = (v * step + tid) * kVec;
-      if (e >= p.width) {
+      if (e >= p.width) continue;
+      xw[v].load(p.x, (long long)row * p.x_stride + e);
+      if (kRes != 0) rw[v].load(p.residual, (long long)row * p.width + e);
+    }
+  };
+  int row = (int)(blockIdx.x * blockDim.y + threadIdx.y);
+  if (row < p.rows) load(row);
+  for (int turn = 0; row < p.rows; row += stride, turn ^= 1) {     // uniform in a row's threads
+    const long long base = (long long)row * p.width;
+    float z[kVecs][kVec];
+    float sum = 0.0f, amax = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) z[v][j] = 0.0f;
-        continue;
-      }
-      load8<1>(x, e, z[v]);
+    for (int v = 0; v < kVecs; ++v) {
+      const int e = (v * step + tid) * kVec;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) z[v][j] = 0.0f;
+      if (e >= p.width) continue;
+      xw[v].unpack(z[v]);
       if (kRes != 0) {
         float r[kVec];
-        load8<kRes == 0 ? 1 : kRes>(p.residual, base + e, r);
+        rw[v].unpack(r);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) z[v][j] += r[j];
         if (kRes == 1) {
@@ -169,62 +185,80 @@ __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p)
         }
       }
       if (kW != 0) {
+        Words<kW == 0 ? 1 : kW> ww;
         float w[kVec];
-        load8<kW == 0 ? 1 : kW>(p.weight, e, w);
+        ww.load(p.weight, e);
+        ww.unpack(w);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           sum = fmaf(z[v][j], z[v][j], sum);
           z[v][j] *= w[j];
         }
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const int e = (v * kVec + j) * step + tid;
-        z[v][j] = 0.0f;
-        if (e >= p.width) continue;
-        float y = bf16_one(x[e]);
-        if (kRes != 0) {
-          y += load1<kRes == 0 ? 1 : kRes>(p.residual, base + e);
-          store1<kRes == 0 ? 1 : kRes>(p.residual_out, base + e, y);
-        }
-        if (kW != 0) {
-          sum = fmaf(y, y, sum);
-          y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
-        }
-        z[v][j] = y;
+      for (int j = 0; j < kVec; ++j) amax = max_nan(amax, fabsf(z[v][j]));
+    }
+    if (kNext && row + stride < p.rows) load(row + stride);
+    reduce_row(sum, amax, turn);
+    float first, mult;
+    const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
+    if (tid == 0) p.scale[row] = s;
+    if (first != 1.0f) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) z[v][j] *= first;
       }
     }
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) amax = max_nan(amax, fabsf(z[v][j]));
-  }
-  reduce_row(sum, amax);
-  float first, mult;
-  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
-  if (tid == 0) p.scale[row] = s;
-  if (first != 1.0f) {
-#pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) z[v][j] *= first;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    if (kWide) {
       const int e = (v * step + tid) * kVec;
       if (e >= p.width) continue;
       uint2 o;
       o.x = pack_codes(code_of(z[v][0], mult), code_of(z[v][1], mult), code_of(z[v][2], mult), code_of(z[v][3], mult));
       o.y = pack_codes(code_of(z[v][4], mult), code_of(z[v][5], mult), code_of(z[v][6], mult), code_of(z[v][7], mult));
       *reinterpret_cast<uint2*>(p.q + base + e) = o;
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const int e = (v * kVec + j) * step + tid;
-        if (e < p.width) p.q[base + e] = (int8_t)(code_of(z[v][j], mult) & 0xFFu);
-      }
     }
+    if (!kNext && row + stride < p.rows) load(row + stride);
+  }
+}
+
+// Rows of any width and alignment, an element at a time (lane by lane, so that
+// a warp's loads are consecutive), kEach of them a thread.
+template <int kRes, int kW, int kEach>
+__global__ void __launch_bounds__(kMaxRowThreads) odd_rows_kernel(const RowParams p) {
+  dev::griddep_launch_dependents();
+  dev::griddep_wait();
+  const int row = (int)blockIdx.x, tid = (int)threadIdx.x, step = (int)blockDim.x;
+  const uint16_t* x = p.x + (long long)row * p.x_stride;
+  const long long base = (long long)row * p.width;
+  float z[kEach];
+  float sum = 0.0f, amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int e = j * step + tid;
+    z[j] = 0.0f;
+    if (e >= p.width) continue;
+    float y = bf16_one(x[e]);
+    if (kRes != 0) {
+      y += load1<kRes == 0 ? 1 : kRes>(p.residual, base + e);
+      store1<kRes == 0 ? 1 : kRes>(p.residual_out, base + e, y);
+    }
+    if (kW != 0) {
+      sum = fmaf(y, y, sum);
+      y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
+    }
+    z[j] = y;
+    amax = max_nan(amax, fabsf(y));
+  }
+  reduce_row(sum, amax, 0);
+  float first, mult;
+  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
+  if (tid == 0) p.scale[row] = s;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int e = j * step + tid;
+    if (e < p.width) p.q[base + e] = (int8_t)(code_of(z[j] * first, mult) & 0xFFu);
   }
 }
 
@@ -248,7 +282,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) long_rows_kernel(const RowPara
     }
     amax = max_nan(amax, fabsf(y));
   }
-  reduce_row(sum, amax);
+  reduce_row(sum, amax, 0);
   float first, mult;
   const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
   if (threadIdx.x == 0) p.scale[row] = s;
@@ -263,35 +297,33 @@ __global__ void __launch_bounds__(kMaxRowThreads) long_rows_kernel(const RowPara
   }
 }
 
-template <int kRes, int kW, int kVecs>
-cudaError_t launch_vecs(const RowParams& p, bool wide, dim3 grid, dim3 block, cudaStream_t stream) {
-  return wide ? launch_chained(rows_kernel<kRes, kW, kVecs, true>, grid, block, 0, 1, stream, p)
-              : launch_chained(rows_kernel<kRes, kW, kVecs, false>, grid, block, 0, 1, stream, p);
-}
-
 template <int kRes, int kW>
 cudaError_t launch_rows(const RowParams& p, bool wide, int num_sms, cudaStream_t stream) {
   const int vecs = (p.width + kVec - 1) / kVec;
-  if (vecs > 4 * kMaxRowThreads) {
+  if (vecs > (wide ? 4 : 2) * kMaxRowThreads) {
     return launch_chained(long_rows_kernel<kRes, kW>, dim3((unsigned)p.rows), dim3(kMaxRowThreads), 0, 1, stream, p);
   }
-  if (vecs <= 4 * 32) {                  // a warp a row, four rows a CTA
-    const dim3 block(32, 4), grid((unsigned)((p.rows + 3) / 4));
-    if (vecs <= 32) return launch_vecs<kRes, kW, 1>(p, wide, grid, block, stream);
-    if (vecs <= 64) return launch_vecs<kRes, kW, 2>(p, wide, grid, block, stream);
-    return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
+  const auto threads = [&](int per) { return (unsigned)(((vecs + per - 1) / per + 31) & ~31); };
+  if (!wide) {
+    const dim3 grid((unsigned)p.rows);
+    return vecs <= kMaxRowThreads
+               ? launch_chained(odd_rows_kernel<kRes, kW, 8>, grid, dim3(threads(1)), 0, 1, stream, p)
+               : launch_chained(odd_rows_kernel<kRes, kW, 16>, grid, dim3(threads(2)), 0, 1, stream, p);
   }
-  const dim3 grid((unsigned)p.rows);
-  // Few rows: one vector a thread, for the shortest chain of latencies (one row
-  // of 7168: 2.5 us, with four 3.3).  Many: several, so that a CTA's reduction
-  // costs less beside its loads (18432 x 7168 codes: 103 us with two, 128 with
-  // one, 112 with four; the norm's 2048 x 7168: 21.1 us with four, 22.1 with one).
-  int per = !wide || p.rows <= 2 * num_sms ? 1 : kW != 0 ? 4 : 2;
-  while (per < 4 && vecs > per * kMaxRowThreads) per *= 2;
-  const dim3 block((unsigned)(((vecs + per - 1) / per + 31) & ~31));
-  if (per == 1) return launch_vecs<kRes, kW, 1>(p, wide, grid, block, stream);
-  if (per == 2) return launch_vecs<kRes, kW, 2>(p, wide, grid, block, stream);
-  return launch_vecs<kRes, kW, 4>(p, wide, grid, block, stream);
+  // A warp a row of up to 512 features, four rows a CTA; else a CTA a row.  Few
+  // rows get one vector a thread, for the shortest chain of latencies (one row
+  // of 7168: 2.5 us, with four 3.3); many get two and a CTA takes several.
+  const bool warp_rows = vecs <= 64;
+  const bool few = p.rows <= 2 * num_sms;
+  const int per = warp_rows ? (vecs <= 32 ? 1 : 2) : vecs > 2 * kMaxRowThreads ? 4 : few && vecs <= kMaxRowThreads ? 1 : 2;
+  const dim3 block = warp_rows ? dim3(32, 4) : dim3(threads(per));
+  // as many CTAs as are resident at once (64 registers a thread: 1024 threads an SM)
+  const int resident = num_sms * (kMaxRowThreads / (int)(block.x * block.y));
+  const int ctas = (p.rows + (int)block.y - 1) / (int)block.y;
+  const dim3 grid((unsigned)(ctas < resident ? ctas : resident));
+  if (per == 1) return launch_chained(rows_kernel<kRes, kW, 1>, grid, block, 0, 1, stream, p);
+  if (per == 2) return launch_chained(rows_kernel<kRes, kW, 2>, grid, block, 0, 1, stream, p);
+  return launch_chained(rows_kernel<kRes, kW, 4>, grid, block, 0, 1, stream, p);
 }
 
 template <int kRes>

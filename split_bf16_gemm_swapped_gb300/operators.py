@@ -197,8 +197,12 @@ def splitk_logprobs(logits, tokens=None, top_k: int = 0, logprob=None, entropy=N
     if tokens is not None:
         if tokens.dtype is not _I64 or tokens.shape != shape or not tokens.is_contiguous():
             raise ValueError(f"tokens must be a contiguous int64 tensor of shape {tuple(shape)}")
-        logprob = (_empty(shape, dtype=_F32, device=device) if logprob is None
-                   else _given(logprob, "logprob", shape, _F32, at))
+        if logprob is None and entropy is None:            # one allocation for the two
+            logprob, entropy = _empty((2, *shape), dtype=_F32, device=device).unbind()
+        elif logprob is None:
+            logprob = _empty(shape, dtype=_F32, device=device)
+        else:
+            _given(logprob, "logprob", shape, _F32, at)
         t_ptr, l_ptr = tokens.data_ptr(), logprob.data_ptr()
     elif logprob is not None:
         raise ValueError("logprob needs tokens")
