@@ -21,7 +21,7 @@ _empty = torch.empty
 # the handle of a device's current stream (what torch.cuda.current_stream()
 # wraps in an object, at the cost of a small kernel)
 _stream_handle = torch._C._cuda_getCurrentRawStream
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
 
 
 def _type_error(name, t, allowed):
@@ -63,18 +63,18 @@ def _rows(t, name):
     raise ValueError(f"{name} is [M, D] with contiguous rows, or a contiguous [L, M, D]")
 
 
-def _call(where, at, stream, *args):
-    """One library call on device `at` (made current) and `stream` (the
-    device's current one when None)."""
-    handle = _stream_handle(at) if stream is None else stream.cuda_stream
-    fn = getattr(load_library(), where)
-    if _current_device() == at:
-        rc = fn(*args, handle)
-    else:
+def _on_device(fn, at):
+    """fn, called with device `at` current."""
+    def call(*args):
         with torch.cuda.device(at):
-            rc = fn(*args, handle)
-    if rc != 0:
-        raise SplitKError(rc, where)
+            return fn(*args)
+    return call
+
+
+def _entry(name, at):
+    """The library's entry point `name` for operands on device `at`."""
+    fn = getattr(load_library(), name)
+    return fn if _current_device() == at else _on_device(fn, at)
 
 
 def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=None, residual_out=None,
@@ -112,8 +112,12 @@ def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale
     q = _empty(shape, dtype=_I8, device=x.device) if q is None else _given(q, "q", shape, _I8, at)
     scale = (_empty(shape[:-1], dtype=_F32, device=x.device) if scale is None
              else _given(scale, "scale", shape[:-1], _F32, at))
-    _call("splitk_rmsnorm_i8", at, stream, x.data_ptr(), stride, r_in, r_out, _CODES.get(r_type, 0),
-          weight.data_ptr(), _CODES[weight.dtype], eps, q.data_ptr(), scale.data_ptr(), M, D)
+    rc = _entry("splitk_rmsnorm_i8", at)(
+        x.data_ptr(), stride, r_in, r_out, _CODES.get(r_type, 0), weight.data_ptr(), _CODES[weight.dtype], eps,
+        q.data_ptr(), scale.data_ptr(), M, D,
+        _stream_handle(at) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise SplitKError(rc, "splitk_rmsnorm_i8")
     return q, scale, residual_out
 
 
@@ -130,7 +134,11 @@ def splitk_quantize_i8(x, q=None, scale=None, stream=None):
     q = _empty(shape, dtype=_I8, device=x.device) if q is None else _given(q, "q", shape, _I8, at)
     scale = (_empty(shape[:-1], dtype=_F32, device=x.device) if scale is None
              else _given(scale, "scale", shape[:-1], _F32, at))
-    _call("splitk_quantize_i8", at, stream, x.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), M, D)
+    rc = _entry("splitk_quantize_i8", at)(
+        x.data_ptr(), stride, q.data_ptr(), scale.data_ptr(), M, D,
+        _stream_handle(at) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise SplitKError(rc, "splitk_quantize_i8")
     return q, scale
 
 
@@ -172,8 +180,12 @@ def splitk_gemm_i8(a_q, a_scale, b_q, b_scale, c=None, bias=None, out_dtype=None
     if out_dtype is not _BF16 and out_dtype is not _F32:
         raise TypeError(f"c must be bfloat16 or float32, not {str(out_dtype)[6:]}")
     c = _empty(outputs, dtype=out_dtype, device=a_q.device) if c is None else _given(c, "c", outputs, out_dtype, at)
-    _call("splitk_gemm_i8", at, stream, a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(),
-          None if bias is None else bias.data_ptr(), c.data_ptr(), _CODES[out_dtype], M, N, K, L)
+    rc = _entry("splitk_gemm_i8", at)(
+        a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(),
+        None if bias is None else bias.data_ptr(), c.data_ptr(), _CODES[out_dtype], M, N, K, L,
+        _stream_handle(at) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise SplitKError(rc, "splitk_gemm_i8")
     return c
 
 
@@ -197,12 +209,8 @@ def splitk_logprobs(logits, tokens=None, top_k: int = 0, logprob=None, entropy=N
     if tokens is not None:
         if tokens.dtype is not _I64 or tokens.shape != shape or not tokens.is_contiguous():
             raise ValueError(f"tokens must be a contiguous int64 tensor of shape {tuple(shape)}")
-        if logprob is None and entropy is None:            # one allocation for the two
-            logprob, entropy = _empty((2, *shape), dtype=_F32, device=device).unbind()
-        elif logprob is None:
-            logprob = _empty(shape, dtype=_F32, device=device)
-        else:
-            _given(logprob, "logprob", shape, _F32, at)
+        logprob = (_empty(shape, dtype=_F32, device=device) if logprob is None
+                   else _given(logprob, "logprob", shape, _F32, at))
         t_ptr, l_ptr = tokens.data_ptr(), logprob.data_ptr()
     elif logprob is not None:
         raise ValueError("logprob needs tokens")
@@ -217,6 +225,9 @@ def splitk_logprobs(logits, tokens=None, top_k: int = 0, logprob=None, entropy=N
         i_ptr, p_ptr = top_ids.data_ptr(), top_logprobs.data_ptr()
     elif top_ids is not None or top_logprobs is not None:
         raise ValueError("the alternatives' outputs need top_k > 0")
-    _call("splitk_logprobs", at, stream, logits.data_ptr(), _CODES[kind], stride, t_ptr, l_ptr, entropy.data_ptr(),
-          top_k, i_ptr, p_ptr, M, V)
+    rc = _entry("splitk_logprobs", at)(
+        logits.data_ptr(), _CODES[kind], stride, t_ptr, l_ptr, entropy.data_ptr(), top_k, i_ptr, p_ptr, M, V,
+        _stream_handle(at) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise SplitKError(rc, "splitk_logprobs")
     return logprob, entropy, top_ids, top_logprobs
