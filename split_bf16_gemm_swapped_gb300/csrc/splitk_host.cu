@@ -1233,6 +1233,8 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int
 
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
+unsigned injected() { return g_inject.load(); }
+
 }  // namespace splitk
 
 using namespace splitk;

@@ -90,7 +90,7 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   I8Plan plan{};
   const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
-  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, s) : launch_i8_tile(p, plan, wait_limit_ns(), s));
+  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, s) : launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
 }
 
 }  // extern "C"

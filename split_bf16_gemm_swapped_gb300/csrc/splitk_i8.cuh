@@ -45,6 +45,12 @@ struct I8Params {
   int M, N, K, L;
 };
 
+// The bound on its waits, and the injected failure of a test.
+struct I8Waits {
+  unsigned long long limit_ns;
+  unsigned inject;
+};
+
 // How the tcgen05 kernel runs: tiles of 256 weight rows by `tokens`, counted
 // tokens first, then rows, then batches; the first `whole` of them on one pair
 // of CTAs each, the others on `split` pairs that share K.
@@ -54,7 +60,7 @@ struct I8Plan {
   int split;
 };
 cudaError_t launch_i8_stream(const I8Params& p, cudaStream_t stream);
-cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, unsigned long long wait_limit_ns, cudaStream_t stream);
+cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, const I8Waits& waits, cudaStream_t stream);
 
 // What one weight row's outputs share; loaded once, before the first store
 // (which the compiler must take to alias it).

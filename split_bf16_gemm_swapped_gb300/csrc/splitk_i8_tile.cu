@@ -108,7 +108,7 @@ struct TileParams {
   I8Params g;
   int split;
   long long tile0;          // the launch's first tile
-  unsigned long long wait_limit_ns;
+  I8Waits waits;
 };
 
 // One arrival of a warp whose lanes have all done their part.
@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int each = total / split, extra = total % split;
   const int k_tiles = each + (rank < extra ? 1 : 0);
   const int kt0 = rank * each + (rank < extra ? rank : extra);
-  const Waiter waiter{slot_abort, p.wait_limit_ns};
+  const Waiter waiter{slot_abort, p.waits.limit_ns};
+  const bool report = half == 0 || (p.waits.inject & kInjectSkipPublish) == 0;
 
   if (warp == 3 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       dev::tmem_wait_st();
       dev::tc_fence_before();
-      warp_arrive_pair(ready_of_leader + 8u * out.index);
+      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index);
     }
   } else if (warp >= kConvB0) {
     // tokens: 128 / half threads a row, each kPer of its 16-code chunks
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         dev::st_shared_v4(at + (((chunk + 1u) ^ (row & 7u)) << 4), f[4], f[5], f[6], f[7]);
       }
       dev::fence_proxy_async_shared();
-      warp_arrive_pair(ready_of_leader + 8u * out.index);
+      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index);
     }
   }
 
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 template <int kTok>
-cudaError_t launch_tile(const I8Params& g, const I8Plan& plan, unsigned long long wait_limit_ns, cudaStream_t stream) {
+cudaError_t launch_tile(const I8Params& g, const I8Plan& plan, const I8Waits& waits, cudaStream_t stream) {
   CUtensorMap a_map, b_map;
   if (!encode_codes(&a_map, g.a, g.K, g.N, g.L, kMmaM) || !encode_codes(&b_map, g.b, g.K, g.M, g.L, half_of(kTok))) {
     return cudaErrorInvalidValue;
@@ -422,7 +423,7 @@ cudaError_t launch_tile(const I8Params& g, const I8Plan& plan, unsigned long lon
   const long long tiles =
       (long long)((g.M + kTok - 1) / kTok) * ((g.N + 2 * kMmaM - 1) / (2 * kMmaM)) * g.L;
   const auto launch = [&](long long first, long long count, int split) {
-    const TileParams p{g, split, first, wait_limit_ns};
+    const TileParams p{g, split, first, waits};
     return launch_chained(i8_tile_kernel<kTok>, dim3((unsigned)(count * 2 * split)), dim3(kTileThreads), tile_smem(kTok),
                           (unsigned)(2 * split), stream, a_map, b_map, p);
   };
@@ -440,12 +441,12 @@ cudaError_t prepare_tile(int max_dynamic_smem) {
 
 }  // namespace
 
-cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, unsigned long long wait_limit_ns, cudaStream_t stream) {
+cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, const I8Waits& waits, cudaStream_t stream) {
   switch (plan.tokens) {
-    case 32: return launch_tile<32>(p, plan, wait_limit_ns, stream);
-    case 64: return launch_tile<64>(p, plan, wait_limit_ns, stream);
-    case 128: return launch_tile<128>(p, plan, wait_limit_ns, stream);
-    default: return launch_tile<256>(p, plan, wait_limit_ns, stream);
+    case 32: return launch_tile<32>(p, plan, waits, stream);
+    case 64: return launch_tile<64>(p, plan, waits, stream);
+    case 128: return launch_tile<128>(p, plan, waits, stream);
+    default: return launch_tile<256>(p, plan, waits, stream);
   }
 }
 

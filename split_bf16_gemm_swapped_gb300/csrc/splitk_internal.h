@@ -176,9 +176,10 @@ int require_device(DeviceSize* out);
 
 // Defined in splitk_host.cu: a map of [L][rows][K] bytes read in boxes of 128
 // bytes of K by `box_rows` rows, 128-byte swizzle, zeros past the ends; and
-// the bound on a kernel's waits.
+// the bound on a kernel's waits and its injected failures.
 bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows);
 unsigned long long wait_limit_ns();
+unsigned injected();
 
 // Defined in splitk_logprobs.cu.
 cudaError_t prepare_logprobs();

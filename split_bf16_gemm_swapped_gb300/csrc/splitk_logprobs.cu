@@ -254,18 +254,62 @@ __device__ __forceinline__ Sums join(Sums part) {
   return part;
 }
 
-// Adds eight logits of each lane, whose warp's largest is at most a.m.
-// kClamp: logits may be so far below it that they are not finite beside it.
-template <bool kClamp>
-__device__ __forceinline__ void add_logits(Sums& a, const float (&f)[8]) {
+// Pairs of f32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void split_pair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Adds eight logits of each lane, whose warp's largest is at most a.m; they may
+// be so far below it that they are not finite beside it.
+__device__ __forceinline__ void add_any(Sums& a, const float (&f)[8]) {
   const float base = a.m == -INFINITY ? 0.0f : a.m;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float d = kClamp ? max_nan((f[j] - base) * kLog2e, kFarBelow) : (f[j] - base) * kLog2e;
+    const float d = max_nan((f[j] - base) * kLog2e, kFarBelow);
     const float e = exp2_approx(d);
     a.s += e;
     a.t = fmaf(e, d, a.t);
   }
+}
+
+// The same for logits at most 1000 below it, two at a time.
+__device__ __forceinline__ void add_near(Sums& a, const float (&f)[8]) {
+  const uint64_t minus = pair(-a.m, -a.m), scale = pair(kLog2e, kLog2e);
+  uint64_t s = pair(a.s, 0.0f), t = pair(a.t, 0.0f);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t d = pair_mul(pair_add(pair(f[j], f[j + 1]), minus), scale);
+    float d0, d1;
+    split_pair(d, d0, d1);
+    const uint64_t e = pair(exp2_approx(d0), exp2_approx(d1));
+    s = pair_add(s, e);
+    t = pair_fma(e, d, t);
+  }
+  float s0, s1, t0, t1;
+  split_pair(s, s0, s1);
+  split_pair(t, t0, t1);
+  a.s = s0 + s1;
+  a.t = t0 + t1;
 }
 
 // The same from packed words.  Of 16-bit logits two at a time are raised to 800
@@ -278,12 +322,12 @@ __device__ __forceinline__ void add_words(Sums& a, uint4 (&w)[Logit<kType>::kLoa
     if (fabsf(a.m) < Logit<kType>::kNear) {
       Logit<kType>::raise(w, Logit<kType>::pair_of(a.m - 800.0f));
       Logit<kType>::unpack(w, f);
-      add_logits<false>(a, f);
+      add_near(a, f);
       return;
     }
   }
   Logit<kType>::unpack(w, f);
-  add_logits<true>(a, f);
+  add_any(a, f);
 }
 
 // One warp: the k best of the n maxima in `best` (0 where taken), by the lowest
@@ -353,8 +397,9 @@ __device__ __forceinline__ uint32_t bound_top(uint32_t value, int k, int warp, i
   return some[0];
 }
 
+// kWarps: 16, 8 or 4 warps a CTA, 32 an SM (64 registers a thread).
 template <int kType, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) logprobs_kernel(const LogprobParams p, int split) {
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(const LogprobParams p, int split) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Sums s_warp[kWarps];
   __shared__ Sums s_cta;
@@ -376,39 +421,51 @@ __global__ void __launch_bounds__(32 * kWarps) logprobs_kernel(const LogprobPara
   Sums a{-INFINITY, 0.0f, 0.0f};
   float lane_top = -INFINITY;
   constexpr int kAhead = Logit<kType>::kAhead;
-  // (a short row: one group at a time, so that every warp has some)
-  const int ahead = g1 - g0 >= kWarps * kAhead ? kAhead : 1;
-  for (int g = g0 + warp * ahead; g < g1; g += kWarps * ahead) {
-    if (ahead == kAhead && g + kAhead <= g1 && row.inside(g, g + kAhead)) {
-      uint4 w[kAhead][Logit<kType>::kLoads];
-      float top = -INFINITY, mine = 0.0f;          // lane i writes down group g + i's maximum
+  // Blocks of kAhead groups, a warp's block kWarps further on loaded while it
+  // adds one; what is left of the row, or a short row (so that every warp has
+  // some), one group at a time.
+  const int inner0 = row.shift > 0 ? max(g0, 1) : g0, inner1 = min(g1, (row.shift + row.V) / kGroup);
+  const int blocks = inner1 - inner0 >= kWarps * kAhead ? (inner1 - inner0) / kAhead : 0;
+  const auto load = [&](int block, uint4 (&w)[kAhead][Logit<kType>::kLoads]) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) row.load_words(g + i, lane, w[i]);
+    for (int i = 0; i < kAhead; ++i) row.load_words(inner0 + block * kAhead + i, lane, w[i]);
+  };
+  uint4 next[kAhead][Logit<kType>::kLoads];
+  if (warp < blocks) load(warp, next);
+  for (int block = warp; block < blocks; block += kWarps) {
+    uint4 w[kAhead][Logit<kType>::kLoads];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float of_lane = Logit<kType>::max_of(w[i]), m = warp_max(of_lane);
-        lane_top = fmaxf(lane_top, of_lane);
-        mine = lane == i ? m : mine;
-        top = fmaxf(top, m);
-      }
-      if (lane < kAhead) s_best[g + lane] = order_of(mine);
-      if (top > a.m) a.rebase(top);
+    for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) add_words<kType>(a, w[i]);
-    } else {
-      for (int i = g; i < min(g + ahead, g1); ++i) {
-        float f[8];
-        row.load_group(i, lane, f);
-        float m = f[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
-        lane_top = fmaxf(lane_top, m);
-        m = warp_max(m);
-        if (lane == 0) s_best[i] = order_of(m);
-        if (m > a.m) a.rebase(m);
-        add_logits<true>(a, f);
-      }
+      for (int q = 0; q < Logit<kType>::kLoads; ++q) w[i][q] = next[i][q];
     }
+    if (block + kWarps < blocks) load(block + kWarps, next);
+    float top = -INFINITY, mine = 0.0f;            // lane i writes down the block's group i's maximum
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float of_lane = Logit<kType>::max_of(w[i]), m = warp_max(of_lane);
+      lane_top = fmaxf(lane_top, of_lane);
+      mine = lane == i ? m : mine;
+      top = fmaxf(top, m);
+    }
+    if (lane < kAhead) s_best[inner0 + block * kAhead + lane] = order_of(mine);
+    if (top > a.m) a.rebase(top);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) add_words<kType>(a, w[i]);
+  }
+  const int tail = inner0 + blocks * kAhead;       // groups [g0, inner0) and [tail, g1)
+  for (int i = warp; i < (inner0 - g0) + (g1 - tail); i += kWarps) {
+    const int g = i < inner0 - g0 ? g0 + i : tail + i - (inner0 - g0);
+    float f[8];
+    row.load_group(g, lane, f);
+    float m = f[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, f[j]);
+    lane_top = fmaxf(lane_top, m);
+    m = warp_max(m);
+    if (lane == 0) s_best[g] = order_of(m);
+    if (m > a.m) a.rebase(m);
+    add_any(a, f);
   }
   a.s = warp_sum(a.s);
   a.t = warp_sum(a.t);
@@ -570,8 +627,10 @@ cudaError_t launch_warps(const LogprobParams& p, int split, cudaStream_t stream)
 }
 
 template <int kType>
-cudaError_t launch_logprobs(const LogprobParams& p, int split, bool few_warps, cudaStream_t stream) {
-  return few_warps ? launch_warps<kType, 4>(p, split, stream) : launch_warps<kType, 16>(p, split, stream);
+cudaError_t launch_logprobs(const LogprobParams& p, int split, int warps, cudaStream_t stream) {
+  return warps == 4   ? launch_warps<kType, 4>(p, split, stream)
+         : warps == 8 ? launch_warps<kType, 8>(p, split, stream)
+                      : launch_warps<kType, 16>(p, split, stream);
 }
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
@@ -585,6 +644,7 @@ cudaError_t prepare_logprobs() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   };
   set(logprobs_kernel<1, 4>), set(logprobs_kernel<2, 4>), set(logprobs_kernel<3, 4>);
+  set(logprobs_kernel<1, 8>), set(logprobs_kernel<2, 8>), set(logprobs_kernel<3, 8>);
   set(logprobs_kernel<1, 16>), set(logprobs_kernel<2, 16>), set(logprobs_kernel<3, 16>);
   return e;
 }
@@ -613,19 +673,23 @@ SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long st
   int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
-  // CTAs sharing a row: as many as three CTAs an SM leave, with 16 groups (one
+  // CTAs sharing a row: as many as two CTAs an SM leave, with 16 groups (one
   // a warp) for each at least.
   int split = 1;
-  while (split < 8 && (long long)M * split * 2 <= 3ll * dev.num_sms && V / (split * 2) >= 16 * kGroup) split *= 2;
-  // CTAs of four warps: for many short rows, so that more rows are at their
-  // different stages at once (4096 x 32000 bf16, top 20: 64 us, with sixteen warps
-  // 83; 1024 x 131072: 88 and 55), and for rows that would leave many of sixteen
-  // warps without a group.
-  const bool few_warps = split == 1 && (V <= 32 * kGroup || (M >= 6 * dev.num_sms && V <= 65536));
+  while (split < 8 && (long long)M * split * 2 <= 2ll * dev.num_sms && V / (split * 2) >= 16 * kGroup) split *= 2;
+  // Smaller CTAs where there are rows enough for them, so that more rows are at
+  // their different stages at once (1024 x 131072 bf16, top 20: 52 us with eight
+  // warps, 55 with sixteen, 61 with four; 4096 x 32000: 72, 103, 64; 400 x 131072:
+  // 32, 25, 39), and for rows that would leave many of sixteen warps without a
+  // group.
+  const int warps = split > 1                                            ? 16
+                    : V <= 32 * kGroup || (M >= 6 * dev.num_sms && V <= 65536) ? 4
+                    : M >= 4 * dev.num_sms                               ? 8
+                                                                         : 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, few_warps, s)
-                        : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, few_warps, s)
-                                                          : launch_logprobs<3>(p, split, few_warps, s);
+  const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, warps, s)
+                        : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, warps, s)
+                                                          : launch_logprobs<3>(p, split, warps, s);
   return launched(e);
 }
 

@@ -279,6 +279,24 @@ def test_nan_scales_reach_their_tokens_alone():
     assert torch.isfinite(c).all()
 
 
+@pytest.mark.parametrize("M,K", [(64, 256), (40, 4096), (300, 2048)])
+def test_product_reports_a_wait_that_runs_out(M, K):
+    """The pair's second CTA keeps its tiles to itself: the first one's bounded
+    wait runs out, the call says so, and the next call is right again."""
+    a, sa, b, sb, _ = product_inputs(1, M, 512, K, M, batched=False)
+    sk.splitk_set_wait_limit_ns(5_000_000)
+    sk.splitk_debug_inject(sk.INJECT_SKIP_PUBLISH)
+    try:
+        sk.splitk_gemm_i8(a, sa, b, sb)
+        torch.cuda.synchronize()
+        assert sk.splitk_get_fault()["code"] == -6
+    finally:
+        sk.splitk_debug_inject(0)
+        sk.splitk_set_wait_limit_ns(0)
+    assert sk.splitk_get_status() == 0
+    check_product(a, sa, b, sb)
+
+
 # ---------------------------------------------------------------- log probabilities
 def logprob_ref(x, t, k):
     x = x.double().cpu()
@@ -477,6 +495,17 @@ def test_operators_run_on_the_stream_they_are_given():
     s.synchronize()
     for u, v in zip(got[1:], ref[1:]):
         assert torch.equal(u, v)
+
+
+def test_the_example_runs():
+    import subprocess
+    import sys
+    from pathlib import Path
+    root = Path(__file__).resolve().parent.parent
+    res = subprocess.run([sys.executable, str(root / "examples" / "quantized_head.py"), "--tokens", "3", "--width", "512",
+                          "--vocabulary", "1001", "--steps", "3"], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout[-2000:] + res.stderr[-2000:]
+    assert "3 steps of 3 tokens" in res.stdout
 
 
 def test_the_chain_in_a_graph():
