@@ -52,12 +52,14 @@ double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out
   return best;
 }
 
-// Up to 16 tokens the weights stream through registers (no tile is filled that
-// far); up to 32 where that is estimated faster: its rate there is what the
-// legacy tensor path's conversions leave, 2.6 TB/s measured.
+// Whether few tokens' weights stream through registers: up to 8 always (no tile
+// is filled that far); up to 32 where that is estimated faster.  Its measured
+// rate there is 4.7 TB/s for two token fragments a warp, 2.6 for four (each weight
+// is converted once, each token fragment for every 16 weight rows).
 bool streams(int M, int N, int K, int L, double tile_time) {
-  if (M <= 16) return true;
-  return M <= 32 && 2.0 + (double)N * K * L / 2.6e6 < tile_time;
+  if (M <= 8) return true;
+  if (M > 32) return false;
+  return 2.5 + (double)N * K * L / (M <= 16 ? 4.7e6 : 2.6e6) < tile_time;
 }
 
 }  // namespace
@@ -90,7 +92,7 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   I8Plan plan{};
   const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
-  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, s) : launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
+  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, dev.num_sms, s) : launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
 }
 
 }  // extern "C"

@@ -59,7 +59,7 @@ struct I8Plan {
   long long whole;
   int split;
 };
-cudaError_t launch_i8_stream(const I8Params& p, cudaStream_t stream);
+cudaError_t launch_i8_stream(const I8Params& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, const I8Waits& waits, cudaStream_t stream);
 
 // What one weight row's outputs share; loaded once, before the first store
