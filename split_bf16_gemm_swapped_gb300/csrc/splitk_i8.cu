@@ -19,15 +19,15 @@ inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 
 // clusters as the device holds at once, each a CTA's K tiles and a fixed share
 // (set-up, first loads, epilogue; more when ranks exchange sums).  Measured on
 // GB300: a K tile of 256 tokens 0.53 (the MMAs), of up to 128 0.36 (shared
-// memory, conversion, and memory with all SMs at it); fixed 10.5 and 4.6, with a
-// split 3 more.
-double tile_us(long long tiles, int tokens, int k_tiles, int split, const int (&clusters)[3]) {
-  const int fit = clusters[split == 1 ? 0 : split == 2 ? 1 : 2];
+// memory, conversion, and memory with all SMs at it); fixed 9.5 and 4.6, with a
+// split 2 more.
+double tile_us(long long tiles, int tokens, int k_tiles, int split, const int (&clusters)[4]) {
+  const int fit = clusters[split - 1];
   if (tiles == 0) return 0.0;
   if (fit <= 0 || split > k_tiles) return 1e30;
   const double rounds = (double)((tiles + fit - 1) / fit);
   const double each = (tokens == 256 ? 0.53 : 0.36) * ((k_tiles + split - 1) / split);
-  return rounds * (each + (tokens == 256 ? 10.5 : 4.6) + (split > 1 ? 3.0 : 0.0));
+  return rounds * (each + (tokens == 256 ? 9.5 : 4.6) + (split > 1 ? 2.0 : 0.0));
 }
 
 // The tile plan with the least estimated time: all tiles on `split` pairs, or
@@ -41,7 +41,7 @@ double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out
     const long long tiles = (long long)((M + tokens - 1) / tokens) * ((N + 255) / 256) * L;
     const long long fit = dev.i8_clusters[0];
     const long long rounds = fit > 0 ? tiles / fit : 0;
-    for (int split : {1, 2, 4}) {
+    for (int split : {1, 2, 3, 4}) {
       const double all = tile_us(tiles, tokens, k_tiles, split, dev.i8_clusters);
       if (all < best) best = all, *out = I8Plan{tokens, 0, split};
       const double rest = tile_us(rounds * fit, tokens, k_tiles, 1, dev.i8_clusters) +
@@ -92,7 +92,9 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   I8Plan plan{};
   const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
-  return launched(streams(M, N, K, L, tile_time) ? launch_i8_stream(p, dev.num_sms, s) : launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
+  if (streams(M, N, K, L, tile_time)) return launched(launch_i8_stream(p, dev.num_sms, s));
+  if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;      // no CTA pair of it fits the device
+  return launched(launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
 }
 
 }  // extern "C"

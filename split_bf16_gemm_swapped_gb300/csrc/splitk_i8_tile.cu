@@ -13,7 +13,11 @@
 // costs the arrival and the reading of the raw codes, and the writing and the
 // MMA's reading of the tokens' f16 (the weights' f16 never pass through it).
 // A pair halves the token side for each SM.  With one CTA a tile, 128 tokens
-// took ~1,050 clocks a K tile (1,024 by that count; 512 the MMAs alone).
+// took ~1,050 clocks a K tile (1,024 by that count; 512 the MMAs alone).  Pairs
+// take ~690 for 128 tokens, and ~1,020 for 256, where the MMAs (1,024) bound it:
+// 1000 x 7168 x 16384 in 128 us, 94 % of the measured bf16 rate.  Up to 64 tokens
+// the weights' arrival bounds it: 64 x 18432 x 7168 in 26 us, 78 % of the copy rate
+// (5 us of that before the first MMA and after the last).
 //
 // `split` pairs of a cluster may share one output tile, each taking a
 // contiguous run of K tiles; each CTA leaves its f32 sums in its own shared
@@ -109,6 +113,7 @@ struct TileParams {
   int split;
   long long tile0;          // the launch's first tile
   I8Waits waits;
+  bool quads;               // C may be stored four channels at a time
 };
 
 // One arrival of a warp whose lanes have all done their part.
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (split > 1) {
     // this rank's slice of the tokens, a column a warp and four weight rows a
     // lane, kAtOnce columns' loads in flight
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 2;
     const int r4 = 4 * lane;
     const I8Channel ch[4] = {I8Channel(p.g, l, n0 + r4), I8Channel(p.g, l, n0 + r4 + 1), I8Channel(p.g, l, n0 + r4 + 2),
                              I8Channel(p.g, l, n0 + r4 + 3)};
@@ -383,6 +388,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int c = col + i * kWarpsAll;
         if (c >= c1) break;
         const float scale = dev::ld_shared_f32(s_scale + 4u * (uint32_t)c);
+        if (p.quads) {                                  // N a multiple of 4, C aligned for it
+          if (n0 + r4 >= p.g.N) continue;
+          const long long at = ((long long)l * p.g.M + m0 + c) * p.g.N + n0 + r4;
+          float o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = ch[e].result(v[i][e], scale);
+          if (p.g.c_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + at) = make_float4(o[0], o[1], o[2], o[3]);
+          } else {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.g.c) + at) =
+                make_uint2(dev::pack_bf16x2(o[0], o[1]), dev::pack_bf16x2(o[2], o[3]));
+          }
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (n0 + r4 + e < p.g.N) store_i8_result(p.g, l, m0 + c, n0 + r4 + e, v[i][e], scale, ch[e]);
@@ -423,7 +442,8 @@ cudaError_t launch_tile(const I8Params& g, const I8Plan& plan, const I8Waits& wa
   const long long tiles =
       (long long)((g.M + kTok - 1) / kTok) * ((g.N + 2 * kMmaM - 1) / (2 * kMmaM)) * g.L;
   const auto launch = [&](long long first, long long count, int split) {
-    const TileParams p{g, split, first, waits};
+    const uintptr_t quad = g.c_f32 ? 16u : 8u;
+    const TileParams p{g, split, first, waits, g.N % 4 == 0 && (uintptr_t)g.c % quad == 0};
     return launch_chained(i8_tile_kernel<kTok>, dim3((unsigned)(count * 2 * split)), dim3(kTileThreads), tile_smem(kTok),
                           (unsigned)(2 * split), stream, a_map, b_map, p);
   };
@@ -450,20 +470,20 @@ cudaError_t launch_i8_tile(const I8Params& p, const I8Plan& plan, const I8Waits&
   }
 }
 
-cudaError_t prepare_i8_tile(int max_dynamic_smem, int (&clusters)[3]) {
+cudaError_t prepare_i8_tile(int max_dynamic_smem, int (&clusters)[4]) {
   cudaError_t e;
   if ((e = prepare_tile<32>(max_dynamic_smem)) != cudaSuccess) return e;
   if ((e = prepare_tile<64>(max_dynamic_smem)) != cudaSuccess) return e;
   if ((e = prepare_tile<128>(max_dynamic_smem)) != cudaSuccess) return e;
   if ((e = prepare_tile<256>(max_dynamic_smem)) != cudaSuccess) return e;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u << i);
+    cfg.gridDim = dim3(2u * (i + 1));
     cfg.blockDim = dim3(kTileThreads);
     cfg.dynamicSmemBytes = tile_smem(256);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2u << i;
+    attr.val.clusterDim.x = 2u * (i + 1);
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;

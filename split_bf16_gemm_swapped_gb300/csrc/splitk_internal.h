@@ -170,7 +170,7 @@ struct DeviceSize {
   int num_sms;
   size_t smem_per_sm;
   size_t smem_optin;
-  int i8_clusters[3];         // clusters of 1, 2 and 4 CTA pairs of the 8-bit product resident at once
+  int i8_clusters[4];         // clusters of 1, 2, 3 and 4 CTA pairs of the 8-bit product resident at once
 };
 int require_device(DeviceSize* out);
 
@@ -185,7 +185,7 @@ unsigned injected();
 cudaError_t prepare_logprobs();
 
 // Defined in splitk_i8_tile.cu.
-cudaError_t prepare_i8_tile(int max_dynamic_smem, int (&clusters)[3]);
+cudaError_t prepare_i8_tile(int max_dynamic_smem, int (&clusters)[4]);
 cudaError_t read_and_clear_fault_i8(int* out_words);
 
 // The status of a launch, with CUDA's own error record cleared.

@@ -13,6 +13,10 @@
 // (maximum, lowest index) hold them too.  So only some k groups are read a
 // second time, whatever the logits are.
 //
+// Memory bounds the pass (1024 x 131072 bf16: 46 us without alternatives, 87 % of
+// the copy rate); each row's join and selection, some 3 us of latencies, is what
+// 20 alternatives add (52 us), as it overlaps only with other rows' passes.
+//
 // A cluster of CTAs shares a row when there are few rows; the first CTA then
 // reads the others' sums and maxima from their shared memory.
 

@@ -8,10 +8,10 @@
 // max|n| = max|y w| / rms, so one joint reduction of (sum y^2, max|y w|) over
 // the row gives both statistics, and the row's values z = y w stay in
 // registers between reading and coding: every byte is read and written once, and
-// memory is the bound.
-// Sums and statistics are f32; the codes are rounded once, by adding
-// 1.5 * 2^23 in the multiplication that scales them (the sum's low byte is
-// then the two's complement code, rounded to nearest even).
+// memory is the bound (2048 x 7168 with a bf16 residual 16.7 us, 92 % of the copy
+// rate; 18432 x 7168 codes 73 us, 81 %).  Sums and statistics are f32; a code is
+// rounded by adding 1.5 * 2^23 (the sum's low byte is then the two's complement
+// code, rounded to nearest even).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -54,8 +54,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// f32 rounded to the nearest whole number (|v * m| <= 127), in the low byte.
-__device__ __forceinline__ uint32_t code_of(float v, float m) { return __float_as_uint(fmaf(v, m, 12582912.0f)); }
+// v * m rounded to the nearest whole number (|v * m| <= 127), in the low byte.
+// The product is rounded to f32 first: a value halfway between two codes (in
+// bf16 rows they are common) then mostly comes out as that half and goes to the
+// even code, where the product's own last bits would send it either way.
+__device__ __forceinline__ uint32_t code_of(float v, float m) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(v, m), 12582912.0f));
+}
 
 __device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return dev::prmt(dev::prmt(a, b, 0x0040u), dev::prmt(c, d, 0x0040u), 0x5410u);
@@ -125,8 +130,9 @@ __device__ __forceinline__ float row_scale(bool norm, float sum, float amax, int
                                            float* mult) {
   const float rinv = norm ? 1.0f / sqrtf(sum / (float)width + eps) : 1.0f;
   float s = fmaxf(amax * rinv / 127.0f, kMinScale);
+  // rinv / s, which is 127 / amax (one rounding) unless the scale is its floor
+  const float m = s > kMinScale ? 127.0f / amax : rinv / s;
   if (!(sum <= kMaxF32) || !(amax <= kMaxF32)) s = __uint_as_float(0x7FC00000u);
-  const float m = rinv / s;
   *first = m > kMaxF32 ? rinv : 1.0f;
   *mult = m > kMaxF32 ? 1.0f / s : m;
   return s;
@@ -137,7 +143,7 @@ __device__ __forceinline__ float row_scale(bool norm, float sum, float amax, int
 //
 // Rows and weight in 16-byte vectors.  A CTA takes row after row; the next row's
 // words are on their way while this one is reduced and coded, so that loads are
-// in flight all the time (18432 x 7168 codes, a CTA a row: 103 us).
+// in flight all the time (18432 x 7168 codes, a CTA a row: 103 us, so 73).
 template <int kRes, int kW, int kVecs>
 __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p) {
   constexpr bool kNext = kVecs <= 2;     // registers for the next row's words
@@ -337,7 +343,7 @@ inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 
 // The checks both entry points share.
 int check_rows(const void* x, long long x_stride, const void* q, const float* scale, int M, int D) {
   if (!x || !q || !scale) return SPLITK_ERR_NULL;
-  if (M < 1 || D < 1 || x_stride < D || D > (1 << 30)) return SPLITK_ERR_INVALID_SHAPE;
+  if (M < 1 || D < 1 || x_stride < D || M > (1 << 30) || D > (1 << 30)) return SPLITK_ERR_INVALID_SHAPE;
   if (!aligned(x, 2) || !aligned(scale, 4)) return SPLITK_ERR_MISALIGNED;
   return SPLITK_OK;
 }

@@ -27,7 +27,8 @@ def rmsnorm(x=P, stride=64, r=None, r_out=None, r_type=0, w=P, w_type=0, eps=1e-
 def test_rmsnorm_refusals():
     for kw in (dict(x=None), dict(w=None), dict(q=None), dict(s=None), dict(r=P), dict(r_out=P)):
         assert rmsnorm(**kw) == NULL, kw
-    for kw in (dict(M=0), dict(D=0), dict(M=-1), dict(stride=63), dict(D=(1 << 30) + 1, stride=1 << 31)):
+    for kw in (dict(M=0), dict(D=0), dict(M=-1), dict(stride=63), dict(D=(1 << 30) + 1, stride=1 << 31),
+               dict(M=(1 << 30) + 1)):
         assert rmsnorm(**kw) == SHAPE, kw
     for kw in (dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(w_type=2),
                dict(r=P, r_out=P, r_type=2), dict(r=P, r_out=P, r_type=-1)):
@@ -58,7 +59,8 @@ def test_gemm_refusals():
     for kw in (dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(c=None)):
         assert gemm(**kw) == NULL, kw
     for kw in (dict(M=0), dict(N=0), dict(K=0), dict(L=0), dict(K=72), dict(K=8), dict(L=65536),
-               dict(N=65535 * 128 + 1), dict(K=(1 << 30) + 16), dict(M=-5)):
+               dict(N=65535 * 128 + 1), dict(K=(1 << 30) + 16), dict(M=-5),
+               dict(M=1 << 30, N=65535 * 128, L=60000)):
         assert gemm(**kw) == SHAPE, kw
     assert gemm(c_type=2) == ARG and gemm(c_type=-1) == ARG
     for kw in (dict(a=P + 8), dict(b=P + 4), dict(sa=P + 2), dict(sb=P + 1), dict(bias=P + 1), dict(c=P + 1),
