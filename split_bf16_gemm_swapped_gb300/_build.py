@@ -3,8 +3,10 @@
 * ``_lib/libsplitk_sm103a.so``: the CUDA kernels and the C ABI declared in
   ``include/splitk.h``, compiled by nvcc for sm_103a only.
 * ``_lib/libsynthetic.so``: the seeded input generator (plain C, gcc).
+* ``_lib/_operators.so``: the Python binding of the operators around the
+  projection (C++ on PyTorch's headers, g++), linked to the first.
 
-Both are rebuilt when a source is newer than the library.  Host code is
+Each is rebuilt when a source is newer than the library.  Host code is
 portable C/C++ (no x86 intrinsics, no -march=native), so the same sources
 build on x86_64 and aarch64.
 """
@@ -24,6 +26,7 @@ LIBDIR = PKG / "_lib"
 
 SPLITK_LIB = LIBDIR / "libsplitk_sm103a.so"
 SYNTHETIC_LIB = LIBDIR / "libsynthetic.so"
+OPERATORS_LIB = LIBDIR / "_operators.so"
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -101,6 +104,29 @@ def build_splitk(force: bool = False, verbose_ptxas: bool = False) -> Path:
     return SPLITK_LIB
 
 
+def build_operators(force: bool = False) -> Path:
+    LIBDIR.mkdir(parents=True, exist_ok=True)
+    src = CSRC / "operators_binding.cpp"
+    if not (force or _stale(OPERATORS_LIB, [src, INCLUDE / "splitk.h"])):
+        return OPERATORS_LIB
+    import sysconfig
+
+    import torch
+    home = Path(torch.__file__).resolve().parent
+    cuda = Path(_nvcc()).resolve().parent.parent
+    includes = [INCLUDE, sysconfig.get_paths()["include"], home / "include",
+                home / "include" / "torch" / "csrc" / "api" / "include", cuda / "include"]
+    tmp = OPERATORS_LIB.with_suffix(f".{os.getpid()}.tmp")
+    _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[x for i in includes for x in ("-isystem" if str(i).startswith(str(home)) else "-I", str(i))],
+          str(src), "-o", str(tmp), f"-L{LIBDIR}", f"-l:{SPLITK_LIB.name}", f"-L{home / 'lib'}",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, OPERATORS_LIB)
+    return OPERATORS_LIB
+
+
 def build_all(force: bool = False) -> None:
     build_synthetic(force)
     build_splitk(force)
+    build_operators(force)

@@ -18,6 +18,7 @@ P = 0x10000          # an aligned address that is never read: every call here is
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     _build.build_splitk()
+    _build.build_operators()
 
 
 def rmsnorm(x=P, stride=64, r=None, r_out=None, r_type=0, w=P, w_type=0, eps=1e-6, q=P, s=P, M=2, D=64):
