@@ -371,6 +371,43 @@ __device__ __forceinline__ uint32_t draw_groups(uint32_t* best, int n, int k, in
   return last;
 }
 
+// Which of a lane's eight logits of group `g` (bit j) are not equal to `value`, or
+// among the group's first k that are.  (Out of line: rare, and reads them again.)
+template <int kType>
+__device__ __noinline__ uint32_t first_equal(Row<kType> row, int g, int lane, float value, int k) {
+  float f[8];
+  row.load_group(g, lane, f);
+  constexpr int kRun = Logit<kType>::kPerLoad;     // consecutive logits of a lane
+  uint32_t in = 0xFFu;
+  int before = 0;                                  // equal ones of the runs before
+#pragma unroll
+  for (int h = 0; h < 8; h += kRun) {
+    uint32_t equal = 0;
+#pragma unroll
+    for (int j = h; j < h + kRun; ++j) {
+      const int id = Row<kType>::at(g, lane, j) - row.shift;
+      if (f[j] == value && id >= 0 && id < row.V) equal |= 1u << j;
+    }
+    int rank = __popc(equal);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(kFull, rank, o);
+      rank += lane >= o ? below : 0;
+    }
+    const int all = __shfl_sync(kFull, rank, 31);
+    rank += before - __popc(equal);
+#pragma unroll
+    for (int j = h; j < h + kRun; ++j) {
+      if (equal >> j & 1u) {
+        if (rank >= k) in &= ~(1u << j);
+        ++rank;
+      }
+    }
+    before += all;
+  }
+  return in;
+}
+
 // A lower bound on the k-th largest logit: the k-th largest of 32 of the lanes'
 // values (logits of the row, all different ones), each warp's largest; 0 if
 // there are not that many.  CTA-wide; `some` holds 32 words.
@@ -542,7 +579,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   }
   __syncthreads();
   int groups = s_groups;
-  if (groups > kMaxGroups) {
+  const bool drawn = groups > kMaxGroups;
+  if (drawn) {
     groups = min(p.k, n);
     if (warp == 0) {
       const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
@@ -552,18 +590,27 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     __syncthreads();
     bound = s_some[0];
   }
-  // their logits that reach the bound (0: all)
+  // their logits that reach the bound (0: all); of many equal to it (a masked
+  // row) each group's first k
   const float least = bound == 0 ? -INFINITY : value_of(bound);
+  const auto add = [&](float v, int id) {
+    if (!(v < least) && id >= 0 && id < p.V) {
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kMaxCandidates) s_cand[at] = key_of(order_of(v), id);
+    }
+  };
   for (int i = warp; i < groups; i += kWarps) {
     float f[8];
     row.load_group(s_sel[i], lane, f);
+    if (drawn) {
+      const uint32_t in = first_equal<kType>(row, s_sel[i], lane, least, p.k);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int id = Row<kType>::at(s_sel[i], lane, j) - row.shift;
-      if (!(f[j] < least) && id >= 0 && id < p.V) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kMaxCandidates) s_cand[at] = key_of(order_of(f[j]), id);
+      for (int j = 0; j < 8; ++j) {
+        if (in >> j & 1u) add(f[j], Row<kType>::at(s_sel[i], lane, j) - row.shift);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) add(f[j], Row<kType>::at(s_sel[i], lane, j) - row.shift);
     }
   }
   __syncthreads();
@@ -584,9 +631,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     }
     return;
   }
-  // More (a short row, many equal logits, a mask that leaves fewer than k): one
-  // alternative after another, from the list, or where that did not hold them
-  // from the groups again.
+  // More (a short row, a sorted one, many equal logits): one alternative after
+  // another, from the list, or where that did not hold them from the groups again.
   uint64_t last = ~0ull;
   for (int r = 0; r < p.k; ++r) {
     uint64_t best = 0;
