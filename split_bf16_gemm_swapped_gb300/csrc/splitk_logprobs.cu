@@ -593,24 +593,20 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   // their logits that reach the bound (0: all); of many equal to it (a masked
   // row) each group's first k
   const float least = bound == 0 ? -INFINITY : value_of(bound);
-  const auto add = [&](float v, int id) {
-    if (!(v < least) && id >= 0 && id < p.V) {
-      const int at = atomicAdd(&s_count, 1);
-      if (at < kMaxCandidates) s_cand[at] = key_of(order_of(v), id);
-    }
-  };
   for (int i = warp; i < groups; i += kWarps) {
+    const int g = s_sel[i];
     float f[8];
-    row.load_group(s_sel[i], lane, f);
-    if (drawn) {
-      const uint32_t in = first_equal<kType>(row, s_sel[i], lane, least, p.k);
+    row.load_group(g, lane, f);
+    uint32_t in = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (in >> j & 1u) add(f[j], Row<kType>::at(s_sel[i], lane, j) - row.shift);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) add(f[j], Row<kType>::at(s_sel[i], lane, j) - row.shift);
+    for (int j = 0; j < 8; ++j) in |= f[j] < least ? 0u : 1u << j;
+    if (drawn) in &= first_equal<kType>(row, g, lane, least, p.k);
+    // a lane has hardly ever more than one, which is read again by its place
+    for (; in != 0; in &= in - 1) {
+      const int id = Row<kType>::at(g, lane, __ffs(in) - 1) - row.shift;
+      if (id < 0 || id >= p.V) continue;
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kMaxCandidates) s_cand[at] = key_of(order_of(Logit<kType>::one(row.x[id])), id);
     }
   }
   __syncthreads();
