@@ -28,6 +28,7 @@ namespace splitk {
 namespace {
 
 constexpr int kRows = 16;            // weight rows a CTA
+constexpr int kPrefetch = 1024;      // codes of a row
 constexpr int kChunk = 64;           // codes of K a warp takes at a time
 constexpr int kAhead = 2;            // chunks whose loads a warp has in flight at once
 
@@ -47,10 +48,17 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps / 8) i8_stream_kernel(cons
   constexpr int kTiles = kTok / 8;
   __shared__ float s_part[kWarps][kRows][kTok + 1];
   dev::griddep_launch_dependents();
-  dev::griddep_wait();
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int n0 = (int)blockIdx.x * kRows, m0 = (int)blockIdx.y * kTok, l = (int)blockIdx.z;
+  // While the work ahead in the stream completes, the rows' first codes come to
+  // L2 (which is where a kernel's writes would change them: nothing is read early).
+  // (1 x 7168 x 2048: 5.1 us without, 4.6; whole rows of 7168: slower again, they
+  // displace what other CTAs are loading.)
+  if ((int)threadIdx.x < kRows && n0 + (int)threadIdx.x < p.N && blockIdx.y == 0) {
+    dev::prefetch_l2(p.a + ((long long)l * p.N + n0 + (int)threadIdx.x) * p.K, (uint32_t)min(p.K, kPrefetch));
+  }
+  dev::griddep_wait();
   // Rows and tokens past the end read the last one instead (their sums are not
   // stored), and the last chunk's lanes past K read in front of it and count
   // as zeros: no load hangs on a branch.

@@ -198,6 +198,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   dev::tc_fence_after();
   // The next kernel may come once this CTA holds its tensor memory.
   dev::griddep_launch_dependents();
+  // While the work ahead in the stream completes, the ring's first weight tiles
+  // come to L2 (which is where a kernel's writes would change them: nothing is
+  // read early).
+  if (warp == 0 && lane < min(stages, k_tiles)) dev::tma_prefetch_3d(&a_map, (kt0 + lane) * kCtaK, n0, l);
   dev::griddep_wait();
   const uint32_t tmem = dev::ld_shared_u32(slot_tmem);
 
