@@ -371,41 +371,43 @@ __device__ __forceinline__ uint32_t draw_groups(uint32_t* best, int n, int k, in
   return last;
 }
 
-// Which of a lane's eight logits of group `g` (bit j) are not equal to `value`, or
-// among the group's first k that are.  (Out of line: rare, and reads them again.)
+// One warp: the first `need` logits of the row that equal `value`, as keys into
+// `cand`; `best` holds the groups' maxima, `bound` the value's order.
 template <int kType>
-__device__ __noinline__ uint32_t first_equal(Row<kType> row, int g, int lane, float value, int k) {
-  float f[8];
-  row.load_group(g, lane, f);
+__device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, int n, uint32_t bound, float value,
+                                         int lane, int need, uint64_t* cand) {
   constexpr int kRun = Logit<kType>::kPerLoad;     // consecutive logits of a lane
-  uint32_t in = 0xFFu;
-  int before = 0;                                  // equal ones of the runs before
+  for (int g0 = 0; g0 < n; g0 += 32) {
+    uint32_t there = __ballot_sync(kFull, g0 + lane < n && best[min(g0 + lane, n - 1)] >= bound);
+    for (; there != 0; there &= there - 1) {
+      const int g = g0 + __ffs(there) - 1;
+      float f[8];
+      row.load_group(g, lane, f);
 #pragma unroll
-  for (int h = 0; h < 8; h += kRun) {
-    uint32_t equal = 0;
+      for (int h = 0; h < 8; h += kRun) {
+        uint32_t equal = 0;
 #pragma unroll
-    for (int j = h; j < h + kRun; ++j) {
-      const int id = Row<kType>::at(g, lane, j) - row.shift;
-      if (f[j] == value && id >= 0 && id < row.V) equal |= 1u << j;
-    }
-    int rank = __popc(equal);
+        for (int j = h; j < h + kRun; ++j) {
+          const int id = Row<kType>::at(g, lane, j) - row.shift;
+          if (f[j] == value && id >= 0 && id < row.V) equal |= 1u << j;
+        }
+        int rank = __popc(equal);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int below = __shfl_up_sync(kFull, rank, o);
-      rank += lane >= o ? below : 0;
-    }
-    const int all = __shfl_sync(kFull, rank, 31);
-    rank += before - __popc(equal);
-#pragma unroll
-    for (int j = h; j < h + kRun; ++j) {
-      if (equal >> j & 1u) {
-        if (rank >= k) in &= ~(1u << j);
-        ++rank;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(kFull, rank, o);
+          rank += lane >= o ? below : 0;
+        }
+        const int all = __shfl_sync(kFull, rank, 31);
+        rank -= __popc(equal);
+        for (; equal != 0 && rank < need; equal &= equal - 1, ++rank) {
+          cand[rank] = key_of(bound, Row<kType>::at(g, lane, __ffs(equal) - 1) - row.shift);
+        }
+        if (all >= need) return;
+        need -= all;
+        cand += all;
       }
     }
-    before += all;
   }
-  return in;
 }
 
 // A lower bound on the k-th largest logit: the k-th largest of 32 of the lanes'
@@ -561,58 +563,75 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   }
   if (p.k == 0) return;
 
-  // The groups to read again: those whose maximum reaches a bound that at
-  // least k of them reach; where too many do (equal maxima), the k best.
-  // The bound is of the lanes' largest logits, or, where other CTAs read a part
-  // of the row, of the groups'.
+  // The groups to read again: those whose maximum reaches a bound that at least k
+  // logits reach, and their logits that do.  Where that is many (equal ones: a mask
+  // that leaves fewer than k, say), those above the bound alone, and the row's
+  // first ones equal to it; where even those groups are many, the k best groups.
+  // The bound is of the lanes' largest logits, or, where other CTAs read a part of
+  // the row, of the groups'.
   uint32_t mine = order_of(lane_top);
   if (split > 1) {
     mine = 0;
     for (int g = n * warp / kWarps + lane; g < n * (warp + 1) / kWarps; g += 32) mine = max(mine, s_best[g]);
   }
   uint32_t bound = bound_top<kWarps>(mine, p.k, warp, lane, s_some);
-  for (int g = (int)threadIdx.x; g < n; g += 32 * kWarps) {
-    if (s_best[g] >= bound) {
-      const int at = atomicAdd(&s_groups, 1);
-      if (at < kMaxGroups) s_sel[at] = g;
-    }
-  }
-  __syncthreads();
-  int groups = s_groups;
-  const bool drawn = groups > kMaxGroups;
-  if (drawn) {
-    groups = min(p.k, n);
-    if (warp == 0) {
-      const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
-      // fewer groups than alternatives: all of them, and every logit in them
-      if (lane == 0) s_some[0] = n <= p.k ? 0u : last;
+  const auto reaching = [&](uint32_t least_order) {
+    for (int g = (int)threadIdx.x; g < n; g += 32 * kWarps) {
+      if (s_best[g] >= least_order) {
+        const int at = atomicAdd(&s_groups, 1);
+        if (at < kMaxGroups) s_sel[at] = g;
+      }
     }
     __syncthreads();
-    bound = s_some[0];
-  }
-  // their logits that reach the bound (0: all); of many equal to it (a masked
-  // row) each group's first k
-  const float least = bound == 0 ? -INFINITY : value_of(bound);
-  for (int i = warp; i < groups; i += kWarps) {
-    const int g = s_sel[i];
-    float f[8];
-    row.load_group(g, lane, f);
-    uint32_t in = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) in |= f[j] < least ? 0u : 1u << j;
-    if (drawn) in &= first_equal<kType>(row, g, lane, least, p.k);
-    // a lane has hardly ever more than one, which is read again by its place
-    for (; in != 0; in &= in - 1) {
-      const int id = Row<kType>::at(g, lane, __ffs(in) - 1) - row.shift;
-      if (id < 0 || id >= p.V) continue;
-      const int at = atomicAdd(&s_count, 1);
-      if (at < kMaxCandidates) s_cand[at] = key_of(order_of(Logit<kType>::one(row.x[id])), id);
+    return s_groups;
+  };
+  int groups = reaching(bound), count;
+  float least = value_of(bound);
+  bool strict = false;
+  const bool ordered = bound <= order_of(INFINITY);          // a NaN equals nothing
+  for (bool again = groups > kMaxGroups;; again = true) {
+    if (again) {
+      __syncthreads();
+      if (threadIdx.x == 0) s_groups = s_count = 0;
+      __syncthreads();
+      groups = reaching(bound + 1);
+      strict = ordered && groups <= kMaxGroups;
+      if (!strict) {
+        groups = min(p.k, n);
+        if (warp == 0) {
+          const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
+          if (lane == 0) s_some[0] = last;
+        }
+        __syncthreads();
+        least = value_of(s_some[0]);
+      }
     }
+    for (int i = warp; i < groups; i += kWarps) {
+      const int g = s_sel[i];
+      float f[8];
+      row.load_group(g, lane, f);
+      uint32_t in = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) in |= f[j] < least || (strict && f[j] == least) ? 0u : 1u << j;
+      // a lane has hardly ever more than one, which is read again by its place
+      for (; in != 0; in &= in - 1) {
+        const int id = Row<kType>::at(g, lane, __ffs(in) - 1) - row.shift;
+        if (id < 0 || id >= p.V) continue;
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kMaxCandidates) s_cand[at] = key_of(order_of(Logit<kType>::one(row.x[id])), id);
+      }
+    }
+    __syncthreads();
+    count = s_count;
+    if (again || count <= kFewCandidates || !ordered) break;
   }
-  __syncthreads();
+  if (strict && count < p.k) {
+    if (warp == 0) first_equal<kType>(row, s_best, n, bound, least, lane, p.k - count, s_cand + count);
+    count = p.k;
+    __syncthreads();
+  }
   // Their order is by (logit, lowest index), each one's place in it the
   // number before it, so how they came into the list does not matter.
-  const int count = s_count;
   long long* ids = p.top_ids + (long long)row_index * p.k;
   float* tops = p.top_logprobs + (long long)row_index * p.k;
   if (count <= kFewCandidates) {

@@ -422,6 +422,39 @@ def test_logprobs_masks_of_the_lowest_value(dtype):
     check_logprobs(x, torch.tensor([3, 8995, 0, 0], device=DEV), 12)
 
 
+@pytest.mark.parametrize("M", [1, 160])
+@pytest.mark.parametrize("V", [300, 20011, 131072])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_of_rows_with_few_kept_logits(dtype, V, M):
+    """About as many logits as alternatives are kept, anywhere in the row: the
+    masked ones of the lowest index follow them."""
+    g = gen(V + M)
+    for low in (float("-inf"), torch.finfo(dtype).min):
+        for keep in (1, 19, 20, 21, 140):
+            x = torch.full((M, V), low, dtype=dtype, device=DEV)
+            at = torch.rand((M, V), device=DEV, generator=g).argsort(dim=1)[:, :keep]
+            x.scatter_(1, at, randn((M, keep), g, dtype, 3.0))
+            check_logprobs(x, at[:, 0].contiguous(), 20)
+
+
+@pytest.mark.parametrize("levels", [2, 3, 40])
+@pytest.mark.parametrize("V", [300, 20011, 131072])
+def test_logprobs_of_rows_with_few_values(V, levels):
+    g = gen(V + levels)
+    for kept in (0.0, 0.001, 0.5):
+        x = torch.randint(1, levels, (5, V), device=DEV, generator=g).to(BF16)
+        x *= torch.rand((5, V), device=DEV, generator=g) < kept
+        check_logprobs(x, torch.zeros(5, dtype=torch.int64, device=DEV), 32)
+
+
+def test_logprobs_of_rows_of_nan_alone():
+    for M, V in ((1, 131072), (1, 500), (200, 40000)):
+        x = torch.full((M, V), float("nan"), dtype=BF16, device=DEV)
+        logprob, entropy, ids, tops = sk.splitk_logprobs(x, torch.zeros(M, dtype=torch.int64, device=DEV), top_k=20)
+        assert torch.isnan(logprob).all() and torch.isnan(entropy).all() and torch.isnan(tops).all()
+        assert (ids >= 0).all() and (ids < V).all()
+
+
 def test_logprobs_of_rows_with_nan_and_infinity():
     g = gen(10)
     x = randn((4, 3000), g, F32)
