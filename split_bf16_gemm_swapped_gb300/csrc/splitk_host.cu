@@ -822,7 +822,7 @@ struct DeviceState {
   int used = 0;
   std::unordered_map<AKey, int, AKeyHash> a_slots;
   std::unordered_map<BKey, CUtensorMap, BKeyHash> b_maps;
-  int i8_clusters[4] = {};         // see DeviceSize
+  int i8_clusters[4] = {}, row_clusters[3] = {};           // see DeviceSize
   int max_clusters[9] = {};        // persistent kernel: clusters of 2, 4, 8 resident at once (0: unknown)
 };
 
@@ -853,7 +853,7 @@ int current_device(DeviceState** out, int* dev_out) {
     if (major != 10 || minor != 3) return SPLITK_ERR_UNSUPPORTED_DEVICE;
     if (!encode_fn()) return SPLITK_ERR_CUDA;
     if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess ||
-        prepare_logprobs() != cudaSuccess || prepare_i8_tile(optin, st.i8_clusters) != cudaSuccess) {
+        prepare_logprobs(st.row_clusters) != cudaSuccess || prepare_i8_tile(optin, st.i8_clusters) != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
@@ -1214,7 +1214,8 @@ int require_device(DeviceSize* out) {
   const int rc = current_device(&st, nullptr);
   if (rc == SPLITK_OK && out) {
     *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin,
-                      {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2], st->i8_clusters[3]}};
+                      {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2], st->i8_clusters[3]},
+                      {st->row_clusters[0], st->row_clusters[1], st->row_clusters[2]}};
   }
   return rc;
 }

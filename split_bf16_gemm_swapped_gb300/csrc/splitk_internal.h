@@ -171,6 +171,7 @@ struct DeviceSize {
   size_t smem_per_sm;
   size_t smem_optin;
   int i8_clusters[4];         // clusters of 1, 2, 3 and 4 CTA pairs of the 8-bit product resident at once
+  int row_clusters[3];        // clusters of 2, 4 and 8 CTAs of the log probabilities resident at once
 };
 int require_device(DeviceSize* out);
 
@@ -182,7 +183,7 @@ unsigned long long wait_limit_ns();
 unsigned injected();
 
 // Defined in splitk_logprobs.cu.
-cudaError_t prepare_logprobs();
+cudaError_t prepare_logprobs(int (&clusters)[3]);
 
 // Defined in splitk_i8_tile.cu.
 cudaError_t prepare_i8_tile(int max_dynamic_smem, int (&clusters)[4]);

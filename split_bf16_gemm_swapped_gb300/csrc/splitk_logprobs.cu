@@ -410,11 +410,11 @@ __device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, i
   }
 }
 
-// A lower bound on the k-th largest logit: the k-th largest of 32 of the lanes'
-// values (logits of the row, all different ones), each warp's largest; 0 if
-// there are not that many.  CTA-wide; `some` holds 32 words.
+// A lower bound on the k-th largest logit is the k-th largest of 32 of the lanes'
+// values (logits of the row, all different ones), each warp's largest; 0 if there
+// are not that many.  First each warp puts its own into `some` ...
 template <int kWarps>
-__device__ __forceinline__ uint32_t bound_top(uint32_t value, int k, int warp, int lane, uint32_t* some) {
+__device__ __forceinline__ void top_lanes(uint32_t value, int warp, int lane, uint32_t* some) {
 #pragma unroll
   for (int i = 0; i < 32 / kWarps; ++i) {
     const uint32_t top = __reduce_max_sync(kFull, value);
@@ -424,20 +424,18 @@ __device__ __forceinline__ uint32_t bound_top(uint32_t value, int k, int warp, i
       value = 0;
     }
   }
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t v = some[lane];
-    int before = 0;
+}
+// ... and then one warp finds the k-th, to some[0].
+__device__ __forceinline__ void kth_largest(int k, int lane, uint32_t* some) {
+  const uint32_t v = some[lane];
+  int before = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t w = __shfl_sync(kFull, v, i);
-      before += w > v || (w == v && i < lane) ? 1 : 0;
-    }
-    __syncwarp();
-    if (before == k - 1) some[0] = v;
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t w = __shfl_sync(kFull, v, i);
+    before += w > v || (w == v && i < lane) ? 1 : 0;
   }
-  __syncthreads();
-  return some[0];
+  __syncwarp();
+  if (before == k - 1) some[0] = v;
 }
 
 // kWarps: 16, 8 or 4 warps a CTA, 32 an SM (64 registers a thread).
@@ -514,132 +512,153 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   a.t = warp_sum(a.t);
   if (lane == 0) s_warp[warp] = a;
   if (threadIdx.x == 0) s_groups = s_count = 0;
+  const bool some = p.k > 0;
+  if (some && split == 1) top_lanes<kWarps>(order_of(lane_top), warp, lane, s_some);
   __syncthreads();
-  const Sums none{-INFINITY, 0.0f, 0.0f};
-  if (warp == 0) {
-    const Sums all = join(lane < kWarps ? s_warp[lane] : none);
-    if (lane == 0) s_cta = all;
-  }
+  // One warp joins the sums, and another looks for the bound meanwhile.
+  constexpr int kJoins = kWarps - 1;
+  Sums part{-INFINITY, 0.0f, 0.0f};
+  if (warp == kJoins && lane < kWarps) part = s_warp[lane];
   if (split > 1) {
     // the first CTA takes the others' sums and maxima from their shared memory
-    __syncwarp();
-    dev::cluster_arrive_release();
-    dev::cluster_wait_acquire();
-    if (rank == 0) {
-      if (warp == 0) {
-        Sums part = none;
-        if (lane < split) {
-          const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), (uint32_t)lane);
-          part = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
-        }
-        part = join(part);
-        if (lane == 0) s_cta = part;
-      }
-      if (p.k > 0) {
-        for (int g = g1 + (int)threadIdx.x; g < n; g += 32 * kWarps) {
-          // the rank whose run of groups holds g
-          const int r = (int)(((long long)(g + 1) * split - 1) / n);
-          s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
-        }
-      }
+    if (warp == kJoins) {
+      part = join(part);
+      if (lane == 0) s_cta = part;
+      __syncwarp();
     }
-    __syncwarp();
     dev::cluster_arrive_release();
     dev::cluster_wait_acquire();
-    if (rank != 0) return;
+    if (rank != 0) {
+      dev::cluster_arrive_release();
+      dev::cluster_wait_acquire();
+      return;
+    }
+    if (warp == kJoins) {
+      part = Sums{-INFINITY, 0.0f, 0.0f};
+      if (lane < split) {
+        const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), (uint32_t)lane);
+        part = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
+      }
+      __syncwarp();
+    }
+    if (some) {
+      for (int g = g1 + (int)threadIdx.x; g < n; g += 32 * kWarps) {
+        // the rank whose run of groups holds g
+        const int r = (int)(((long long)(g + 1) * split - 1) / n);
+        s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
+      }
+      __syncthreads();
+      // where other CTAs read a part of the row, the bound is of the groups' maxima
+      uint32_t mine = 0;
+      for (int g = n * warp / kWarps + lane; g < n * (warp + 1) / kWarps; g += 32) mine = max(mine, s_best[g]);
+      top_lanes<kWarps>(mine, warp, lane, s_some);
+    }
+    dev::cluster_arrive_release();
+    __syncthreads();
   }
+  if (warp == kJoins) {
+    part = join(part);
+    if (lane == 0) s_cta = part;
+  }
+  if (some && warp == 0) kth_largest(p.k, lane, s_some);
   __syncthreads();
+  if (split > 1) dev::cluster_wait_acquire();
+  const bool writes = (int)threadIdx.x == 32 * kJoins;       // the row's own results
+  long long token = -1;
+  if (writes && p.tokens != nullptr) token = p.tokens[row_index];
+
+  int groups = 0, count = 0;
+  if (some) {
+    // The groups to read again: those whose maximum reaches the bound, and their
+    // logits that do.  Where that is many (equal ones: a mask that leaves fewer
+    // than k, say), those above the bound alone, and the row's first ones equal to
+    // it; where even those groups are many, the k best groups.
+    const uint32_t bound = s_some[0];
+    const auto reaching = [&](uint32_t least_order) {
+      for (int g = (int)threadIdx.x; g < n; g += 32 * kWarps) {
+        if (s_best[g] >= least_order) {
+          const int at = atomicAdd(&s_groups, 1);
+          if (at < kMaxGroups) s_sel[at] = g;
+        }
+      }
+      __syncthreads();
+      return s_groups;
+    };
+    groups = reaching(bound);
+    float least = value_of(bound);
+    bool strict = false;
+    const bool ordered = bound < order_of(INFINITY);         // a finite logit is above it, and it is no NaN
+    for (bool again = groups > kMaxGroups;; again = true) {
+      if (again) {
+        __syncthreads();
+        if (threadIdx.x == 0) s_groups = s_count = 0;
+        __syncthreads();
+        groups = reaching(bound + 1);
+        strict = ordered && groups <= kMaxGroups;
+        least = value_of(bound + 1);
+        if (!strict) {
+          groups = min(p.k, n);
+          if (warp == 0) {
+            const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
+            if (lane == 0) s_some[0] = last;
+          }
+          __syncthreads();
+          least = value_of(s_some[0]);
+        }
+      }
+      for (int i = warp; i < groups; i += kWarps) {
+        const int g = s_sel[i];
+        float f[8];
+        row.load_group(g, lane, f);
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) in |= f[j] < least ? 0u : 1u << j;
+        // a lane has hardly ever more than one, which is read again by its place
+        for (; in != 0; in &= in - 1) {
+          const int id = Row<kType>::at(g, lane, __ffs(in) - 1) - row.shift;
+          if (id < 0 || id >= p.V) continue;
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kMaxCandidates) s_cand[at] = key_of(order_of(Logit<kType>::one(row.x[id])), id);
+        }
+      }
+      __syncthreads();
+      count = s_count;
+      if (again || count <= kFewCandidates || !ordered) break;
+    }
+    if (strict && count < p.k) {
+      if (warp == 0) first_equal<kType>(row, s_best, n, bound, value_of(bound), lane, p.k - count, s_cand + count);
+      count = p.k;
+      __syncthreads();
+    }
+  }
+
   const Sums all = s_cta;
   // a row whose every logit is masked: no probabilities (log 0), entropy 0
   const float log_s = all.s == 0.0f ? 0.0f : logf(all.s);
   const float base = all.m == -INFINITY && all.s == 0.0f ? 0.0f : all.m;
-  if (threadIdx.x == 0) {
+  if (writes) {
     p.entropy[row_index] = all.s == 0.0f ? 0.0f : log_s - kLn2 * (all.t / all.s);
     if (p.tokens != nullptr) {
-      const long long t = p.tokens[row_index];
-      p.logprob[row_index] =
-          t >= 0 && t < (long long)p.V ? (Logit<kType>::one(row.x[t]) - base) - log_s : __uint_as_float(0x7FC00000u);
+      p.logprob[row_index] = token >= 0 && token < (long long)p.V ? (Logit<kType>::one(row.x[token]) - base) - log_s
+                                                                  : __uint_as_float(0x7FC00000u);
     }
   }
-  if (p.k == 0) return;
+  if (!some) return;
 
-  // The groups to read again: those whose maximum reaches a bound that at least k
-  // logits reach, and their logits that do.  Where that is many (equal ones: a mask
-  // that leaves fewer than k, say), those above the bound alone, and the row's
-  // first ones equal to it; where even those groups are many, the k best groups.
-  // The bound is of the lanes' largest logits, or, where other CTAs read a part of
-  // the row, of the groups'.
-  uint32_t mine = order_of(lane_top);
-  if (split > 1) {
-    mine = 0;
-    for (int g = n * warp / kWarps + lane; g < n * (warp + 1) / kWarps; g += 32) mine = max(mine, s_best[g]);
-  }
-  uint32_t bound = bound_top<kWarps>(mine, p.k, warp, lane, s_some);
-  const auto reaching = [&](uint32_t least_order) {
-    for (int g = (int)threadIdx.x; g < n; g += 32 * kWarps) {
-      if (s_best[g] >= least_order) {
-        const int at = atomicAdd(&s_groups, 1);
-        if (at < kMaxGroups) s_sel[at] = g;
-      }
-    }
-    __syncthreads();
-    return s_groups;
-  };
-  int groups = reaching(bound), count;
-  float least = value_of(bound);
-  bool strict = false;
-  const bool ordered = bound <= order_of(INFINITY);          // a NaN equals nothing
-  for (bool again = groups > kMaxGroups;; again = true) {
-    if (again) {
-      __syncthreads();
-      if (threadIdx.x == 0) s_groups = s_count = 0;
-      __syncthreads();
-      groups = reaching(bound + 1);
-      strict = ordered && groups <= kMaxGroups;
-      if (!strict) {
-        groups = min(p.k, n);
-        if (warp == 0) {
-          const uint32_t last = draw_groups(s_best, n, groups, lane, s_sel);
-          if (lane == 0) s_some[0] = last;
-        }
-        __syncthreads();
-        least = value_of(s_some[0]);
-      }
-    }
-    for (int i = warp; i < groups; i += kWarps) {
-      const int g = s_sel[i];
-      float f[8];
-      row.load_group(g, lane, f);
-      uint32_t in = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) in |= f[j] < least || (strict && f[j] == least) ? 0u : 1u << j;
-      // a lane has hardly ever more than one, which is read again by its place
-      for (; in != 0; in &= in - 1) {
-        const int id = Row<kType>::at(g, lane, __ffs(in) - 1) - row.shift;
-        if (id < 0 || id >= p.V) continue;
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kMaxCandidates) s_cand[at] = key_of(order_of(Logit<kType>::one(row.x[id])), id);
-      }
-    }
-    __syncthreads();
-    count = s_count;
-    if (again || count <= kFewCandidates || !ordered) break;
-  }
-  if (strict && count < p.k) {
-    if (warp == 0) first_equal<kType>(row, s_best, n, bound, least, lane, p.k - count, s_cand + count);
-    count = p.k;
-    __syncthreads();
-  }
   // Their order is by (logit, lowest index), each one's place in it the
   // number before it, so how they came into the list does not matter.
   long long* ids = p.top_ids + (long long)row_index * p.k;
   float* tops = p.top_logprobs + (long long)row_index * p.k;
   if (count <= kFewCandidates) {
-    for (int c = (int)threadIdx.x; c < count; c += 32 * kWarps) {
-      const uint64_t key = s_cand[c];
+    // four lanes count for one
+    for (int c0 = 8 * warp; c0 < count; c0 += 8 * kWarps) {
+      const int c = c0 + (lane >> 2);
+      const uint64_t key = s_cand[min(c, count - 1)];
       int before = 0;
-      for (int i = 0; i < count; ++i) before += s_cand[i] > key ? 1 : 0;
-      if (before < p.k) {
+      for (int i = lane & 3; i < count; i += 4) before += s_cand[i] > key ? 1 : 0;
+      before += __shfl_xor_sync(kFull, before, 1);
+      before += __shfl_xor_sync(kFull, before, 2);
+      if ((lane & 3) == 0 && c < count && before < p.k) {
         ids[before] = id_of(key);
         tops[before] = (value_of((uint32_t)(key >> 32)) - base) - log_s;
       }
@@ -702,7 +721,7 @@ inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 
 
 }  // namespace
 
-cudaError_t prepare_logprobs() {
+cudaError_t prepare_logprobs(int (&clusters)[3]) {
   const int most = (int)logprob_smem(kMaxVocab);
   cudaError_t e = cudaSuccess;
   const auto set = [&](auto* kernel) {
@@ -711,6 +730,19 @@ cudaError_t prepare_logprobs() {
   set(logprobs_kernel<1, 4>), set(logprobs_kernel<2, 4>), set(logprobs_kernel<3, 4>);
   set(logprobs_kernel<1, 8>), set(logprobs_kernel<2, 8>), set(logprobs_kernel<3, 8>);
   set(logprobs_kernel<1, 16>), set(logprobs_kernel<2, 16>), set(logprobs_kernel<3, 16>);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2u << i;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2u << i);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = (size_t)most;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters[i], logprobs_kernel<2, 16>, &cfg);
+  }
   return e;
 }
 
@@ -738,10 +770,11 @@ SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long st
   int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
-  // CTAs sharing a row: as many as two CTAs an SM leave, with 16 groups (one
-  // a warp) for each at least.
+  // CTAs sharing a row: as many as leave each row's cluster a place at once (38 x
+  // 131072 bf16, top 20: 10.1 us in clusters of four, 12.7 of eight, which do not all
+  // fit; 24 rows: 8.9 and 8.4), with 16 groups (one a warp) for each at least.
   int split = 1;
-  while (split < 8 && (long long)M * split * 2 <= 2ll * dev.num_sms && V / (split * 2) >= 16 * kGroup) split *= 2;
+  for (int i = 0; i < 3 && M <= dev.row_clusters[i] && V >= (2 << i) * 16 * kGroup; ++i) split = 2 << i;
   // Smaller CTAs where there are rows enough for them, so that more rows are at
   // their different stages at once (1024 x 131072 bf16, top 20: 52 us with eight
   // warps, 55 with sixteen, 61 with four; 4096 x 32000: 72, 103, 64; 400 x 131072:
