@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   __shared__ Sums s_cta;
   __shared__ int s_sel[kMaxGroups];
   __shared__ uint32_t s_some[32];
-  __shared__ int s_groups, s_count;
-  __shared__ uint64_t s_cand[kMaxCandidates], s_round[2][kWarps];
+  __shared__ int s_groups, s_count, s_few_count;
+  __shared__ uint64_t s_cand[kMaxCandidates], s_few[kFewCandidates], s_round[2][kWarps];
   dev::griddep_launch_dependents();
   dev::griddep_wait();
 
@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   if (writes && p.tokens != nullptr) token = p.tokens[row_index];
 
   int groups = 0, count = 0;
+  const uint64_t* list = s_cand;
   if (some) {
     // The groups to read again: those whose maximum reaches the bound, and their
     // logits that do.  Where that is many (equal ones: a mask that leaves fewer
@@ -623,6 +624,27 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
       }
       __syncthreads();
       count = s_count;
+      if (count > kFewCandidates && count <= kMaxCandidates) {
+        // The same again for the list (a short row's lanes have few logits, so its
+        // bound is low): its parts' largest give a closer bound.
+        uint32_t top = 0;
+        for (int c = kWarps * lane + warp; c < count; c += 32 * kWarps) top = max(top, (uint32_t)(s_cand[c] >> 32));
+        top_lanes<kWarps>(top, warp, lane, s_some);
+        __syncthreads();
+        if (warp == 0) kth_largest(p.k, lane, s_some);
+        if (threadIdx.x == 32) s_few_count = 0;
+        __syncthreads();
+        const uint32_t closer = s_some[0];
+        for (int c = (int)threadIdx.x; c < count; c += 32 * kWarps) {
+          const uint64_t key = s_cand[c];
+          if ((uint32_t)(key >> 32) >= closer) {
+            const int at = atomicAdd(&s_few_count, 1);
+            if (at < kFewCandidates) s_few[at] = key;
+          }
+        }
+        __syncthreads();
+        if (s_few_count <= kFewCandidates) count = s_few_count, list = s_few;
+      }
       if (again || count <= kFewCandidates || !ordered) break;
     }
     if (strict && count < p.k) {
@@ -653,9 +675,9 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     // four lanes count for one
     for (int c0 = 8 * warp; c0 < count; c0 += 8 * kWarps) {
       const int c = c0 + (lane >> 2);
-      const uint64_t key = s_cand[min(c, count - 1)];
+      const uint64_t key = list[min(c, count - 1)];
       int before = 0;
-      for (int i = lane & 3; i < count; i += 4) before += s_cand[i] > key ? 1 : 0;
+      for (int i = lane & 3; i < count; i += 4) before += list[i] > key ? 1 : 0;
       before += __shfl_xor_sync(kFull, before, 1);
       before += __shfl_xor_sync(kFull, before, 2);
       if ((lane & 3) == 0 && c < count && before < p.k) {
@@ -770,20 +792,25 @@ SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long st
   int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
-  // CTAs sharing a row: as many as leave each row's cluster a place at once (38 x
-  // 131072 bf16, top 20: 10.1 us in clusters of four, 12.7 of eight, which do not all
-  // fit; 24 rows: 8.9 and 8.4), with 16 groups (one a warp) for each at least.
+  // CTAs sharing a row of 128 KB or more (shorter ones gain less than a cluster
+  // costs: bf16, top 20, 30 x 32000 6.2 us in one CTA and 7.3 in eight, 30 x 131072
+  // 9.9 in two and 8.7 in eight): as many as leave each row's cluster a place at
+  // once (38 x 131072: 10.1 us in four, 12.7 in eight, which do not all fit).
   int split = 1;
-  for (int i = 0; i < 3 && M <= dev.row_clusters[i] && V >= (2 << i) * 16 * kGroup; ++i) split = 2 << i;
-  // Smaller CTAs where there are rows enough for them, so that more rows are at
-  // their different stages at once (1024 x 131072 bf16, top 20: 52 us with eight
-  // warps, 55 with sixteen, 61 with four; 4096 x 32000: 72, 103, 64; 400 x 131072:
-  // 32, 25, 39), and for rows that would leave many of sixteen warps without a
-  // group.
-  const int warps = split > 1                                            ? 16
-                    : V <= 32 * kGroup || (M >= 6 * dev.num_sms && V <= 65536) ? 4
-                    : M >= 4 * dev.num_sms                               ? 8
-                                                                         : 16;
+  if ((long long)V * (logits_type == SPLITK_DTYPE_F32 ? 4 : 2) >= 1ll << 17) {
+    for (int i = 0; i < 3 && M <= dev.row_clusters[i]; ++i) split = 2 << i;
+  }
+  // Few rows get large CTAs, for their latency.  Rows enough to fill the device
+  // get smaller ones, so that more rows are at their different stages at once, the
+  // more so the less there is to a row (bf16, top 20, with 4, 8 and 16 warps: 100 x
+  // 8000 6.5, 5.7 and 5.7 us; 400 x 16000 11.4, 10.4, 13.8; 1024 x 8000 12.7, 15.3,
+  // 21.0; 1024 x 65536 36, 31, 36; 4096 x 32000 65, 71, 101; 400 x 131072 39, 31, 25;
+  // 1024 x 131072 61, 52, 55).  A warp has a group at least, or a row's bound is
+  // of too few lanes.
+  int warps = split > 1 || 2ll * M <= 3ll * dev.num_sms ? 16
+              : V > 65536                               ? (M < 4 * dev.num_sms ? 16 : 8)
+                                                        : (M < (V <= 16384 ? 4 : 12) * dev.num_sms ? 8 : 4);
+  while (warps > 4 && V + kGroup / 2 < warps * kGroup) warps /= 2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_type == SPLITK_DTYPE_BF16  ? launch_logprobs<1>(p, split, warps, s)
                         : logits_type == SPLITK_DTYPE_F32 ? launch_logprobs<2>(p, split, warps, s)

@@ -447,6 +447,15 @@ def test_logprobs_of_rows_with_few_values(V, levels):
         check_logprobs(x, torch.zeros(5, dtype=torch.int64, device=DEV), 32)
 
 
+@pytest.mark.parametrize("V", [129, 200, 640, 777, 1024, 1300, 1919, 1920, 3968, 4100])
+def test_logprobs_of_short_rows(V):
+    """Rows whose lanes have a logit or two, in few CTAs and in many."""
+    g = gen(V)
+    for M in (3, 250, 700):
+        for dtype in (BF16, F32):
+            check_logprobs(randn((M, V), g, dtype, 3.0), torch.randint(0, V, (M,), device=DEV, generator=g), 32)
+
+
 def test_logprobs_of_rows_of_nan_alone():
     for M, V in ((1, 131072), (1, 500), (200, 40000)):
         x = torch.full((M, V), float("nan"), dtype=BF16, device=DEV)
