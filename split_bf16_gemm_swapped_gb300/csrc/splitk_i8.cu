@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "splitk.h"
 #include "splitk_i8.cuh"
 #include "splitk_internal.h"
@@ -55,11 +57,17 @@ double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out
 // Whether few tokens' weights stream through registers: up to 8 always (no tile
 // is filled that far); up to 32 where that is estimated faster.  Its measured
 // rate there is 4.7 TB/s for two token fragments a warp, 2.6 for four (each weight
-// is converted once, each token fragment for every 16 weight rows).
-bool streams(int M, int N, int K, int L, double tile_time) {
+// is converted once, each token fragment for every 16 weight rows).  With four,
+// two CTAs an SM take 1 us and 1.25 for each 1024 of K (17 x 2048 x 16384: 23.1 us
+// streamed, 15.5 in tiles; 17 x 18432 x 256: 9.2 and 5.2; 17 x 2048 x 4096: 7.8
+// and 8.3).
+bool streams(int M, int N, int K, int L, double tile_time, int num_sms) {
   if (M <= 8) return true;
   if (M > 32) return false;
-  return 2.5 + (double)N * K * L / (M <= 16 ? 4.7e6 : 2.6e6) < tile_time;
+  const double codes = (double)N * K * L;
+  if (M <= 16) return 2.5 + codes / 4.7e6 < tile_time;
+  const long long rounds = ((long long)((N + 15) / 16) * L + 2 * num_sms - 1) / (2 * num_sms);
+  return std::max(2.5 + codes / 2.6e6, 2.0 + rounds * (1.0 + 1.25 * ((K + 1023) / 1024))) < tile_time;
 }
 
 }  // namespace
@@ -92,7 +100,7 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   I8Plan plan{};
   const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
-  if (streams(M, N, K, L, tile_time)) return launched(launch_i8_stream(p, dev.num_sms, s));
+  if (streams(M, N, K, L, tile_time, dev.num_sms)) return launched(launch_i8_stream(p, dev.num_sms, s));
   if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;      // no CTA pair of it fits the device
   return launched(launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
 }
