@@ -584,9 +584,10 @@ SPLITK_API int splitk_set_wait_limit_ns(uint64_t ns);
  * SPLITK_INJECT_SKIP_PUBLISH: cluster ranks other than 0 skip publishing
  * their partials, so rank 0's bounded wait for them runs out and the call
  * reports SPLITK_ERR_TIMEOUT (the output is then undefined); in
- * splitk_gemm_i8() the second CTA of a pair does not report its tiles, and the
- * first one's wait for them runs out.  No GPU fault is
- * involved: nothing is stored remotely and every wait stays bounded.
+ * splitk_gemm_i8() of more than 8 tokens, which then runs on pairs of CTAs,
+ * the second of a pair does not report its tiles, and the first one's wait for
+ * them runs out.  No GPU fault is involved: nothing is stored remotely and every
+ * wait stays bounded.
  * 0 turns injection off.
  */
 #define SPLITK_INJECT_SKIP_PUBLISH 0x1u

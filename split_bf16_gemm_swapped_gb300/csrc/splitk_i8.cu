@@ -54,20 +54,21 @@ double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out
   return best;
 }
 
-// Whether few tokens' weights stream through registers: up to 8 always (no tile
-// is filled that far); up to 32 where that is estimated faster.  Its measured
-// rate there is 4.7 TB/s for two token fragments a warp, 2.6 for four (each weight
-// is converted once, each token fragment for every 16 weight rows).  With four,
-// two CTAs an SM take 1 us and 1.25 for each 1024 of K (17 x 2048 x 16384: 23.1 us
-// streamed, 15.5 in tiles; 17 x 18432 x 256: 9.2 and 5.2; 17 x 2048 x 4096: 7.8
-// and 8.3).
+// Whether the weights stream through registers, 16 rows and up to 32 tokens a
+// CTA: up to 8 tokens always (no tile is filled that far), more where that is
+// estimated faster.  Its measured rate is 4.7 TB/s for two token fragments a
+// warp, 2.6 for four (each weight is converted once, each token fragment for every
+// 16 weight rows).  With four, two CTAs an SM take 1 us and 1.25 for each 1024 of K
+// (streamed and in tiles: 17 x 2048 x 16384 23.1 us and 15.5, 17 x 18432 x 256 9.2
+// and 5.2, 64 x 2048 x 1024 3.9 and 6.9, 256 x 500 x 4096 7.8 and 9.5).
 bool streams(int M, int N, int K, int L, double tile_time, int num_sms) {
   if (M <= 8) return true;
-  if (M > 32) return false;
   const double codes = (double)N * K * L;
   if (M <= 16) return 2.5 + codes / 4.7e6 < tile_time;
-  const long long rounds = ((long long)((N + 15) / 16) * L + 2 * num_sms - 1) / (2 * num_sms);
-  return std::max(2.5 + codes / 2.6e6, 2.0 + rounds * (1.0 + 1.25 * ((K + 1023) / 1024))) < tile_time;
+  const long long blocks = (M + 31) / 32;
+  if (blocks > 65535) return false;                    // CTAs of a launch's y dimension
+  const long long rounds = (blocks * ((N + 15) / 16) * L + 2 * num_sms - 1) / (2 * num_sms);
+  return std::max(2.5 + blocks * codes / 2.6e6, 2.0 + rounds * (1.0 + 1.25 * ((K + 1023) / 1024))) < tile_time;
 }
 
 }  // namespace
@@ -100,9 +101,13 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   I8Plan plan{};
   const double tile_time = plan_tiles(M, N, K, L, dev, &plan);
-  if (streams(M, N, K, L, tile_time, dev.num_sms)) return launched(launch_i8_stream(p, dev.num_sms, s));
+  // (an injected failure is one of tiles; a streamed product has no wait to fail)
+  const I8Waits waits{wait_limit_ns(), injected()};
+  if ((M <= 8 || waits.inject == 0) && streams(M, N, K, L, tile_time, dev.num_sms)) {
+    return launched(launch_i8_stream(p, dev.num_sms, s));
+  }
   if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;      // no CTA pair of it fits the device
-  return launched(launch_i8_tile(p, plan, I8Waits{wait_limit_ns(), injected()}, s));
+  return launched(launch_i8_tile(p, plan, waits, s));
 }
 
 }  // extern "C"

@@ -279,6 +279,23 @@ def test_nan_scales_reach_their_tokens_alone():
     assert torch.isfinite(c).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(33, 64, 64), (47, 1000, 2048), (100, 500, 256), (300, 200, 4096), (1000, 65, 1024),
+                                   (64, 2048, 2048), (700, 17, 16), (2_097_153, 1, 16)])
+def test_product_of_few_weights_and_many_tokens(M, N, K):
+    a, sa, b, sb, bias = product_inputs(1, M, N, K, M, batched=False)
+    check_product(a, sa, b, sb, bias=bias)
+    check_product(a, sa, b, sb, out=F32)
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 500, 7184), (64, 701, 7168), (65, 257, 16384), (129, 1000, 7168), (257, 300, 8208),
+                                   (12, 18433, 7168), (20, 18433, 272), (40, 18432, 80), (300, 9001, 144),
+                                   (1000, 2100, 1040), (513, 4098, 2064)])
+@pytest.mark.parametrize("L", [1, 2])
+def test_product_tiles_of_odd_sizes(M, N, K, L):
+    a, sa, b, sb, bias = product_inputs(L, M, N, K, M + N, batched=L > 1)
+    check_product(a, sa, b, sb, bias=bias if M % 2 else None)
+
+
 @pytest.mark.parametrize("M,K", [(64, 256), (40, 4096), (300, 2048)])
 def test_product_reports_a_wait_that_runs_out(M, K):
     """The pair's second CTA keeps its tiles to itself: the first one's bounded
