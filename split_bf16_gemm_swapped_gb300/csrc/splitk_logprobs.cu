@@ -231,6 +231,16 @@ struct Sums {
   }
 };
 
+// ... of a warp, a CTA or a row.  Where one logit outweighs the others, its 1
+// rounds away what little they add, and the logarithm of 1 + s wants that s: so
+// the sum without the lane that holds the largest logit is kept too, and where
+// that lane is (its logits can be summed again).
+struct Part {
+  Sums sums;
+  float rest;
+  int where;                 // CTA of the row << 16 | warp << 8 | lane
+};
+
 __device__ __forceinline__ float warp_max(float v) {
   float d;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
@@ -251,10 +261,14 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 }
 
 // One warp: the parts its lanes hold, added relative to their largest maximum.
-__device__ __forceinline__ Sums join(Sums part) {
-  part.rebase(warp_max(part.m));
-  part.s = warp_sum(part.s);
-  part.t = warp_sum(part.t);
+__device__ __forceinline__ Part join(Part part) {
+  const float top = warp_max(part.sums.m);
+  const bool largest = part.sums.m == top;
+  part.sums.rebase(top);
+  part.rest = warp_sum(largest ? part.rest : part.sums.s);
+  part.sums.s = warp_sum(part.sums.s);
+  part.sums.t = warp_sum(part.sums.t);
+  part.where = __shfl_sync(kFull, part.where, __ffs(__ballot_sync(kFull, largest)) - 1);
   return part;
 }
 
@@ -438,12 +452,53 @@ __device__ __forceinline__ void kth_largest(int k, int lane, uint32_t* some) {
   if (before == k - 1) some[0] = v;
 }
 
+// A CTA's share of a row's groups: blocks of kAhead, and what is left on either
+// side (of a short share, all of it, so that every warp has some) one at a time; its
+// warps take either in turn.
+template <int kType, int kWarps>
+struct Share {
+  int g0, g1, inner0, blocks, tail;
+  __device__ Share(const Row<kType>& row, int n, int rank, int split) {
+    constexpr int kAhead = Logit<kType>::kAhead;
+    g0 = (int)((long long)n * rank / split);
+    g1 = (int)((long long)n * (rank + 1) / split);
+    inner0 = row.shift > 0 ? max(g0, 1) : g0;
+    const int inner = min(g1, (row.shift + row.V) / kGroup) - inner0;
+    blocks = inner >= kWarps * kAhead ? inner / kAhead : 0;
+    tail = inner0 + blocks * kAhead;
+  }
+  // the i-th of the single ones: groups [g0, inner0) and [tail, g1)
+  __device__ int singles() const { return (inner0 - g0) + (g1 - tail); }
+  __device__ int single(int i) const { return i < inner0 - g0 ? g0 + i : tail + i - (inner0 - g0); }
+};
+
+// One warp: the sum of lane `owner`'s logits in the groups of warp `warp` of a share,
+// without the one that is `m`, the largest.
+template <int kType, int kWarps>
+__device__ __noinline__ float sum_beside(Row<kType> row, const Share<kType, kWarps> share, int warp, int lane,
+                                        int owner, float m) {
+  constexpr int kAhead = Logit<kType>::kAhead;
+  const int in_blocks = (share.blocks - warp + kWarps - 1) / kWarps * kAhead;
+  const int alone = (share.singles() - warp + kWarps - 1) / kWarps;
+  float s = 0.0f;
+  for (int i = lane; i < in_blocks + alone; i += 32) {
+    const int g = i < in_blocks ? share.inner0 + (warp + i / kAhead * kWarps) * kAhead + i % kAhead
+                                : share.single(warp + (i - in_blocks) * kWarps);
+    float f[8];
+    row.load_group(g, owner, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += f[j] == m ? 0.0f : exp2_approx(max_nan((f[j] - m) * kLog2e, kFarBelow));
+  }
+  return warp_sum(s);
+}
+
 // kWarps: 16, 8 or 4 warps a CTA, 32 an SM (64 registers a thread).
 template <int kType, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(const LogprobParams p, int split) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Sums s_warp[kWarps];
-  __shared__ Sums s_cta;
+  __shared__ Part s_warp[kWarps];
+  __shared__ Part s_cta;
+  __shared__ bool s_apart;
   __shared__ int s_sel[kMaxGroups];
   __shared__ uint32_t s_some[32];
   __shared__ int s_groups, s_count, s_few_count;
@@ -456,17 +511,14 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   const int row_index = (int)blockIdx.x / split;
   const Row<kType> row(p, row_index);
   const int n = row.groups();
-  const int g0 = (int)((long long)n * rank / split), g1 = (int)((long long)n * (rank + 1) / split);
+  const Share<kType, kWarps> share(row, n, rank, split);
   uint32_t* s_best = reinterpret_cast<uint32_t*>(smem);              // [n] the groups' maxima
 
   Sums a{-INFINITY, 0.0f, 0.0f};
   float lane_top = -INFINITY;
   constexpr int kAhead = Logit<kType>::kAhead;
-  // Blocks of kAhead groups, a warp's block kWarps further on loaded while it
-  // adds one; what is left of the row, or a short row (so that every warp has
-  // some), one group at a time.
-  const int inner0 = row.shift > 0 ? max(g0, 1) : g0, inner1 = min(g1, (row.shift + row.V) / kGroup);
-  const int blocks = inner1 - inner0 >= kWarps * kAhead ? (inner1 - inner0) / kAhead : 0;
+  // a warp's next block is loaded while it adds one
+  const int inner0 = share.inner0, blocks = share.blocks;
   const auto load = [&](int block, uint4 (&w)[kAhead][Logit<kType>::kLoads]) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) row.load_words(inner0 + block * kAhead + i, lane, w[i]);
@@ -494,9 +546,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) add_words<kType>(a, w[i]);
   }
-  const int tail = inner0 + blocks * kAhead;       // groups [g0, inner0) and [tail, g1)
-  for (int i = warp; i < (inner0 - g0) + (g1 - tail); i += kWarps) {
-    const int g = i < inner0 - g0 ? g0 + i : tail + i - (inner0 - g0);
+  for (int i = warp; i < share.singles(); i += kWarps) {
+    const int g = share.single(i);
     float f[8];
     row.load_group(g, lane, f);
     float m = f[0];
@@ -508,16 +559,19 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     if (m > a.m) a.rebase(m);
     add_any(a, f);
   }
+  const int owner = (__ffs(__ballot_sync(kFull, lane_top == a.m)) - 1) & 31;
+  const float rest = warp_sum(lane == owner ? 0.0f : a.s);
   a.s = warp_sum(a.s);
   a.t = warp_sum(a.t);
-  if (lane == 0) s_warp[warp] = a;
+  if (lane == 0) s_warp[warp] = Part{a, rest, rank << 16 | warp << 8 | owner};
   if (threadIdx.x == 0) s_groups = s_count = 0;
   const bool some = p.k > 0;
   if (some && split == 1) top_lanes<kWarps>(order_of(lane_top), warp, lane, s_some);
   __syncthreads();
   // One warp joins the sums, and another looks for the bound meanwhile.
   constexpr int kJoins = kWarps - 1;
-  Sums part{-INFINITY, 0.0f, 0.0f};
+  const Part none{{-INFINITY, 0.0f, 0.0f}, 0.0f, 0};
+  Part part = none;
   if (warp == kJoins && lane < kWarps) part = s_warp[lane];
   if (split > 1) {
     // the first CTA takes the others' sums and maxima from their shared memory
@@ -534,15 +588,17 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
       return;
     }
     if (warp == kJoins) {
-      part = Sums{-INFINITY, 0.0f, 0.0f};
+      part = none;
       if (lane < split) {
         const uint32_t at = dev::mapa(dev::smem_u32(&s_cta), (uint32_t)lane);
-        part = Sums{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)};
+        part = Part{{dev::ld_cluster_f32(at), dev::ld_cluster_f32(at + 4), dev::ld_cluster_f32(at + 8)},
+                    dev::ld_cluster_f32(at + 12),
+                    (int)dev::ld_cluster_u32(at + 16)};
       }
       __syncwarp();
     }
     if (some) {
-      for (int g = g1 + (int)threadIdx.x; g < n; g += 32 * kWarps) {
+      for (int g = share.g1 + (int)threadIdx.x; g < n; g += 32 * kWarps) {
         // the rank whose run of groups holds g
         const int r = (int)(((long long)(g + 1) * split - 1) / n);
         s_best[g] = dev::ld_cluster_u32(dev::mapa(dev::smem_u32(&s_best[g]), (uint32_t)r));
@@ -558,7 +614,13 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   }
   if (warp == kJoins) {
     part = join(part);
-    if (lane == 0) s_cta = part;
+    // The largest logit apart from the others where they add less than an eighth.
+    const bool apart = part.sums.s < 1.125f && fabsf(part.sums.m) < INFINITY;
+    if (apart) {
+      part.sums.s = part.rest + sum_beside<kType, kWarps>(row, Share<kType, kWarps>(row, n, part.where >> 16, split),
+                                                          part.where >> 8 & 255, lane, part.where & 255, part.sums.m);
+    }
+    if (lane == 0) s_cta = part, s_apart = apart;
   }
   if (some && warp == 0) kth_largest(p.k, lane, s_some);
   __syncthreads();
@@ -654,12 +716,13 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     }
   }
 
-  const Sums all = s_cta;
+  const Sums all = s_cta.sums;
+  const float total = s_apart ? 1.0f + all.s : all.s;
   // a row whose every logit is masked: no probabilities (log 0), entropy 0
-  const float log_s = all.s == 0.0f ? 0.0f : logf(all.s);
-  const float base = all.m == -INFINITY && all.s == 0.0f ? 0.0f : all.m;
+  const float log_s = s_apart ? log1pf(all.s) : total == 0.0f ? 0.0f : logf(total);
+  const float base = all.m == -INFINITY && total == 0.0f ? 0.0f : all.m;
   if (writes) {
-    p.entropy[row_index] = all.s == 0.0f ? 0.0f : log_s - kLn2 * (all.t / all.s);
+    p.entropy[row_index] = total == 0.0f ? 0.0f : log_s - kLn2 * (all.t / total);
     if (p.tokens != nullptr) {
       p.logprob[row_index] = token >= 0 && token < (long long)p.V ? (Logit<kType>::one(row.x[token]) - base) - log_s
                                                                   : __uint_as_float(0x7FC00000u);

@@ -507,6 +507,29 @@ def test_logprobs_of_large_logits_keep_their_differences():
         assert torch.equal(u, v)
 
 
+@pytest.mark.parametrize("M,V", [(1, 900), (3, 5000), (40, 40000), (700, 3000), (2, 131072), (200, 70001)])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_logprobs_of_rows_that_are_all_but_decided(M, V, dtype):
+    """log(1 + s) of a small s keeps s's precision, wherever the largest logit
+    stands and however the row is shared out."""
+    g = gen(M + V)
+    for D in (4.0, 9.0, 15.5):
+        for low in (float("-inf"), -1000.0):
+            x = torch.full((M, V), low, dtype=dtype, device=DEV)
+            at = torch.rand((M, V), device=DEV, generator=g).argsort(dim=1)[:, :4]
+            x.scatter_(1, at[:, 1:], 2.0 - D)
+            x.scatter_(1, at[:, :1], 2.0)
+            logprob, entropy, ids, tops = sk.splitk_logprobs(x, at[:, 0].contiguous(), top_k=1)
+            s = 3 * math.exp(-D)
+            ref, h = -math.log1p(s), math.log1p(s) + s * D / (1 + s)
+            # the exponent D log2 e rounds twice (1.5 2^-24 D as a share of s); the
+            # power of two, the sum and the logarithm add a few 2^-24
+            share = 2.0 ** -24 * (1.5 * D + 12)
+            assert ((logprob.double() - ref).abs() <= share * -ref).all()
+            assert ((entropy.double() - h).abs() <= 2 * share * h).all()
+            assert (ids == at[:, :1]).all() and torch.equal(tops[:, 0], logprob)
+
+
 def test_logprobs_token_outside_the_vocabulary():
     x = torch.zeros((4, 100), device=DEV)
     out = sk.splitk_logprobs(x, torch.tensor([-1, 100, 1 << 40, 99], device=DEV))
