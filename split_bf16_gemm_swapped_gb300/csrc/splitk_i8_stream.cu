@@ -9,7 +9,7 @@
 // the chunk's j-th product for weights and tokens alike.  Neither operand
 // passes through shared memory, and a 16-byte load needs no shuffle.
 //
-// Memory bounds it: 18432 x 7168 codes take 23.4 us for one token, 5.7 TB/s.  The
+// Memory bounds it: 18432 x 7168 codes take 23.2 us for one token, 5.7 TB/s.  The
 // loads in flight are what brings it there, so none hangs on a branch.
 //
 // The warps' f32 sums are added in warp order through shared memory, so the
