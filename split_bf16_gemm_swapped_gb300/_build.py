@@ -121,7 +121,7 @@ def build_operators(force: bool = False) -> Path:
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[x for i in includes for x in ("-isystem" if str(i).startswith(str(home)) else "-I", str(i))],
           str(src), "-o", str(tmp), f"-L{LIBDIR}", f"-l:{SPLITK_LIB.name}", f"-L{home / 'lib'}",
-          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+          "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, OPERATORS_LIB)
     return OPERATORS_LIB
 

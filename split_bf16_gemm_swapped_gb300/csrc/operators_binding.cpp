@@ -11,13 +11,14 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 
 #include "splitk.h"
@@ -104,7 +105,7 @@ struct Output {
   }
   void* data(at::IntArrayRef shape, ScalarType type, const at::Device& device) {
     if (given != nullptr) return given->data_ptr();
-    made = at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    made = Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
     return made.data_ptr();
   }
   PyObject* wrap() const { return THPVariable_Wrap(given != nullptr ? *given : made); }
