@@ -70,7 +70,7 @@ struct Logit;
 template <>
 struct Logit<1> {
   static constexpr int kPerLoad = 8, kLoads = 1, kAhead = 4;
-  static constexpr float kNear = 65536.0f;
+  static constexpr float kNear = 65536.0f, kLowest = -3.38953139e38f;
   __device__ static uint32_t pair_of(float v) { return dev::pack_bf16x2(v, v); }
   using T = uint16_t;
   __device__ static float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -101,7 +101,7 @@ struct Logit<1> {
 template <>
 struct Logit<3> {
   static constexpr int kPerLoad = 8, kLoads = 1, kAhead = 4;
-  static constexpr float kNear = 60000.0f;
+  static constexpr float kNear = 60000.0f, kLowest = -65504.0f;
   __device__ static uint32_t pair_of(float v) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(v), "f"(v));
@@ -136,6 +136,7 @@ struct Logit<3> {
 template <>
 struct Logit<2> {
   static constexpr int kPerLoad = 4, kLoads = 2, kAhead = 2;
+  static constexpr float kLowest = -3.402823466e38f;
   using T = float;
   __device__ static float one(float v) { return v; }
   __device__ static void unpack(const uint4 (&w)[2], float (&f)[8]) {
@@ -654,7 +655,8 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     float least = value_of(bound);
     bool strict = false;
     const bool ordered = bound < order_of(INFINITY);         // a finite logit is above it, and it is no NaN
-    for (bool again = groups > kMaxGroups;; again = true) {
+    // (a bound that is a mask's value is reached by every masked logit)
+    for (bool again = groups > kMaxGroups || least <= Logit<kType>::kLowest;; again = true) {
       if (again) {
         __syncthreads();
         if (threadIdx.x == 0) s_groups = s_count = 0;
