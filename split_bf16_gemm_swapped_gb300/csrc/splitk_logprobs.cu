@@ -18,7 +18,7 @@
 // the copy rate); each row's join and selection, some 3 us of latencies, is what
 // 20 alternatives add (52 us), as it overlaps only with other rows' passes.  Rows of
 // a few thousand logits are bound by the instructions of either (4096 x 8000: 19
-// us and 34, the copy rate 10).
+// us and 35, the copy rate 10).
 //
 // A cluster of CTAs shares a row when there are few rows; the first CTA then
 // reads the others' sums and maxima from their shared memory.
@@ -430,30 +430,43 @@ __device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, i
 
 // A lower bound on the k-th largest logit is the k-th largest of 32 of the lanes'
 // values (logits of the row, all different ones), each warp's largest; 0 if there
-// are not that many.  First each warp puts its own into `some` ...
+// are not that many.  Of 64 where `wide`.  First each warp puts its own into `some` ...
 template <int kWarps>
-__device__ __forceinline__ void top_lanes(uint32_t value, int warp, int lane, uint32_t* some) {
+__device__ __forceinline__ void top_lanes(uint32_t value, bool wide, int warp, int lane, uint32_t* some) {
+  const auto next = [&](int at) {
 #pragma unroll
-  for (int i = 0; i < 32 / kWarps; ++i) {
-    const uint32_t top = __reduce_max_sync(kFull, value);
-    const int owner = __ffs(__ballot_sync(kFull, value == top)) - 1;
-    if (lane == owner) {
-      some[(32 / kWarps) * warp + i] = top;
-      value = 0;
+    for (int i = 0; i < 32 / kWarps; ++i) {
+      const uint32_t top = __reduce_max_sync(kFull, value);
+      const int owner = __ffs(__ballot_sync(kFull, value == top)) - 1;
+      if (lane == owner) {
+        some[at + (32 / kWarps) * warp + i] = top;
+        value = 0;
+      }
     }
-  }
+  };
+  next(0);
+  if (wide) next(32);
 }
 // ... and then one warp finds the k-th, to some[0].
-__device__ __forceinline__ void kth_largest(int k, int lane, uint32_t* some) {
-  const uint32_t v = some[lane];
-  int before = 0;
+__device__ __forceinline__ void kth_largest(int k, bool wide, int lane, uint32_t* some) {
+  const uint32_t v = some[lane], u = wide ? some[32 + lane] : 0u;
+  int before = 0, before_u = wide ? 0 : 64;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const uint32_t w = __shfl_sync(kFull, v, i);
     before += w > v || (w == v && i < lane) ? 1 : 0;
   }
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t w = __shfl_sync(kFull, v, i), x = __shfl_sync(kFull, u, i);
+      before += x > v ? 1 : 0;
+      before_u += (w >= u ? 1 : 0) + (x > u || (x == u && i < lane) ? 1 : 0);
+    }
+  }
   __syncwarp();
   if (before == k - 1) some[0] = v;
+  if (before_u == k - 1) some[0] = u;
 }
 
 // A CTA's share of a row's groups: blocks of kAhead, and what is left on either
@@ -504,7 +517,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   __shared__ Part s_cta;
   __shared__ bool s_apart;
   __shared__ int s_sel[kMaxGroups];
-  __shared__ uint32_t s_some[32];
+  __shared__ uint32_t s_some[64];
   __shared__ int s_groups, s_count, s_few_count;
   __shared__ uint64_t s_cand[kMaxCandidates], s_few[kFewCandidates], s_round[2][kWarps];
   dev::griddep_launch_dependents();
@@ -570,7 +583,11 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   if (lane == 0) s_warp[warp] = Part{a, rest, rank << 16 | warp << 8 | owner};
   if (threadIdx.x == 0) s_groups = s_count = 0;
   const bool some = p.k > 0;
-  if (some && split == 1) top_lanes<kWarps>(order_of(lane_top), warp, lane, s_some);
+  // k close to 32 would make the bound the least warp's (1024 x 131072 bf16, top 32:
+  // 67 us, of 64 values 56; rows of few groups have few logits a lane to choose from:
+  // 4096 x 1000 22.6 us, of 64 25.5)
+  const bool wide = p.k > 24 && n > 24;
+  if (some && split == 1) top_lanes<kWarps>(order_of(lane_top), wide, warp, lane, s_some);
   __syncthreads();
   // One warp joins the sums, and another looks for the bound meanwhile.
   constexpr int kJoins = kWarps - 1;
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
       // where other CTAs read a part of the row, the bound is of the groups' maxima
       uint32_t mine = 0;
       for (int g = n * warp / kWarps + lane; g < n * (warp + 1) / kWarps; g += 32) mine = max(mine, s_best[g]);
-      top_lanes<kWarps>(mine, warp, lane, s_some);
+      top_lanes<kWarps>(mine, wide, warp, lane, s_some);
     }
     dev::cluster_arrive_release();
     __syncthreads();
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
     }
     if (lane == 0) s_cta = part, s_apart = apart;
   }
-  if (some && warp == 0) kth_largest(p.k, lane, s_some);
+  if (some && warp == 0) kth_largest(p.k, wide, lane, s_some);
   __syncthreads();
   if (split > 1) dev::cluster_wait_acquire();
   const bool writes = (int)threadIdx.x == 32 * kJoins;       // the row's own results
@@ -696,9 +713,9 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
         // bound is low): its parts' largest give a closer bound.
         uint32_t top = 0;
         for (int c = kWarps * lane + warp; c < count; c += 32 * kWarps) top = max(top, (uint32_t)(s_cand[c] >> 32));
-        top_lanes<kWarps>(top, warp, lane, s_some);
+        top_lanes<kWarps>(top, wide, warp, lane, s_some);
         __syncthreads();
-        if (warp == 0) kth_largest(p.k, lane, s_some);
+        if (warp == 0) kth_largest(p.k, wide, lane, s_some);
         if (threadIdx.x == 32) s_few_count = 0;
         __syncthreads();
         const uint32_t closer = s_some[0];
