@@ -479,8 +479,8 @@ SPLITK_API int splitk_gemm_bf16_noalloc(const void *a, const void *b, void *c,
  *     y = x[m] + residual[m]                   (f32)
  *     residual_out[m] = y                      (rounded to its type)
  *     n = y * weight / sqrt(mean(y^2) + eps)   (f32, of the unrounded y)
- *     scale[m] = max(max|n| / 127, 2^-126)
- *     q[m] = n / scale[m] rounded to nearest even, -127..127
+ *     scale[m] = max(max|n| * (1 / 127), 2^-126)     (1 / 127 rounded to f32)
+ *     q[m] = n / scale[m], the f32 quotient rounded to nearest even, -127..127
  *   x             bf16, rows x_stride elements apart (x_stride >= D)
  *   residual      [M][D] bf16 or f32 (residual_type), or NULL with
  *                 residual_out NULL: y = x and no sum is written.
@@ -488,8 +488,8 @@ SPLITK_API int splitk_gemm_bf16_noalloc(const void *a, const void *b, void *c,
  *   weight        [D] bf16 or f32 (weight_type)
  *   eps           > 0
  *   q             [M][D] 8-bit codes;  scale  [M] f32
- * A row that holds a NaN or an infinity, or whose sum of squares passes the
- * f32 range, has scale NaN; its codes then mean nothing.
+ * A row that holds a NaN or an infinity, or whose sum of squares or largest n
+ * passes the f32 range, has scale NaN; its codes then mean nothing.
  */
 SPLITK_API int splitk_rmsnorm_i8(const void *x, long long x_stride, const void *residual,
                                  void *residual_out, int residual_type, const void *weight,
@@ -498,7 +498,8 @@ SPLITK_API int splitk_rmsnorm_i8(const void *x, long long x_stride, const void *
 
 /*
  * The codes and scales alone (n = x above): activations that follow no norm,
- * or weights (a row is then a channel).
+ * or weights (a row is then a channel).  x is exact in f32, so codes and scales
+ * are to the bit what these 32-bit operations give.
  */
 SPLITK_API int splitk_quantize_i8(const void *x, long long x_stride, void *q, float *scale,
                                   int M, int D, splitk_stream_t stream);

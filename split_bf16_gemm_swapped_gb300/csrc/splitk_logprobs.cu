@@ -276,31 +276,6 @@ __device__ __forceinline__ Part join(Part part) {
   return part;
 }
 
-// Pairs of f32 in one instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void split_pair(uint64_t p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // Adds eight logits of each lane, whose warp's largest is at most a.m; they may
 // be so far below it that they are not finite beside it.
 __device__ __forceinline__ void add_any(Sums& a, const float (&f)[8]) {
@@ -316,20 +291,20 @@ __device__ __forceinline__ void add_any(Sums& a, const float (&f)[8]) {
 
 // The same for logits at most 1000 below it, two at a time.
 __device__ __forceinline__ void add_near(Sums& a, const float (&f)[8]) {
-  const uint64_t minus = pair(-a.m, -a.m), scale = pair(kLog2e, kLog2e);
-  uint64_t s = pair(a.s, 0.0f), t = pair(a.t, 0.0f);
+  const uint64_t minus = dev::f32x2(-a.m, -a.m), scale = dev::f32x2(kLog2e, kLog2e);
+  uint64_t s = dev::f32x2(a.s, 0.0f), t = dev::f32x2(a.t, 0.0f);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const uint64_t d = pair_mul(pair_add(pair(f[j], f[j + 1]), minus), scale);
+    const uint64_t d = dev::f32x2_mul(dev::f32x2_add(dev::f32x2(f[j], f[j + 1]), minus), scale);
     float d0, d1;
-    split_pair(d, d0, d1);
-    const uint64_t e = pair(exp2_approx(d0), exp2_approx(d1));
-    s = pair_add(s, e);
-    t = pair_fma(e, d, t);
+    dev::f32x2_split(d, d0, d1);
+    const uint64_t e = dev::f32x2(exp2_approx(d0), exp2_approx(d1));
+    s = dev::f32x2_add(s, e);
+    t = dev::f32x2_fma(e, d, t);
   }
   float s0, s1, t0, t1;
-  split_pair(s, s0, s1);
-  split_pair(t, t0, t1);
+  dev::f32x2_split(s, s0, s1);
+  dev::f32x2_split(t, t0, t1);
   a.s = s0 + s1;
   a.t = t0 + t1;
 }

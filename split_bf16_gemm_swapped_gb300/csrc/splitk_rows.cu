@@ -3,13 +3,13 @@
 //
 //   y = x + r                                   (f32; r' = y in r's type)
 //   n = y * w / sqrt(mean(y^2) + eps)           (quantise alone: n = x)
-//   s = max(max|n| / 127, 2^-126);  q = rne(n / s)
+//   s = max(max|n| (1/127), 2^-126);  q = rne(n / s), the f32 quotient
 //
 // max|n| = max|y w| / rms, so one joint reduction of (sum y^2, max|y w|) over
 // the row gives both statistics, and the row's values z = y w stay in
 // registers between reading and coding: every byte is read and written once, and
-// memory is the bound (2048 x 7168 with a bf16 residual 16.7 us, 92 % of the copy
-// rate; 18432 x 7168 codes 73 us, 81 %).  Sums and statistics are f32; a code is
+// memory is the bound (2048 x 7168 with a bf16 residual 16.8 us, 92 % of the copy
+// rate; 18432 x 7168 codes 74 us, 80 %).  Sums and statistics are f32; a code is
 // rounded by adding 1.5 * 2^23 (the sum's low byte is then the two's complement
 // code, rounded to nearest even).
 
@@ -54,16 +54,34 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// v * m rounded to the nearest whole number (|v * m| <= 127), in the low byte.
-// The product is rounded to f32 first: a value halfway between two codes (in
-// bf16 rows they are common) then mostly comes out as that half and goes to the
-// even code, where the product's own last bits would send it either way.
-__device__ __forceinline__ uint32_t code_of(float v, float m) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(v, m), 12582912.0f));
+// The code of n, rne(n / s) with the f32 quotient (|n / s| <= 127), in the low
+// byte.  Values at and beside halves between two codes are common in bf16 rows (half
+// the largest is one), and the product with r = 1 / s alone sends them either way.
+// The product's remainder n - q s (exact in one fused operation) times r
+// corrects it to the quotient (Markstein 1990, "Computation of elementary functions
+// on the IBM RISC System/6000 processor"), for two more instructions on a pair.
+constexpr float kRound = 12582912.0f;          // 1.5 * 2^23
+__device__ __forceinline__ uint32_t code_of(float n, float s, float r) {
+  const float q = __fmul_rn(n, r);
+  return __float_as_uint(__fadd_rn(fmaf(fmaf(-q, s, n), r, q), kRound));
 }
 
 __device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return dev::prmt(dev::prmt(a, b, 0x0040u), dev::prmt(c, d, 0x0040u), 0x5410u);
+}
+
+// Eight of them, two in an instruction.
+__device__ __forceinline__ uint2 codes_of(const float (&n)[kVec], float s, float r) {
+  const uint64_t minus_s = dev::f32x2(-s, -s), rr = dev::f32x2(r, r), round = dev::f32x2(kRound, kRound);
+  uint32_t c[kVec];
+#pragma unroll
+  for (int j = 0; j < kVec; j += 2) {
+    const uint64_t v = dev::f32x2(n[j], n[j + 1]), q = dev::f32x2_mul(v, rr);
+    float lo, hi;
+    dev::f32x2_split(dev::f32x2_add(dev::f32x2_fma(dev::f32x2_fma(q, minus_s, v), rr, q), round), lo, hi);
+    c[j] = __float_as_uint(lo), c[j + 1] = __float_as_uint(hi);
+  }
+  return make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
 }
 
 // Eight consecutive elements in 16-byte words of type kType (1 bf16, 2 f32).
@@ -121,22 +139,27 @@ __device__ __forceinline__ void reduce_row(float& sum, float& amax, int turn) {
   }
 }
 
-// The row's scale, and the factors from z = y w to codes: z * first * mult.
-// `first` is 1 unless the scale is so near its floor that one factor would
-// pass f32 (a row of zeros, say).  A row that holds a NaN or an infinity (or
-// whose sum of squares passes f32) has no codes: its scale is NaN, and so is
-// every product that uses it.
-__device__ __forceinline__ float row_scale(bool norm, float sum, float amax, int width, float eps, float* first,
-                                           float* mult) {
-  const float rinv = norm ? 1.0f / sqrtf(sum / (float)width + eps) : 1.0f;
-  float s = fmaxf(amax * rinv / 127.0f, kMinScale);
-  // rinv / s, which is 127 / amax (one rounding) unless the scale is its floor
-  const float m = s > kMinScale ? 127.0f / amax : rinv / s;
-  if (!(sum <= kMaxF32) || !(amax <= kMaxF32)) s = __uint_as_float(0x7FC00000u);
-  *first = m > kMaxF32 ? rinv : 1.0f;
-  *mult = m > kMaxF32 ? 1.0f / s : m;
-  return s;
-}
+// The row's scale, and what its codes are made of: values z = y w become
+// n = z * factor (factor 1 where there is no norm), and n's code is that of n / s,
+// r = 1 / s.  (n and s are both 2^64 times themselves where s is so small that a
+// remainder would pass f32's smallest numbers; a quotient's the same.)
+//
+// 1 / 127 is a factor, as PyTorch's division of a GPU tensor by 127 has it: codes
+// and scales are to the bit what the elementary operations give for a row.  A row
+// that holds a NaN or an infinity (or whose sum of squares or largest n passes
+// f32) has no codes: its scale is NaN, and so is every product that uses it.
+struct RowCodes {
+  float scale, factor, lift, s, r;
+  __device__ __forceinline__ RowCodes(bool norm, float sum, float amax, int width, float eps) {
+    factor = norm ? 1.0f / sqrtf(sum / (float)width + eps) : 1.0f;
+    const float top = amax * factor;               // max|n|: rounding keeps the order
+    scale = fmaxf(top * (1.0f / 127.0f), kMinScale);
+    lift = scale < 0x1p-60f ? 0x1p64f : 1.0f;
+    s = scale * lift;
+    r = 1.0f / s;
+    if (!(sum <= kMaxF32) || !(top <= kMaxF32)) scale = __uint_as_float(0x7FC00000u);
+  }
+};
 
 // kRes: 0 no residual, 1 bf16, 2 f32.  kW: 0 no norm (quantise alone), 1 bf16
 // weight, 2 f32 weight.  kVecs: 8-element vectors a thread holds.
@@ -206,24 +229,27 @@ __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p)
     }
     if (kNext && row + stride < p.rows) load(row + stride);
     reduce_row(sum, amax, turn);
-    float first, mult;
-    const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
-    if (tid == 0) p.scale[row] = s;
-    if (first != 1.0f) {
+    const RowCodes codes(kW != 0, sum, amax, p.width, p.eps);
+    if (tid == 0) p.scale[row] = codes.scale;
+    if (kW != 0) {
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) z[v][j] *= first;
+        for (int j = 0; j < kVec; ++j) z[v][j] *= codes.factor;
+      }
+    }
+    if (codes.lift != 1.0f) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) z[v][j] *= codes.lift;
       }
     }
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int e = (v * step + tid) * kVec;
       if (e >= p.width) continue;
-      uint2 o;
-      o.x = pack_codes(code_of(z[v][0], mult), code_of(z[v][1], mult), code_of(z[v][2], mult), code_of(z[v][3], mult));
-      o.y = pack_codes(code_of(z[v][4], mult), code_of(z[v][5], mult), code_of(z[v][6], mult), code_of(z[v][7], mult));
-      *reinterpret_cast<uint2*>(p.q + base + e) = o;
+      *reinterpret_cast<uint2*>(p.q + base + e) = codes_of(z[v], codes.s, codes.r);
     }
     if (!kNext && row + stride < p.rows) load(row + stride);
   }
@@ -261,13 +287,12 @@ __global__ void __launch_bounds__(kMaxRowThreads, kRes != 0 && kEach == 8 ? 2 : 
     amax = max_nan(amax, fabsf(y));
   }
   reduce_row(sum, amax, 0);
-  float first, mult;
-  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
-  if (tid == 0) p.scale[row] = s;
+  const RowCodes codes(kW != 0, sum, amax, p.width, p.eps);
+  if (tid == 0) p.scale[row] = codes.scale;
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
     const int e = j * step + tid;
-    if (e < p.width) p.q[base + e] = (int8_t)(code_of(z[j] * first, mult) & 0xFFu);
+    if (e < p.width) p.q[base + e] = (int8_t)(code_of(z[j] * codes.factor * codes.lift, codes.s, codes.r) & 0xFFu);
   }
 }
 
@@ -292,9 +317,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) long_rows_kernel(const RowPara
     amax = max_nan(amax, fabsf(y));
   }
   reduce_row(sum, amax, 0);
-  float first, mult;
-  const float s = row_scale(kW != 0, sum, amax, p.width, p.eps, &first, &mult);
-  if (threadIdx.x == 0) p.scale[row] = s;
+  const RowCodes codes(kW != 0, sum, amax, p.width, p.eps);
+  if (threadIdx.x == 0) p.scale[row] = codes.scale;
   for (int e = (int)threadIdx.x; e < p.width; e += (int)blockDim.x) {
     float y = bf16_one(x[e]);
     if (kRes != 0) {
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) long_rows_kernel(const RowPara
       store1<kRes == 0 ? 1 : kRes>(p.residual_out, base + e, y);
     }
     if (kW != 0) y *= load1<kW == 0 ? 1 : kW>(p.weight, e);
-    p.q[base + e] = (int8_t)(code_of(y * first, mult) & 0xFFu);
+    p.q[base + e] = (int8_t)(code_of(y * codes.factor * codes.lift, codes.s, codes.r) & 0xFFu);
   }
 }
 

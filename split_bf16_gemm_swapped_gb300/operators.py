@@ -40,7 +40,7 @@ def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale
                       stream=None):
     """Residual addition, RMS norm and 8-bit codes with a scale per row:
     y = x + residual, n = y * weight / sqrt(mean(y^2) + eps), codes
-    q = round(n / scale) with scale = max|n| / 127.
+    q = round(n / scale) with scale = max|n| * (1 / 127), in float32.
 
     x [M, D] (rows any distance apart) or contiguous [L, M, D], bfloat16;
     residual contiguous of x's shape, bfloat16 or float32; weight [D],
@@ -54,9 +54,11 @@ def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale
 
 
 def splitk_quantize_i8(x, q=None, scale=None, stream=None):
-    """8-bit codes with a scale per row, scale = max|x| / 127: activations
-    (a row is a token) or weights (a row is a channel).  x as in
-    splitk_rmsnorm_i8; returns (q int8, scale float32)."""
+    """8-bit codes with a scale per row: activations (a row is a token) or weights
+    (a row is a channel).  x as in splitk_rmsnorm_i8; returns (q int8, scale
+    float32), to the bit what scale = (x.float().abs().amax(-1) / 127) and
+    torch.round(x.float() / scale[..., None]) give on the GPU (scale at least
+    2**-126)."""
     out = _native.quantize_i8(x, q, scale, stream)
     if type(out) is int:
         raise SplitKError(out, "splitk_quantize_i8")

@@ -614,3 +614,69 @@ def test_the_chain_in_a_graph():
         for u, v in zip(outs, step()):
             assert torch.equal(u, v)
     assert sk.splitk_get_status() == 0
+
+
+def plain_codes(x):
+    """Codes and scales by elementary 32-bit operations."""
+    x = x.float()
+    scale = (x.abs().amax(-1) / 127).clamp_min(2.0 ** -126)
+    return torch.round(x / scale[..., None]).to(torch.int8), scale
+
+
+@pytest.mark.parametrize("M,D", [(2000, 7168), (3000, 1000), (700, 4999), (300, 16384), (40, 33000), (5000, 255), (1, 7168)])
+def test_codes_are_the_formulas_to_the_bit(M, D):
+    """No tolerance: x is exact in 32 bits, and the scale and the quotient are
+    one rounding each.  Rows with outliers, rows whose values are whole
+    multiples of a unit (most of them halves between two codes when the largest
+    is 254 units), and tiny ones."""
+    g = gen(D)
+    x = randn((M, D), g, BF16)
+    x = torch.where(torch.rand(D, device=DEV, generator=g) < 0.01, x * 30, x)
+    steps = torch.randint(-254, 255, (M, D), device=DEV, generator=g).to(BF16)       # below 256: exact in bf16
+    steps[:, 0] = torch.randint(128, 255, (M,), device=DEV, generator=g).to(BF16)
+    even = steps.clone()
+    even[:, 0] = 254
+    tiny = randn((M, D), g, BF16, 2.0 ** -120)
+    for rows in (x, steps, even, tiny):
+        q, scale = sk.splitk_quantize_i8(rows)
+        ref_q, ref_s = plain_codes(rows)
+        assert torch.equal(scale, ref_s)
+        assert torch.equal(q, ref_q), (q != ref_q).sum().item()
+
+
+def test_every_code_of_every_largest_value():
+    """Each bf16 mantissa as a row's largest value, with every bf16 value below
+    it whose code is not 0: quotients have no other mantissas."""
+    top = (128 + torch.arange(128, device=DEV)).float()                   # 128 .. 255
+    values = top.repeat(9) * 2.0 ** -torch.arange(9, device=DEV).repeat_interleave(128).float()
+    x = torch.where(values <= top[:, None], values, 0.0)
+    x = torch.cat([x, -x], 1)
+    for unit in (1.0, 2.0 ** -100, 2.0 ** 100):
+        q, scale = sk.splitk_quantize_i8((unit * x).to(BF16))
+        ref_q, ref_s = plain_codes(unit * x)
+        assert torch.equal(scale, ref_s) and torch.equal(q, ref_q)
+
+
+@pytest.mark.parametrize("D", [64, 1000, 4999, 7168, 16384, 33000])
+def test_codes_of_the_norm_are_those_of_its_rows(D):
+    """Features of one magnitude and a weight that carries the row: n is then a
+    known f32 (the root of a power of four is exact), and so are its codes."""
+    g = gen(D)
+    M = 50
+    sign = torch.where(torch.rand((M, D), device=DEV, generator=g) < 0.5, -1.0, 1.0)
+    w = torch.randint(1, 255, (D,), device=DEV, generator=g).float()
+    w[D // 2] = 254
+    # mean(y^2) = 4 exactly (sums of 4 below 2^24), and eps is far below its last bit
+    q, scale, _ = sk.splitk_rmsnorm_i8((2 * sign).to(BF16), w, eps=1e-12)
+    ref_q, ref_s = plain_codes(sign * w)
+    assert torch.equal(scale, ref_s) and torch.equal(q, ref_q)
+
+
+def test_norm_whose_rows_pass_the_range_has_no_codes():
+    """n past f32 is an infinity: the scale is NaN, as for one in the row."""
+    x = torch.zeros((2, 256), dtype=BF16, device=DEV)
+    x[0, 0] = x[1, 0] = 1
+    w = torch.full((256,), 3e38, device=DEV)
+    w[1:] = 1
+    _, scale, _ = sk.splitk_rmsnorm_i8(x, w)
+    assert torch.isnan(scale).all()
