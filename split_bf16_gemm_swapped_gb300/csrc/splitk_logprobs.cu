@@ -365,7 +365,10 @@ __device__ __forceinline__ uint32_t draw_groups(uint32_t* best, int n, int k, in
 }
 
 // One warp: the first `need` logits of the row that equal `value`, as keys into
-// `cand`; `best` holds the groups' maxima, `bound` the value's order.
+// `cand`; `best` holds the groups' maxima, `bound` the value's order.  Maxima pass over
+// NaN, so a group whose maximum is `value` may hold nothing else of the row (where
+// the value is -inf, which what is beside a row reads as): its NaN count as equal.
+// That leaves no logit of the row out, and the caller has `need` of them.
 template <int kType>
 __device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, int n, uint32_t bound, float value,
                                          int lane, int need, uint64_t* cand) {
@@ -374,6 +377,7 @@ __device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, i
     uint32_t there = __ballot_sync(kFull, g0 + lane < n && best[min(g0 + lane, n - 1)] >= bound);
     for (; there != 0; there &= there - 1) {
       const int g = g0 + __ffs(there) - 1;
+      const bool nan_too = best[g] == bound;
       float f[8];
       row.load_group(g, lane, f);
 #pragma unroll
@@ -382,7 +386,8 @@ __device__ __noinline__ void first_equal(Row<kType> row, const uint32_t* best, i
 #pragma unroll
         for (int j = h; j < h + kRun; ++j) {
           const int id = Row<kType>::at(g, lane, j) - row.shift;
-          if (f[j] == value && id >= 0 && id < row.V) equal |= 1u << j;
+          const bool is = f[j] == value || (nan_too && f[j] != f[j]);
+          if (is && id >= 0 && id < row.V) equal |= 1u << j;
         }
         int rank = __popc(equal);
 #pragma unroll

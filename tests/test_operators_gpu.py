@@ -680,3 +680,57 @@ def test_norm_whose_rows_pass_the_range_has_no_codes():
     w[1:] = 1
     _, scale, _ = sk.splitk_rmsnorm_i8(x, w)
     assert torch.isnan(scale).all()
+
+
+def check_nan_rows(x):
+    """Rows that hold a NaN: no values, but alternatives that are tokens of the
+    row, each one once."""
+    M, V = x.shape
+    for k in (1, 5, 20, 32):
+        if k > V:
+            continue
+        t = torch.zeros(M, dtype=torch.int64, device=DEV)
+        logprob, entropy, ids, tops = sk.splitk_logprobs(x, t, top_k=k)
+        assert torch.isnan(logprob).all() and torch.isnan(entropy).all() and torch.isnan(tops).all()
+        assert (ids >= 0).all() and (ids < V).all()
+        assert (ids.sort(dim=1).values.diff(dim=1) > 0).all()
+
+
+@pytest.mark.parametrize("V", [1, 5, 33, 200, 255, 256, 300, 511, 4000, 8192])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_logprobs_of_short_rows_of_nan_and_few_others(V, dtype):
+    """Groups that hold NaN and masked logits, or NaN and what is beside the
+    row, at every alignment of a row's ends."""
+    nan, inf = float("nan"), float("inf")
+    g = gen(V)
+    for offset, pad in ((0, 0), (1, 0), (3, 6), (7, 1)):
+        for M in (1, 200):
+            room = torch.zeros((M, offset + V + pad), dtype=dtype, device=DEV)
+            x = room[:, offset:offset + V]
+            x.fill_(nan)
+            check_nan_rows(x)
+            if V == 1:
+                continue
+            for other in (-inf, -3.0, inf):
+                for few in (1, 2, 3, 40):
+                    x.fill_(nan)
+                    x[:, torch.randperm(V, device=DEV, generator=g)[:min(few, V - 1)]] = other
+                    check_nan_rows(x)
+
+
+@pytest.mark.parametrize("M,V", [(1, 131072), (3, 50001), (300, 50001), (1, 40000), (700, 8000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_of_long_rows_of_nan_and_masks(M, V, dtype):
+    """A masked logit in each group of 256 and NaN beside it, and fewer finite
+    logits than alternatives."""
+    nan, inf = float("nan"), float("inf")
+    for step in (7, 200, 256, 3000):
+        for finite in (0, 3):
+            x = torch.full((M, V), nan, dtype=dtype, device=DEV)
+            x[:, ::step] = -inf
+            x[:, V // 3:V // 3 + finite] = 1.0
+            check_nan_rows(x)
+            x = torch.full((M, V), -inf, dtype=dtype, device=DEV)
+            x[:, step // 2::step] = nan
+            x[:, V // 3:V // 3 + finite] = 1.0
+            check_nan_rows(x)
