@@ -134,23 +134,37 @@ struct Rows {
 
 int as_int(int64_t v) { return v > INT32_MAX ? -1 : (int)v; }       // a size the library refuses
 
-// The stream argument's handle, or the device's current stream's.
-splitk_stream_t stream_of(PyObject* o, const at::Device& device) {
-  if (o == Py_None) {
-    return reinterpret_cast<splitk_stream_t>(c10::cuda::getCurrentCUDAStream(device.index()).stream());
-  }
+// The stream argument, or the device's current stream.
+struct Stream {
+  c10::cuda::CUDAStream stream;
+  bool given;
+  splitk_stream_t handle() const { return reinterpret_cast<splitk_stream_t>(stream.stream()); }
+};
+Stream stream_of(PyObject* o, const at::Device& device) {
+  if (o == Py_None) return {c10::cuda::getCurrentCUDAStream(device.index()), false};
   PyObject* handle = PyObject_GetAttrString(o, "cuda_stream");
   if (handle == nullptr) throw python_error();
   void* p = PyLong_AsVoidPtr(handle);
   Py_DECREF(handle);
   if (p == nullptr && PyErr_Occurred()) throw python_error();
-  return reinterpret_cast<splitk_stream_t>(p);
+  return {c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), device.index()), true};
 }
 
-// Python may run other threads while memory is found and the call enqueued.
-struct Released {
-  PyThreadState* state = PyEval_SaveThread();
-  ~Released() { PyEval_RestoreThread(state); }
+// What a call is enqueued under: Python may run other threads while memory is
+// found and the call enqueued; the operands' device is the current one, and a stream
+// given is its current stream, so that outputs made here are of that stream's
+// memory: a block freed on another stream may still be in use there, and this
+// one's, freed in turn, must not go to another while this one writes it.
+struct Enqueue {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  c10::cuda::CUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard current;
+  Enqueue(const at::Device& device, const Stream& s) : guard(device) {
+    if (s.given) current.reset_stream(s.stream);
+  }
 };
 
 PyObject* none() { return Py_NewRef(Py_None); }
@@ -202,16 +216,15 @@ PyObject* rmsnorm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     q.check("q", shape, ScalarType::Char, device);
     scale.check("scale", rows, ScalarType::Float, device);
-    const splitk_stream_t stream = stream_of(a[7], device);
+    const Stream stream = stream_of(a[7], device);
     int rc;
     {
-      Released released;
-      c10::cuda::CUDAGuard guard(device);
+      const Enqueue enqueue(device, stream);
       rc = splitk_rmsnorm_i8(x.data_ptr(), r.stride, residual ? residual->data_ptr() : nullptr,
                              residual ? out.data(shape, r_type, device) : nullptr, code_of(r_type), weight.data_ptr(),
                              code_of(weight.scalar_type()), (float)eps, q.data(shape, ScalarType::Char, device),
                              static_cast<float*>(scale.data(rows, ScalarType::Float, device)), as_int(r.rows),
-                             as_int(r.width), stream);
+                             as_int(r.width), stream.handle());
     }
     if (rc != SPLITK_OK) return PyLong_FromLong(rc);
     return Py_BuildValue("NNN", q.wrap(), scale.wrap(), residual ? out.wrap() : none());
@@ -230,14 +243,13 @@ PyObject* quantize_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef shape = x.sizes(), rows = shape.slice(0, shape.size() - 1);
     q.check("q", shape, ScalarType::Char, device);
     scale.check("scale", rows, ScalarType::Float, device);
-    const splitk_stream_t stream = stream_of(a[3], device);
+    const Stream stream = stream_of(a[3], device);
     int rc;
     {
-      Released released;
-      c10::cuda::CUDAGuard guard(device);
+      const Enqueue enqueue(device, stream);
       rc = splitk_quantize_i8(x.data_ptr(), r.stride, q.data(shape, ScalarType::Char, device),
                               static_cast<float*>(scale.data(rows, ScalarType::Float, device)), as_int(r.rows),
-                              as_int(r.width), stream);
+                              as_int(r.width), stream.handle());
     }
     if (rc != SPLITK_OK) return PyLong_FromLong(rc);
     return Py_BuildValue("NN", q.wrap(), scale.wrap());
@@ -287,14 +299,13 @@ PyObject* gemm_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       type_error(std::string("c must be bfloat16 or float32, not ") + name_of(type));
     }
     c.check("c", outputs, type, device);
-    const splitk_stream_t stream = stream_of(a[7], device);
+    const Stream stream = stream_of(a[7], device);
     int rc;
     {
-      Released released;
-      c10::cuda::CUDAGuard guard(device);
+      const Enqueue enqueue(device, stream);
       rc = splitk_gemm_i8(a_q.data_ptr(), a_scale.data_ptr<float>(), b_q.data_ptr(), b_scale.data_ptr<float>(),
                           bias ? bias->data_ptr() : nullptr, c.data(outputs, type, device), code_of(type), as_int(M),
-                          as_int(N), as_int(K), as_int(L), stream);
+                          as_int(N), as_int(K), as_int(L), stream.handle());
     }
     if (rc != SPLITK_OK) return PyLong_FromLong(rc);
     return c.wrap();
@@ -333,18 +344,17 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (k == 0 && (ids.given != nullptr || tops.given != nullptr)) {
       value_error("the alternatives' outputs need top_k > 0");
     }
-    const splitk_stream_t stream = stream_of(a[7], device);
+    const Stream stream = stream_of(a[7], device);
     int rc = SPLITK_ERR_INVALID_ARGUMENT;
     if (k == 0 || some) {
-      Released released;
-      c10::cuda::CUDAGuard guard(device);
+      const Enqueue enqueue(device, stream);
       rc = splitk_logprobs(logits.data_ptr(), code_of(logits.scalar_type()), r.stride,
                            tokens ? reinterpret_cast<const long long*>(tokens->data_ptr<int64_t>()) : nullptr,
                            tokens ? static_cast<float*>(logprob.data(rows, ScalarType::Float, device)) : nullptr,
                            static_cast<float*>(entropy.data(rows, ScalarType::Float, device)), (int)k,
                            some ? static_cast<long long*>(ids.data(wide, ScalarType::Long, device)) : nullptr,
                            some ? static_cast<float*>(tops.data(wide, ScalarType::Float, device)) : nullptr,
-                           as_int(r.rows), as_int(r.width), stream);
+                           as_int(r.rows), as_int(r.width), stream.handle());
     }
     if (rc != SPLITK_OK) return PyLong_FromLong(rc);
     return Py_BuildValue("NNNN", tokens ? logprob.wrap() : none(), entropy.wrap(), some ? ids.wrap() : none(),

@@ -6,6 +6,11 @@ and every step runs in the library's kernels (``include/splitk.h`` says what
 each computes).  The binding is compiled (``csrc/operators_binding.cpp``,
 ``_lib/_operators.so``): a single-token call takes the GPU a few microseconds,
 less than its checks would take here.
+
+A call's stream is the device's current one, or the one given as `stream`.
+Outputs a call makes belong to that stream, as if it had been current.  As with
+PyTorch's own calls, tensors of another stream are the caller's to order
+(stream.wait_stream) and to keep until the work is done (tensor.record_stream).
 """
 from __future__ import annotations
 

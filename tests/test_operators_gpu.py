@@ -734,3 +734,73 @@ def test_logprobs_of_long_rows_of_nan_and_masks(M, V, dtype):
             x[:, step // 2::step] = nan
             x[:, V // 3:V // 3 + finite] = 1.0
             check_nan_rows(x)
+
+
+def stream_of_memory(t):
+    """The stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= at < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+def made_on(s, **kw):
+    """What each operator makes, on stream s."""
+    x = torch.ones((4, 512), dtype=BF16, device=DEV)
+    w = torch.ones(512, device=DEV)
+    a, sa = torch.ones((256, 512), dtype=torch.int8, device=DEV), torch.ones(256, device=DEV)
+    t = torch.zeros(4, dtype=torch.int64, device=DEV)
+    s.wait_stream(torch.cuda.current_stream())
+    for operand in (x, w, a, sa, t):
+        operand.record_stream(s)
+    q, scale, out = sk.splitk_rmsnorm_i8(x, w, x, **kw)
+    c = sk.splitk_gemm_i8(a, sa, q, scale, **kw)
+    return (q, scale, out, c, *sk.splitk_quantize_i8(x, **kw), *sk.splitk_logprobs(c, t, top_k=2, **kw))
+
+
+def test_outputs_are_of_the_memory_of_the_stream_given():
+    s = torch.cuda.Stream()
+    external = torch.cuda.ExternalStream(s.cuda_stream)
+    current = torch.cuda.current_stream()
+    for stream in (s, external):
+        made = made_on(s, stream=stream)
+        assert torch.cuda.current_stream() == current                   # as before
+        assert all(stream_of_memory(t) == s.cuda_stream for t in made)
+        s.synchronize()
+    with torch.cuda.stream(s):
+        assert all(stream_of_memory(t) == s.cuda_stream for t in made_on(s))
+        default = made_on(current, stream=current)
+    assert all(stream_of_memory(t) == current.cuda_stream for t in default)
+    torch.cuda.synchronize()
+
+
+def test_an_output_is_no_block_that_another_stream_still_writes():
+    """A block freed on the current stream, whose last kernel there waits, does
+    not become the output of a call on a stream given; and an output dropped
+    while that stream still writes it does not come back on the current one."""
+    g = gen(30)
+    s = torch.cuda.Stream()
+    a, b = codes((1024, 512), g), codes((300, 512), g)
+    sa, sb = torch.rand(1024, device=DEV, generator=g), torch.rand(300, device=DEV, generator=g)
+    ref = sk.splitk_gemm_i8(a, sa, b, sb, out_dtype=F32)
+    torch.cuda.synchronize()
+    victim = torch.empty((300, 1024), device=DEV)
+    torch.cuda._sleep(50_000_000)
+    victim.fill_(7)
+    del victim
+    c = sk.splitk_gemm_i8(a, sa, b, sb, out_dtype=F32, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(c, ref)
+    at = c.data_ptr()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    del c
+    c = sk.splitk_gemm_i8(a, sa, b, sb, out_dtype=F32, stream=s)
+    assert c.data_ptr() == at                            # in the stream's order: its own memory again
+    del c
+    other = torch.full((300, 1024), 3.0, device=DEV)
+    assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert (other == 3).all()
