@@ -7,7 +7,10 @@ arguments: every step of the GEMM runs in the library's sm_103a kernels, and
 there is no CPU or PyTorch fallback -- if the library is missing, importing a
 function that needs it raises.
 
-PyTorch supplies device memory and streams.  Tensors:
+PyTorch supplies device memory and streams.  A call runs on the device's current
+stream, or on the one given as `stream`; an output it makes belongs to that
+stream, and tensors of another are the caller's to order and to keep
+(Tensor.record_stream), as with PyTorch's own calls.  Tensors:
   a  weights      [L, N, K] (or [N, K]) bfloat16, CUDA, contiguous
   b  activations  [L, M, K] (or [M, K]) bfloat16, CUDA, contiguous
   c  output       [L, M, N] (or [M, N]) bfloat16, CUDA, contiguous
@@ -228,11 +231,20 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(int(stream.cuda_stream))
 
 
-def _out(c, a, M, N, L):
+def _out(c, a, M, N, L, stream=None):
+    """The output given, checked, or a new one: of the memory of the stream that
+    writes it, since a block freed on another may still be in use there."""
     import torch
     shape = (M, N) if a.dim() == 2 else (L, M, N)
     if c is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=a.device)
+        if stream is None:
+            return torch.empty(shape, dtype=torch.bfloat16, device=a.device)
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = int(stream.cuda_stream)
+            stream = (torch.cuda.ExternalStream(handle, device=a.device) if handle
+                      else torch.cuda.default_stream(a.device))
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=torch.bfloat16, device=a.device)
     if tuple(c.shape) != shape or c.dtype != torch.bfloat16 or not c.is_contiguous():
         raise ValueError(f"c must be a contiguous bfloat16 tensor of shape {shape}")
     if c.device != a.device:
@@ -253,7 +265,7 @@ def splitk_gemm_bf16(a, b, c=None, split_k: int = 0, stream=None):
     import torch
     M, N, K, L = _dims(a, b)
     _require_cuda(a, b)
-    c = _out(c, a, M, N, L)
+    c = _out(c, a, M, N, L, stream)
     _require_cuda(c)
     with torch.cuda.device(a.device):
         rc = load_library().splitk_gemm_bf16(
@@ -311,7 +323,7 @@ def splitk_gemm_w4a16(a_q, a_s, b, c=None, split_k: int = 0, stream=None):
     import torch
     M, N, K, L = _w4_dims(a_q, a_s, b)
     _require_cuda(a_q, a_s, b)
-    c = _out(c, b, M, N, L)
+    c = _out(c, b, M, N, L, stream)
     with torch.cuda.device(b.device):
         rc = load_library().splitk_gemm_w4a16(a_q.data_ptr(), a_s.data_ptr(), b.data_ptr(), c.data_ptr(),
                                               M, N, K, L, int(split_k), _stream_handle(stream, b.device))
@@ -323,7 +335,7 @@ def splitk_gemm_w4a16_planned(a_q, a_s, b, c, plan: Plan, flags: int = 0, stream
     import torch
     M, N, K, L = _w4_dims(a_q, a_s, b)
     _require_cuda(a_q, a_s, b)
-    c = _out(c, b, M, N, L)
+    c = _out(c, b, M, N, L, stream)
     with torch.cuda.device(b.device):
         rc = load_library().splitk_gemm_w4a16_planned(a_q.data_ptr(), a_s.data_ptr(), b.data_ptr(),
                                                       c.data_ptr(), M, N, K, L, ctypes.byref(plan),
@@ -375,7 +387,7 @@ def splitk_gemm_w8a16(a_q, a_s, b, c=None, split_k: int = 0, stream=None):
     import torch
     M, N, K, L = _w8_dims(a_q, a_s, b)
     _require_cuda(a_q, a_s, b)
-    c = _out(c, b, M, N, L)
+    c = _out(c, b, M, N, L, stream)
     with torch.cuda.device(b.device):
         rc = load_library().splitk_gemm_w8a16(a_q.data_ptr(), a_s.data_ptr(), b.data_ptr(), c.data_ptr(),
                                               M, N, K, L, int(split_k), _stream_handle(stream, b.device))
@@ -387,7 +399,7 @@ def splitk_gemm_w8a16_planned(a_q, a_s, b, c, plan: Plan, flags: int = 0, stream
     import torch
     M, N, K, L = _w8_dims(a_q, a_s, b)
     _require_cuda(a_q, a_s, b)
-    c = _out(c, b, M, N, L)
+    c = _out(c, b, M, N, L, stream)
     with torch.cuda.device(b.device):
         rc = load_library().splitk_gemm_w8a16_planned(a_q.data_ptr(), a_s.data_ptr(), b.data_ptr(),
                                                       c.data_ptr(), M, N, K, L, ctypes.byref(plan),
@@ -427,7 +439,7 @@ def splitk_tune(a_list, b, c=None, split_k: int = 0, reps: int = 64, stream=None
         if tuple(a.shape) != tuple(a_list[0].shape) or a.dtype != a_list[0].dtype:
             raise ValueError("the weight tensors must have one shape and dtype")
     _require_cuda(*a_list, b)
-    c = _out(c, a_list[0], M, N, L)
+    c = _out(c, a_list[0], M, N, L, stream)
     ptrs = (ctypes.c_void_p * len(a_list))(*[a.data_ptr() for a in a_list])
     plan = Plan()
     us = ctypes.c_float(0.0)
@@ -447,7 +459,7 @@ def splitk_gemm_bf16_bias(a, b, bias, c=None, split_k: int = 0, stream=None):
     _require_cuda(a, b, bias)
     if bias.dtype != torch.bfloat16 or bias.numel() != L * N:
         raise ValueError("bias must be a bfloat16 tensor of L*N elements")
-    c = _out(c, a, M, N, L)
+    c = _out(c, a, M, N, L, stream)
     _require_cuda(c)
     with torch.cuda.device(a.device):
         rc = load_library().splitk_gemm_bf16_bias(
@@ -468,7 +480,7 @@ def splitk_gemm_bf16_noalloc(a, b, c, split_k: int = 0, stream=None):
     _require_cuda(a, b)
     if c is None:
         raise ValueError("splitk_gemm_bf16_noalloc needs a preallocated output c")
-    c = _out(c, a, M, N, L)
+    c = _out(c, a, M, N, L, stream)
     _require_cuda(c)
     with torch.cuda.device(a.device):
         rc = load_library().splitk_gemm_bf16_noalloc(
@@ -482,7 +494,7 @@ def splitk_gemm_bf16_planned(a, b, c, plan: Plan, flags: int = 0, stream=None):
     import torch
     M, N, K, L = _dims(a, b)
     _require_cuda(a, b)
-    c = _out(c, a, M, N, L)
+    c = _out(c, a, M, N, L, stream)
     _require_cuda(c)
     with torch.cuda.device(a.device):
         rc = load_library().splitk_gemm_bf16_planned(

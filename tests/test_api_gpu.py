@@ -374,3 +374,62 @@ def test_host_io_copy_kernels_chain_calls_in_order(M, N, K, L, split):
         assert sk.splitk_get_status() == 0
         for i in range(3):
             assert np.array_equal(c_hosts[i].view(torch.int16).numpy().view(np.uint16), wants[i]), (pinned, i)
+
+
+def _stream_of_memory(t):
+    at = t.data_ptr()
+    for segment in torch.cuda.memory_snapshot():
+        if segment["address"] <= at < segment["address"] + segment["total_size"]:
+            return segment["stream"]
+    raise AssertionError("no segment holds the tensor")
+
+
+class _Handle:
+    """A stream of another library: nothing but its handle."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_outputs_are_of_the_memory_of_the_stream_given():
+    """A block freed on the current stream may still be in use there, so the
+    output of a call on another stream is none of them."""
+    a, b = to_dev(np.zeros((256, 1024), np.uint16)), to_dev(np.zeros((4, 1024), np.uint16))
+    bias = torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    q4, q8, sc = torch.zeros((256, 512), **u8), torch.zeros((256, 1024), **u8), torch.full((256, 32), 127, **u8)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan4, plan8 = sk.splitk_plan_w4a16(4, 256, 1024), sk.splitk_plan_w8a16(4, 256, 1024)
+    for stream in (s, _Handle(s.cuda_stream)):
+        made = [sk.splitk_gemm_bf16(a, b, stream=stream), sk.splitk_gemm_bf16_bias(a, b, bias, stream=stream),
+                sk.splitk_gemm_bf16_planned(a, b, None, sk.splitk_plan(4, 256, 1024), stream=stream),
+                sk.splitk_gemm_w4a16(q4, sc, b, stream=stream), sk.splitk_gemm_w8a16(q8, sc, b, stream=stream),
+                sk.splitk_gemm_w4a16_planned(q4, sc, b, None, plan4, stream=stream),
+                sk.splitk_gemm_w8a16_planned(q8, sc, b, None, plan8, stream=stream)]
+        assert all(_stream_of_memory(c) == s.cuda_stream for c in made)
+        s.synchronize()
+        assert bool((made[1] == 1).all()) and not any(bool(c.any()) for c in made[:1] + made[2:])
+    current = torch.cuda.current_stream()
+    assert _stream_of_memory(sk.splitk_gemm_bf16(a, b)) == current.cuda_stream
+    with torch.cuda.stream(s):
+        assert _stream_of_memory(sk.splitk_gemm_bf16(a, b)) == s.cuda_stream
+        assert _stream_of_memory(sk.splitk_gemm_bf16(a, b, stream=_Handle(0))) == 0
+    torch.cuda.synchronize()
+    assert sk.splitk_get_status() == 0
+
+
+def test_an_output_is_no_block_that_another_stream_still_writes():
+    a, b = _draw(1, 300, 1024, 1024, 5)
+    a, b = to_dev(a[0]), to_dev(b[0])
+    s = torch.cuda.Stream()
+    ref = sk.splitk_gemm_bf16(a, b)
+    torch.cuda.synchronize()
+    victim = torch.empty_like(ref)
+    torch.cuda._sleep(50_000_000)
+    victim.fill_(7)
+    del victim
+    c = sk.splitk_gemm_bf16(a, b, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(c, ref)
