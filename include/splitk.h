@@ -513,8 +513,8 @@ SPLITK_API int splitk_quantize_i8(const void *x, long long x_stride, void *q, fl
  *   b_q      [L][M][K] token codes, 16-byte aligned;  b_scale  [L][M] f32
  *   bias     [L][N] bf16, or NULL
  *   c        [L][M][N] bf16 or f32 (c_type)
- * K must be a multiple of 16 and at most 2^30; the limits of N and L are those of
- * splitk_gemm_bf16().  The products are exact and summed in f32, so
+ * K must be a multiple of 16; K and M are at most 2^30, and the limits of N and L
+ * are those of splitk_gemm_bf16().  The products are exact and summed in f32, so
  * the sum is exact while its partial sums stay below 2^24 in magnitude (any
  * codes at all up to K = 1024); it is rounded once more, by the output's type.
  */

@@ -84,7 +84,8 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
                               splitk_stream_t stream) {
   if (!a_q || !a_scale || !b_q || !b_scale || !c) return SPLITK_ERR_NULL;
   if (c_type != SPLITK_DTYPE_BF16 && c_type != SPLITK_DTYPE_F32) return SPLITK_ERR_INVALID_ARGUMENT;
-  if (M < 1 || N < 1 || K < 1 || L < 1 || K % 16 != 0 || L > 65535 || N > 65535 * 128 || K > (1 << 30)) {
+  // (M rounded up to whole tiles stays an int)
+  if (M < 1 || N < 1 || K < 1 || L < 1 || K % 16 != 0 || L > 65535 || N > 65535 * 128 || K > (1 << 30) || M > (1 << 30)) {
     return SPLITK_ERR_INVALID_SHAPE;
   }
   // tiles of 128 tokens by 256 weight rows, eight CTAs each at most

@@ -139,3 +139,15 @@ def test_the_binding_refuses_tensors_that_are_not_on_a_gpu():
         sk.splitk_logprobs(cpu)
     with pytest.raises(ValueError, match="device"):
         sk.splitk_rmsnorm_i8(meta(2, 64), torch.zeros(64, dtype=f32))
+
+
+def test_gemm_refuses_token_counts_past_its_index_arithmetic():
+    """Counts of tiles and blocks round M up in 32 bits."""
+    for M in ((1 << 30) + 1, (1 << 31) - 255, (1 << 31) - 1):
+        for N, K in ((1, 16), (16, 64)):
+            assert gemm(M=M, N=N, K=K) == SHAPE, (M, N, K)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses here are not memory")
+def test_gemm_takes_token_counts_up_to_two_to_the_30():
+    assert gemm(M=1 << 30, N=1, K=16) == DEVICE
