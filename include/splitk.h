@@ -517,6 +517,9 @@ SPLITK_API int splitk_quantize_i8(const void *x, long long x_stride, void *q, fl
  * are those of splitk_gemm_bf16().  The products are exact and summed in f32, so
  * the sum is exact while its partial sums stay below 2^24 in magnitude (any
  * codes at all up to K = 1024); it is rounded once more, by the output's type.
+ * Past 2^24 the tensor cores' additions may truncate: the sum is off by at most
+ * (K / 16 + 16) * 2^-23 of the sum of |A * B|, and mostly
+ * towards zero where the products are of one sign.
  */
 SPLITK_API int splitk_gemm_i8(const void *a_q, const float *a_scale, const void *b_q,
                               const float *b_scale, const void *bias, void *c, int c_type,

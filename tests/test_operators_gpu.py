@@ -804,3 +804,22 @@ def test_an_output_is_no_block_that_another_stream_still_writes():
     assert other.data_ptr() != at
     torch.cuda.synchronize()
     assert (other == 3).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 64, 300])
+@pytest.mark.parametrize("K", [2048, 16384, 65536, 262144])
+def test_product_of_codes_of_one_sign(M, K):
+    """Sums far past 2^24, where additions may truncate: within the bound that
+    the header gives, and never above the sum by more than its one rounding to
+    nearest where that is what the additions do (half a unit of 2^-23 an
+    addition of 16 codes)."""
+    g = gen(K + M)
+    a = torch.randint(100, 128, (300, K), device=DEV, generator=g, dtype=torch.int32).to(torch.int8)
+    b = torch.randint(100, 128, (M, K), device=DEV, generator=g, dtype=torch.int32).to(torch.int8)
+    c = sk.splitk_gemm_i8(a, torch.ones(300, device=DEV), b, torch.ones(M, device=DEV), out_dtype=F32).double()
+    total = torch.matmul(b.double(), a.double().T)
+    off = (c - total) / total
+    # (the scales are 1: two products and the output round nothing)
+    most = (K / 16 + 16) * 2.0 ** -23
+    assert off.abs().max().item() <= most
+    assert off.max().item() <= most / 2
