@@ -822,6 +822,9 @@ struct DeviceState {
   int used = 0;
   std::unordered_map<AKey, int, AKeyHash> a_slots;
   std::unordered_map<BKey, CUtensorMap, BKeyHash> b_maps;
+  // Kernels prepared at their first use: a caller of one operator neither waits
+  // for the others nor depends on them.
+  bool i8_ready = false, logprobs_ready = false;
   int i8_clusters[4] = {}, row_clusters[3] = {};           // see DeviceSize
   int max_clusters[9] = {};        // persistent kernel: clusters of 2, 4, 8 resident at once (0: unknown)
 };
@@ -852,8 +855,7 @@ int current_device(DeviceState** out, int* dev_out) {
     }
     if (major != 10 || minor != 3) return SPLITK_ERR_UNSUPPORTED_DEVICE;
     if (!encode_fn()) return SPLITK_ERR_CUDA;
-    if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess ||
-        prepare_logprobs(st.row_clusters) != cudaSuccess || prepare_i8_tile(optin, st.i8_clusters) != cudaSuccess) {
+    if (prepare_kernels(optin) != cudaSuccess || prepare_persistent(optin) != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
@@ -1208,16 +1210,40 @@ void* mapped_device_pointer(const void* host) {
 
 }  // namespace
 
-int require_device(DeviceSize* out) {
+namespace {
+
+// The current device's state with one operator's kernels prepared: `ready` says
+// whether they are, `prepare` does it.
+template <class F>
+int require(DeviceSize* out, bool DeviceState::*ready, F prepare) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   const int rc = current_device(&st, nullptr);
-  if (rc == SPLITK_OK && out) {
-    *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin,
-                      {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2], st->i8_clusters[3]},
-                      {st->row_clusters[0], st->row_clusters[1], st->row_clusters[2]}};
+  if (rc != SPLITK_OK) return rc;
+  if (ready && !(st->*ready)) {
+    if (prepare(*st) != cudaSuccess) {
+      cudaGetLastError();
+      return SPLITK_ERR_CUDA;
+    }
+    st->*ready = true;
   }
-  return rc;
+  *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin,
+                    {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2], st->i8_clusters[3]},
+                    {st->row_clusters[0], st->row_clusters[1], st->row_clusters[2]}};
+  return SPLITK_OK;
+}
+
+}  // namespace
+
+int require_device(DeviceSize* out) {
+  return require(out, nullptr, [](DeviceState&) { return cudaSuccess; });
+}
+int require_i8(DeviceSize* out) {
+  return require(out, &DeviceState::i8_ready,
+                 [](DeviceState& st) { return prepare_i8_tile((int)st.smem_optin, st.i8_clusters); });
+}
+int require_logprobs(DeviceSize* out) {
+  return require(out, &DeviceState::logprobs_ready, [](DeviceState& st) { return prepare_logprobs(st.row_clusters); });
 }
 
 bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows) {
@@ -1594,8 +1620,9 @@ SPLITK_API int splitk_get_fault(splitk_fault_t* out) {
       return SPLITK_ERR_UNSUPPORTED_DEVICE;
     }
     int words_p[kFaultWords] = {0}, words_i[kFaultWords] = {0};
+    const bool i8 = dev >= 0 && dev < kMaxDevices && g_dev[dev].i8_ready;
     if (read_and_clear_fault(words) != cudaSuccess || read_and_clear_fault_persistent(words_p) != cudaSuccess ||
-        read_and_clear_fault_i8(words_i) != cudaSuccess) {
+        (i8 && read_and_clear_fault_i8(words_i) != cudaSuccess)) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }

@@ -95,7 +95,7 @@ SPLITK_API int splitk_gemm_i8(const void* a_q, const float* a_scale, const void*
     return SPLITK_ERR_MISALIGNED;
   }
   DeviceSize dev;
-  int rc = require_device(&dev);
+  int rc = require_i8(&dev);
   if (rc != SPLITK_OK) return rc;
   const I8Params p{static_cast<const int8_t*>(a_q), static_cast<const int8_t*>(b_q), a_scale, b_scale,
                    static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L};

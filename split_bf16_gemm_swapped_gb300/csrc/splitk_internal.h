@@ -165,7 +165,8 @@ cudaError_t read_and_clear_fault_persistent(int* out_words);
 
 // Defined in splitk_host.cu: whether the current device can run this
 // library (SPLITK_OK or SPLITK_ERR_UNSUPPORTED_DEVICE / SPLITK_ERR_CUDA),
-// and its size.
+// and its size; and the same with the kernels of the 8-bit product or of the log
+// probabilities prepared, which the counts of their clusters need.
 struct DeviceSize {
   int num_sms;
   size_t smem_per_sm;
@@ -174,6 +175,8 @@ struct DeviceSize {
   int row_clusters[3];        // clusters of 2, 4 and 8 CTAs of the log probabilities resident at once
 };
 int require_device(DeviceSize* out);
+int require_i8(DeviceSize* out);
+int require_logprobs(DeviceSize* out);
 
 // Defined in splitk_host.cu: a map of [L][rows][K] bytes read in boxes of 128
 // bytes of K by `box_rows` rows, 128-byte swizzle, zeros past the ends; and

@@ -854,7 +854,7 @@ SPLITK_API int splitk_logprobs(const void* logits, int logits_type, long long st
     return SPLITK_ERR_MISALIGNED;
   }
   DeviceSize dev;
-  int rc = require_device(&dev);
+  int rc = require_logprobs(&dev);
   if (rc != SPLITK_OK) return rc;
   const LogprobParams p{logits, stride, tokens, logprob, entropy, top_ids, top_logprobs, M, V, top_k};
   // CTAs sharing a row of 128 KB or more (shorter ones gain less than a cluster

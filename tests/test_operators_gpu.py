@@ -823,3 +823,34 @@ def test_product_of_codes_of_one_sign(M, K):
     most = (K / 16 + 16) * 2.0 ** -23
     assert off.abs().max().item() <= most
     assert off.max().item() <= most / 2
+
+
+FIRST_IN_A_GRAPH = """
+import torch, split_bf16_gemm_swapped_gb300 as sk
+dev = torch.device("cuda:0")
+b = torch.randint(-127, 128, (64, 512), dtype=torch.int32, device=dev).to(torch.int8)
+a = torch.randint(-127, 128, (1000, 512), dtype=torch.int32, device=dev).to(torch.int8)
+sa, sb = torch.rand(1000, device=dev), torch.rand(64, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c = sk.splitk_gemm_i8(a, sa, b, sb)
+    _, h, ids, top = sk.splitk_logprobs(c, top_k=3)
+g.replay()
+torch.cuda.synchronize()
+ref = sk.splitk_gemm_i8(a, sa, b, sb)
+_, h2, ids2, top2 = sk.splitk_logprobs(ref, top_k=3)
+assert torch.equal(c, ref) and torch.equal(h, h2) and torch.equal(ids, ids2) and torch.equal(top, top2)
+assert sk.splitk_get_status() == 0
+print("same")
+"""
+
+
+def test_an_operators_first_call_may_be_captured():
+    """Preparing its kernels is nothing that a capture forbids."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    root = Path(__file__).resolve().parent.parent
+    res = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "same" in res.stdout, res.stdout[-2000:] + res.stderr[-2000:]
