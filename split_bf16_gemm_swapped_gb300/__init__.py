@@ -615,7 +615,8 @@ _OPERATORS = ("splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "spli
 
 
 def __getattr__(name):
-    """The operators around the projection, loaded (with PyTorch) on first use."""
+    """The operators around the projection (their binding, and PyTorch, are
+    loaded by the first call)."""
     if name in _OPERATORS:
         from . import operators
         globals().update({n: getattr(operators, n) for n in _OPERATORS})

@@ -16,8 +16,7 @@ from __future__ import annotations
 
 import importlib.machinery
 import importlib.util
-
-import torch  # noqa: F401  (the binding's types)
+import threading
 
 from . import SplitKError, _build, load_library
 
@@ -34,11 +33,28 @@ def _load():
             "(python -c 'import __graft_entry__ as g; g.build()')")
     loader = importlib.machinery.ExtensionFileLoader("_operators", str(path))
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_operators", loader))
+    import torch  # noqa: F401  (the binding's types)
     loader.exec_module(module)
     return module
 
 
-_native = _load()
+class _Unloaded:
+    """Stands for the binding until the first call: the names of this module need
+    neither PyTorch nor the built binding."""
+
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        global _native
+        if name.startswith("__"):
+            raise AttributeError(name)
+        with self._lock:
+            if _native is self:
+                _native = _load()
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
 
 
 def splitk_rmsnorm_i8(x, weight, residual=None, eps: float = 1e-6, q=None, scale=None, residual_out=None,

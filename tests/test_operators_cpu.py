@@ -151,3 +151,48 @@ def test_gemm_refuses_token_counts_past_its_index_arithmetic():
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses here are not memory")
 def test_gemm_takes_token_counts_up_to_two_to_the_30():
     assert gemm(M=1 << 30, N=1, K=16) == DEVICE
+
+
+UNBUILT = """
+import sys
+sys.modules["torch"] = None                       # an import of it raises
+from pathlib import Path
+from split_bf16_gemm_swapped_gb300 import _build
+_build.OPERATORS_LIB = Path({missing!r})
+import split_bf16_gemm_swapped_gb300 as sk
+from split_bf16_gemm_swapped_gb300 import *
+assert all(hasattr(sk, name) for name in sk.__all__)
+assert splitk_logprobs is sk.splitk_logprobs and splitk_logprobs.__doc__
+print("imported")
+"""
+
+
+def test_the_names_need_neither_pytorch_nor_the_binding(tmp_path):
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = UNBUILT.format(missing=str(tmp_path / "missing.so"))
+    res = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                         text=True, timeout=300)
+    assert res.returncode == 0 and "imported" in res.stdout, res.stderr[-2000:]
+
+
+def test_a_call_without_the_binding_raises(tmp_path):
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = f"""
+from pathlib import Path
+from split_bf16_gemm_swapped_gb300 import _build
+_build.OPERATORS_LIB = Path({str(tmp_path / "missing.so")!r})
+import torch, split_bf16_gemm_swapped_gb300 as sk
+for call in (lambda: sk.splitk_quantize_i8(torch.zeros(1, 8)), lambda: sk.splitk_logprobs(torch.zeros(1, 8))):
+    try:
+        call()
+    except RuntimeError as e:
+        assert "missing" in str(e), e
+        print("raised")
+"""
+    res = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                         text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.count("raised") == 2, res.stderr[-2000:]
