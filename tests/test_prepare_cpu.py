@@ -123,9 +123,10 @@ def library(tmp_path_factory):
     with ThreadPoolExecutor() as pool:
         for res in pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs):
             assert res.returncode == 0, res.stderr[-3000:]
+    # (its calls go to the fakes, whatever CUDA runtime the process holds)
     so = where / "libfake.so"
     res = subprocess.run(["g++", "-shared", "-o", str(so), *(str(where / f) for f in ("host.o", "i8.o", "kernels.o", "runtime.o")),
-                          "-Wl,-z,defs", "-lpthread"], capture_output=True, text=True)
+                          "-Wl,-z,defs,-Bsymbolic", "-lpthread"], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-3000:]
     return so
 
