@@ -6,15 +6,18 @@
 * ``_lib/_operators.so``: the Python binding of the operators around the
   projection (C++ on PyTorch's headers, g++), linked to the first.
 
-Each is rebuilt when a source is newer than the library.  Host code is
+Each is rebuilt when a source is newer than the library, and the binding also
+when PyTorch or Python is another than it was built for.  Host code is
 portable C/C++ (no x86 intrinsics, no -march=native), so the same sources
 build on x86_64 and aarch64.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -27,6 +30,7 @@ LIBDIR = PKG / "_lib"
 SPLITK_LIB = LIBDIR / "libsplitk_sm103a.so"
 SYNTHETIC_LIB = LIBDIR / "libsynthetic.so"
 OPERATORS_LIB = LIBDIR / "_operators.so"
+OPERATORS_STAMP = LIBDIR / "_operators.abi"         # what it was built for
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -104,13 +108,26 @@ def build_splitk(force: bool = False, verbose_ptxas: bool = False) -> Path:
     return SPLITK_LIB
 
 
+def operators_abi() -> str:
+    """The PyTorch (whose C++ types the binding uses) and the Python it is built
+    for."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        from torch import __version__ as version
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def operators_built_for() -> str:
+    return OPERATORS_STAMP.read_text() if OPERATORS_STAMP.exists() else ""
+
+
 def build_operators(force: bool = False) -> Path:
     LIBDIR.mkdir(parents=True, exist_ok=True)
     src = CSRC / "operators_binding.cpp"
-    if not (force or _stale(OPERATORS_LIB, [src, INCLUDE / "splitk.h"])):
+    abi = operators_abi()
+    if not (force or _stale(OPERATORS_LIB, [src, INCLUDE / "splitk.h"]) or operators_built_for() != abi):
         return OPERATORS_LIB
-    import sysconfig
-
     import torch
     home = Path(torch.__file__).resolve().parent
     cuda = Path(_nvcc()).resolve().parent.parent
@@ -122,7 +139,10 @@ def build_operators(force: bool = False) -> Path:
           *[x for i in includes for x in ("-isystem" if str(i).startswith(str(home)) else "-I", str(i))],
           str(src), "-o", str(tmp), f"-L{LIBDIR}", f"-l:{SPLITK_LIB.name}", f"-L{home / 'lib'}",
           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+    # (a build cut short between the two leaves no stamp: built again)
+    OPERATORS_STAMP.unlink(missing_ok=True)
     os.replace(tmp, OPERATORS_LIB)
+    OPERATORS_STAMP.write_text(abi)
     return OPERATORS_LIB
 
 

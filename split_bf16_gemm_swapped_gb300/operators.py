@@ -31,6 +31,10 @@ def _load():
         raise RuntimeError(
             f"{path} is missing: build the binding first "
             "(python -c 'import __graft_entry__ as g; g.build()')")
+    if _build.operators_built_for() != _build.operators_abi():
+        raise RuntimeError(
+            f"{path} was built for another PyTorch or Python ({_build.operators_built_for() or 'unknown'}; this is "
+            f"{_build.operators_abi()}): build it again (python -c 'import __graft_entry__ as g; g.build()')")
     loader = importlib.machinery.ExtensionFileLoader("_operators", str(path))
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_operators", loader))
     import torch  # noqa: F401  (the binding's types)

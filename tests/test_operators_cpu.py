@@ -196,3 +196,43 @@ for call in (lambda: sk.splitk_quantize_i8(torch.zeros(1, 8)), lambda: sk.splitk
     res = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
                          text=True, timeout=300)
     assert res.returncode == 0 and res.stdout.count("raised") == 2, res.stderr[-2000:]
+
+
+def test_the_binding_is_built_again_for_another_pytorch(monkeypatch, tmp_path):
+    """It uses PyTorch's C++ types: newer than its sources is not enough."""
+    lib, built = tmp_path / "_operators.so", []
+    monkeypatch.setattr(_build, "OPERATORS_LIB", lib)
+    monkeypatch.setattr(_build, "OPERATORS_STAMP", tmp_path / "_operators.abi", raising=False)
+
+    def compile(cmd, cwd=None):
+        from pathlib import Path
+        built.append(cmd)
+        Path(cmd[cmd.index("-o") + 1]).write_bytes(b"")
+
+    monkeypatch.setattr(_build, "_run", compile)
+    for _ in range(2):
+        _build.build_operators()
+    assert len(built) == 1 and lib.exists()
+    version = _build.importlib.metadata.version
+    monkeypatch.setattr(_build.importlib.metadata, "version",
+                        lambda name: "0.0.1" if name == "torch" else version(name))
+    for _ in range(2):
+        _build.build_operators()
+    assert len(built) == 2
+    soabi = _build.sysconfig.get_config_var
+    monkeypatch.setattr(_build.sysconfig, "get_config_var",
+                        lambda name: "other" if name == "SOABI" else soabi(name))
+    for _ in range(2):
+        _build.build_operators()
+    assert len(built) == 3
+
+
+def test_a_binding_of_another_pytorch_is_not_loaded(monkeypatch, tmp_path):
+    from split_bf16_gemm_swapped_gb300 import operators
+    stamp = tmp_path / "_operators.abi"
+    monkeypatch.setattr(_build, "OPERATORS_STAMP", stamp, raising=False)
+    for text in (None, "torch 0.0.1, other"):
+        if text:
+            stamp.write_text(text)
+        with pytest.raises(RuntimeError, match="another PyTorch"):
+            operators._load()
