@@ -122,7 +122,15 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31u) == 0) dev::mbar_arrive(bar);
 }
 
-// The same on a barrier of another CTA of the pair.  The release is at CTA
+// A raw slot whose codes the warp has loaded is free for the next tile's copy.
+// The copy is of the async proxy, and an arrival alone does not hold it back
+// until loads that are still under way have read the slot: each lane's fence does.
+__device__ __forceinline__ void warp_free(uint32_t bar) {
+  dev::fence_proxy_async_shared();
+  warp_arrive(bar);
+}
+
+// An arrival on a barrier of another CTA of the pair.  The release is at CTA
 // scope: what it publishes (tensor memory, and shared memory fenced to the
 // async proxy) is read by the MMA from this CTA's own memories, not by the
 // waiting thread.  (At cluster scope it waits ~1,250 clocks for every
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (uint32_t j = 0; j < 8; ++j) {
         dev::ld_shared_v4(src + ((j ^ (row & 7u)) << 4), c[j][0], c[j][1], c[j][2], c[j][3]);
       }
-      warp_arrive(bar_free + 8u * in.index);
+      warp_free(bar_free + 8u * in.index);
       if (kt >= kBufs &&
           !__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_used + 8u * out.index, out.phase ^ 1u, kRoleEpiDecode, kt))) break;
       dev::tc_fence_after();
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (uint32_t j = 0; j < kPer; ++j) {
         dev::ld_shared_v4(src + (((first + j) ^ (row & 7u)) << 4), c[j][0], c[j][1], c[j][2], c[j][3]);
       }
-      warp_arrive(bar_free + 8u * in.index);
+      warp_free(bar_free + 8u * in.index);
       if (kt >= kBufs &&
           !__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_used + 8u * out.index, out.phase ^ 1u, kRoleEpiDecode, kt))) break;
       const uint32_t dst = s_f + (uint32_t)out.index * f16_b(kTok) + row * 128u;

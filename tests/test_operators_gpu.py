@@ -854,3 +854,24 @@ def test_an_operators_first_call_may_be_captured():
     root = Path(__file__).resolve().parent.parent
     res = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH], cwd=root, capture_output=True, text=True, timeout=300)
     assert res.returncode == 0 and "same" in res.stdout, res.stdout[-2000:] + res.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M,N,K,runs", [(64, 18432, 1024, 6000), (64, 18432, 1280, 2000), (20, 18432, 1024, 2000),
+                                        (20, 18432, 2048, 1000), (128, 14336, 1024, 2000), (128, 7168, 2048, 1000),
+                                        (256, 18432, 1024, 1000), (300, 7168, 2048, 500), (1000, 4100, 1040, 300)])
+def test_every_run_of_the_tiles_is_exact(M, N, K, runs):
+    """A tile's codes are all read before the next tile's copy takes their place,
+    and what one CTA of a pair converts is there when the other's MMAs read it:
+    in each of many runs (the sums are whole numbers below 2^24)."""
+    g = gen(M + N)
+    a, b = codes((N, K), g), codes((M, K), g)
+    one = torch.ones(N, device=DEV), torch.ones(M, device=DEV)
+    ref = torch.matmul(b.double(), a.double().T).float()
+    c = torch.empty((M, N), device=DEV)
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(runs):
+        c.fill_(0.5)
+        sk.splitk_gemm_i8(a, one[0], b, one[1], c=c)
+        wrong += (c != ref).any()
+    assert wrong.item() == 0
+    assert sk.splitk_get_status() == 0
