@@ -51,6 +51,17 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
                : "memory");
 }
 
+// The arrival alone; what it publishes is released by a fence before it.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Releases at cluster scope what was written to this CTA's shared memory, and
+// that alone.
+__device__ __forceinline__ void fence_release_shared_cluster() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
 // try_wait with a suspend-time hint: a waiting thread sleeps until the phase
 // completes or `hint_ns` passes, instead of spinning on the barrier and
 // taking issue slots from the warps that do the work.

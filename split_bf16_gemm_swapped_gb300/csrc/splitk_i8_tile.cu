@@ -130,15 +130,18 @@ __device__ __forceinline__ void warp_free(uint32_t bar) {
   warp_arrive(bar);
 }
 
-// An arrival on a barrier of another CTA of the pair.  The release is at CTA
-// scope: what it publishes (tensor memory, and shared memory fenced to the
-// async proxy) is read by the MMA from this CTA's own memories, not by the
-// waiting thread.  (At cluster scope it waits ~1,250 clocks for every
-// outstanding memory operation.)
-__device__ __forceinline__ void warp_arrive_pair(uint32_t cluster_bar) {
+// An arrival on a barrier of the pair's leader, which issues the MMAs that read what
+// the warp has written to this CTA's memories.  For tensor memory the arrival is
+// enough: the tcgen05 fences on either side order it.  Shared memory (fenced to
+// the async proxy by each lane) is released at cluster scope, which the leader's
+// wait acquires at; by a fence of shared memory alone, since an arrival's own
+// release waits ~1,250 clocks for every outstanding memory operation (1000 x 7168 x
+// 16384: 268 us then, or 150 with threads of their own to release it).
+__device__ __forceinline__ void warp_arrive_pair(uint32_t cluster_bar, bool shared) {
   __syncwarp();
   if ((threadIdx.x & 31u) == 0) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    if (shared) dev::fence_release_shared_cluster();
+    dev::mbar_arrive_remote_relaxed(cluster_bar);
   }
 }
 
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       RingPos pos = RingPos::at(first, kBufs);
       for (int kt = first; kt < k_tiles; kt += kIssuers, pos.advance(kIssuers, kBufs)) {
         const uint32_t i = (uint32_t)pos.index;
-        if (!__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_ready + 8u * i, pos.phase, kRoleMma, kt))) break;
+        if (!__all_sync(0xFFFFFFFFu, waiter.wait<true>(bar_ready + 8u * i, pos.phase, kRoleMma, kt))) break;
         dev::tc_fence_after();
         const uint64_t b_d = dev::smem_desc_advance(b_desc, i * f16_b(kTok));
         const uint32_t a_t = base_col + a_col0(kTok) + i * kATmemCols;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       dev::tmem_wait_st();
       dev::tc_fence_before();
-      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index);
+      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index, false);
     }
   } else if (warp >= kConvB0) {
     // tokens: 128 / half threads a row, each kPer of its 16-code chunks
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         dev::st_shared_v4(at + (((chunk + 1u) ^ (row & 7u)) << 4), f[4], f[5], f[6], f[7]);
       }
       dev::fence_proxy_async_shared();
-      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index);
+      if (report) warp_arrive_pair(ready_of_leader + 8u * out.index, true);
     }
   }
 
