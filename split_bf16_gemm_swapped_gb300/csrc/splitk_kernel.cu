@@ -370,9 +370,13 @@ __global__ void __launch_bounds__(kDecWG == 2 ? kThreadsW4Wide : kThreads, kDecW
     if (lane == 0) dev::mbar_arrive(bar);
   };
   // Tile kt's codes (ring stage `stage`) read into registers: the stage may
-  // take tile kt + stages (no arrival when there is none).
+  // take tile kt + stages (no arrival when there is none).  The copy that fills
+  // it is of the async proxy, so each lane's loads are fenced to that before
+  // the arrival.
   auto code_free = [&](int kt, int stage) {
-    if (kt + stages < k_tiles) warp_arrive(bar_empty0 + 8u * (uint32_t)stage);
+    if (kt + stages >= k_tiles) return;
+    dev::fence_proxy_async_shared();
+    warp_arrive(bar_empty0 + 8u * (uint32_t)stage);
   };
 
   if (warp == 0) {

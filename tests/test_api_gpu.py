@@ -433,3 +433,23 @@ def test_an_output_is_no_block_that_another_stream_still_writes():
     s.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(c, ref)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M,N,K,split", [(1, 18432, 7168, 0), (16, 4096, 7168, 8), (32, 7168, 4096, 4)])
+def test_quantized_products_give_one_result_in_many_runs(bits, M, N, K, split):
+    """A ring stage's codes are all read before the copy of the next tile takes
+    their place."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + N + bits)
+    aq = torch.randint(0, 120, (N, K * bits // 8), device=DEV, generator=g, dtype=torch.int32).to(torch.uint8)
+    scale = torch.randint(118, 124, (N, K // 32), device=DEV, generator=g, dtype=torch.int32).to(torch.uint8)
+    b = torch.randn((M, K), device=DEV, generator=g).to(torch.bfloat16)
+    gemm = sk.splitk_gemm_w4a16 if bits == 4 else sk.splitk_gemm_w8a16
+    first = gemm(aq, scale, b, split_k=split)
+    c, differ = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(500):
+        gemm(aq, scale, b, c=c, split_k=split)
+        differ += (c != first).any()
+    assert differ.item() == 0 and bool(torch.isfinite(first).all())
+    assert sk.splitk_get_status() == 0
