@@ -875,3 +875,67 @@ def test_every_run_of_the_tiles_is_exact(M, N, K, runs):
         wrong += (c != ref).any()
     assert wrong.item() == 0
     assert sk.splitk_get_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 4, 128])
+def test_rows_before_a_wide_down_projection(M):
+    D = 53248
+    g = gen(M)
+    x = randn((M, D), g, BF16)
+    q, scale = sk.splitk_quantize_i8(x)
+    ref_q, ref_s = plain_codes(x)
+    assert torch.equal(scale, ref_s) and torch.equal(q, ref_q)
+    check_norm(x, randn((M, D), g, BF16), randn((D,), g, F32))
+
+
+@pytest.mark.parametrize("N,K", [(32000, 2048), (50257, 1024), (131072, 1040)])
+@pytest.mark.parametrize("M", [1, 12, 40, 130])
+def test_product_of_a_vocabulary_head(M, N, K):
+    a, sa, b, sb, bias = product_inputs(1, M, N, K, M + N, batched=False)
+    check_product(a, sa, b, sb, bias=bias if M == 12 else None, out=F32 if M == 40 else BF16)
+
+
+def test_the_chain_in_threads_on_streams_of_their_own():
+    """Each thread runs the chain on its own stream while the others do, with
+    tokens enough for either product kernel, and gets what it gets alone."""
+    import threading
+    D, V, steps = 1024, 4000, 60
+    g = gen(40)
+    a, sa = sk.splitk_quantize_i8(randn((V, D), g, BF16, 0.05))
+    w = randn((D,), g, F32)
+    inputs = [(randn((M, D), g, BF16), randn((M, D), g, BF16)) for M in (1, 8, 40, 200)]
+
+    def chain(x, r, **kw):
+        q, s, out = sk.splitk_rmsnorm_i8(x, w, r, **kw)
+        logits = sk.splitk_gemm_i8(a, sa, q, s, out_dtype=F32, **kw)
+        return (q, s, out, logits, *sk.splitk_logprobs(logits, top_k=7, **kw)[1:])
+
+    alone = [[t.clone() for t in chain(x, r)] for x, r in inputs]
+    torch.cuda.synchronize()
+    wrong, errors = [0] * len(inputs), []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for step in range(steps):
+                # the stream given, or the thread's current one
+                if step % 2:
+                    got = chain(*inputs[i], stream=s)
+                else:
+                    with torch.cuda.stream(s):
+                        got = chain(*inputs[i])
+                s.synchronize()
+                wrong[i] += not all(torch.equal(u, v) for u, v in zip(got, alone[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                      # a thread's exception fails the test, not the thread alone
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(inputs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert wrong == [0] * len(inputs)
+    torch.cuda.synchronize()
+    assert sk.splitk_get_status() == 0
