@@ -60,7 +60,9 @@ double plan_tiles(int M, int N, int K, int L, const DeviceSize& dev, I8Plan* out
 // warp, 2.6 for four (each weight is converted once, each token fragment for every
 // 16 weight rows).  With four, two CTAs an SM take 1 us and 1.25 for each 1024 of K
 // (streamed and in tiles: 17 x 2048 x 16384 23.1 us and 15.5, 17 x 18432 x 256 9.2
-// and 5.2, 64 x 2048 x 1024 3.9 and 6.9, 256 x 500 x 4096 7.8 and 9.5).
+// and 5.2, 64 x 2048 x 1024 3.9 and 6.9, 256 x 500 x 4096 7.8 and 9.5; of 150 sizes from
+// 33 x 64 x 64 to 1000 x 4096 x 4096 one is chosen wrongly by more than 3 %: 64 x 4096 x
+// 1024 6.4 and 6.2).
 bool streams(int M, int N, int K, int L, double tile_time, int num_sms) {
   if (M <= 8) return true;
   const double codes = (double)N * K * L;

@@ -15,9 +15,10 @@
 // A pair halves the token side for each SM.  With one CTA a tile, 128 tokens
 // took ~1,050 clocks a K tile (1,024 by that count; 512 the MMAs alone).  Pairs
 // take ~690 for 128 tokens, and ~1,020 for 256, where the MMAs (1,024) bound it:
-// 1000 x 7168 x 16384 in 128 us, 94 % of the measured bf16 rate.  Up to 64 tokens
-// the weights' arrival bounds it: 64 x 18432 x 7168 in 24.9 us, 81 % of the copy rate
-// (5 us of that before the first MMA and after the last).
+// 1000 x 7168 x 16384 in 128 us, 94 % of the measured bf16 rate (one call after another
+// runs into the power cap: 139).  Up to 64 tokens the weights' arrival bounds it: 64 x
+// 18432 x 7168 in 25.3 us, 80 % of the copy rate (5 us of that before the first MMA and
+// after the last).
 //
 // `split` pairs of a cluster may share one output tile, each taking a
 // contiguous run of K tiles; each CTA leaves its f32 sums in its own shared

@@ -15,8 +15,8 @@
 // it, from the row's start.
 //
 // Memory bounds the pass (1024 x 131072 bf16: 46 us without alternatives, 87 % of
-// the copy rate); each row's join and selection, some 3 us of latencies, is what
-// 20 alternatives add (52 us), as it overlaps only with other rows' passes.  Rows of
+// the copy rate); each row's join and selection is what 20 alternatives add (6 us of
+// a launch: 52), as it overlaps only with other rows' passes.  Rows of
 // a few thousand logits are bound by the instructions of either (4096 x 8000: 19
 // us and 35, the copy rate 10).
 //
@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) logprobs_kernel(cons
   if (threadIdx.x == 0) s_groups = s_count = 0;
   const bool some = p.k > 0;
   // k close to 32 would make the bound the least warp's (1024 x 131072 bf16, top 32:
-  // 67 us, of 64 values 56; rows of few groups have few logits a lane to choose from:
-  // 4096 x 1000 22.6 us, of 64 25.5)
+  // 64 us, of 64 values 56; rows of few groups have few logits a lane to choose from:
+  // 4096 x 1000 22.6 us, of 64 25.5; rows masked to some 20 logits pay 0.3-1.2 us for
+  // it: 1 x 131072 7.6 and 8.8, 65 x 50001 f32 9.5 and 10.1)
   const bool wide = p.k > 24 && n > 24;
   if (some && split == 1) top_lanes<kWarps>(order_of(lane_top), wide, warp, lane, s_some);
   __syncthreads();

@@ -6,10 +6,14 @@
 //   s = max(max|n| (1/127), 2^-126);  q = rne(n / s), the f32 quotient
 //
 // max|n| = max|y w| / rms, so one joint reduction of (sum y^2, max|y w|) over
-// the row gives both statistics, and the row's values z = y w stay in
-// registers between reading and coding: every byte is read and written once, and
-// memory is the bound (2048 x 7168 with a bf16 residual 16.8 us, 92 % of the copy
-// rate; 18432 x 7168 codes 74 us, 80 %).  Sums and statistics are f32; a code is
+// the row gives both statistics, and the row's values z = y w stay on
+// chip between reading and coding: every byte is read and written once (up to
+// 32768 features; longer rows are read twice, long_rows_kernel), and memory is
+// the bound (2048 x 7168 with a bf16 residual 16.8 us, 92 % of the copy
+// rate; 18432 x 7168 codes 74 us, 80 %).  Up to 16384 features in vectors they stay in
+// registers; with four vectors a thread some spill (a thread's bytes: 30 at most
+// without a residual, 260-310 with one: 64 x 20000 6.4 us, 1.3 the copy's), and so they
+// do in odd_rows_kernel (50-90).  Sums and statistics are f32; a code is
 // rounded by adding 1.5 * 2^23 (the sum's low byte is then the two's complement
 // code, rounded to nearest even).
 
@@ -166,7 +170,7 @@ struct RowCodes {
 //
 // Rows and weight in 16-byte vectors.  A CTA takes row after row; the next row's
 // words are on their way while this one is reduced and coded, so that loads are
-// in flight all the time (18432 x 7168 codes, a CTA a row: 103 us, so 73).
+// in flight all the time (18432 x 7168 codes, a CTA a row: 103 us, so 74).
 template <int kRes, int kW, int kVecs>
 __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p) {
   constexpr bool kNext = kVecs <= 2;     // registers for the next row's words
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rows_kernel(const RowParams p)
 // Rows of any width and alignment, an element at a time (lane by lane, so that
 // a warp's loads are consecutive), kEach of them a thread.  With a residual two
 // thousand threads an SM (32 registers) serve better than half as many: 333 x 4999,
-// f32, 8.8 us and 11.6; without one the loads want the registers: 2000 x 5001 codes
+// f32, 8.9 us and 11.6, spills of 52 bytes included; without one the loads want the registers: 2000 x 5001 codes
 // 20 us and 17.
 template <int kRes, int kW, int kEach>
 __global__ void __launch_bounds__(kMaxRowThreads, kRes != 0 && kEach == 8 ? 2 : 1) odd_rows_kernel(const RowParams p) {
