@@ -939,3 +939,53 @@ def test_the_chain_in_threads_on_streams_of_their_own():
     assert wrong == [0] * len(inputs)
     torch.cuda.synchronize()
     assert sk.splitk_get_status() == 0
+
+
+def guarded(shape, dtype, value):
+    """A contiguous output inside a buffer full of `value`, and what is around it."""
+    n = math.prod(shape)
+    room = torch.full((n + 64,), value, dtype=dtype, device=DEV)
+    return room[32:32 + n].view(shape), (room[:32], room[32 + n:])
+
+
+def untouched(guards, value):
+    return all(bool((g == value).all()) for g in guards)
+
+
+@pytest.mark.parametrize("M,D", [(1, 1), (3, 77), (5, 512), (130, 7168), (2, 16392), (3, 40001)])
+def test_norm_and_codes_write_their_outputs_and_nothing_else(M, D):
+    g = gen(M + D)
+    x, r, w = randn((M, D), g, BF16), randn((M, D), g, F32), randn((D,), g, F32)
+    (q, gq), (s, gs), (out, go) = guarded((M, D), torch.int8, 99), guarded((M,), F32, 7.0), guarded((M, D), F32, 7.0)
+    sk.splitk_rmsnorm_i8(x, w, r, q=q, scale=s, residual_out=out)
+    torch.cuda.synchronize()
+    assert untouched(gq, 99) and untouched(gs, 7.0) and untouched(go, 7.0)
+    ref = sk.splitk_rmsnorm_i8(x, w, r)
+    assert torch.equal(q, ref[0]) and torch.equal(s, ref[1]) and torch.equal(out, ref[2])
+    sk.splitk_quantize_i8(x, q=q, scale=s)
+    torch.cuda.synchronize()
+    assert untouched(gq, 99) and untouched(gs, 7.0)
+
+
+@pytest.mark.parametrize("M,V,k", [(1, 5, 5), (3, 1000, 20), (200, 4100, 32), (2, 131072, 32), (700, 8000, 1)])
+def test_logprobs_write_their_outputs_and_nothing_else(M, V, k):
+    g = gen(M + V)
+    t = torch.randint(0, V, (M,), device=DEV, generator=g)
+    for fill in (None, float("nan"), float("-inf")):
+        x = randn((M, V), g, BF16, 3.0)
+        if fill is not None:
+            x[:, V // 2:] = fill
+        (lp, g0), (h, g1) = guarded((M,), F32, 7.0), guarded((M,), F32, 7.0)
+        (ids, g2), (tops, g3) = guarded((M, k), torch.int64, 7), guarded((M, k), F32, 7.0)
+        sk.splitk_logprobs(x, t, top_k=k, logprob=lp, entropy=h, top_ids=ids, top_logprobs=tops)
+        torch.cuda.synchronize()
+        assert all(untouched(gd, 7) for gd in (g0, g1, g2, g3))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_logprobs_of_the_largest_vocabulary(dtype):
+    V = 1 << 22
+    g = gen(22)
+    x = randn((2, V), g, dtype, 3.0)
+    x[1, 1000:] = float("-inf")
+    check_logprobs(x, torch.tensor([V - 1, 3], device=DEV), 32)
