@@ -203,7 +203,8 @@ _TABLE = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, 
 def _unpacked(codes, scale, dtype=F32):
     table = torch.tensor(_TABLE, device=codes.device, dtype=dtype)
     q = torch.stack((codes & 15, codes >> 4), dim=-1).flatten(-2)
-    return _values(table[q.int()], torch.exp2(scale.to(dtype) - 127))
+    power = (scale.int() << 23).view(F32) if dtype == F32 else ((scale.long() + 896) << 52).view(F64)
+    return _values(table[q.int()], power)
 
 
 def _plain_quantise(s):
@@ -296,7 +297,7 @@ def exact(case, seed):
             b = v.reshape(len(v), -1, BLOCK)
             top = b.abs().max(2).values.clamp_min(2.0 ** -124)
             floor = torch.floor(torch.log2(top))
-            power = torch.ldexp(torch.ones_like(top), floor)
+            power = ((floor.long() + 1023) << 52).view(F64)
             # (a power of two's logarithm may be a bit off)
             scale = torch.where(power > top, power / 2, torch.where(2 * power <= top, 2 * power, power)) / 4
             q = (b / scale[..., None]).abs()
