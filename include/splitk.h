@@ -548,6 +548,115 @@ SPLITK_API int splitk_logprobs(const void *logits, int logits_type, long long st
                                int V, splitk_stream_t stream);
 
 /*
+ * ---- A decode step in 4 bits: microscaled codes, and the logits' adjustment ----
+ *
+ * Rows of values as the codes that splitk_gemm_w4a16() takes for its weights (the
+ * OCP MXFP4 format): E2M1 codes, low nibble first, and an E8M0 scale code for 32
+ * consecutive ones.  splitk_quantize_mx4() makes them from weights or activations,
+ * splitk_rmsnorm_mx4() from a projection's output, splitk_gemm_mx4() multiplies two
+ * operands held so, and splitk_dequantize_mx4() gives their values back (weights for
+ * a product in bf16).  splitk_adjust_logits() stands between the last projection and
+ * splitk_logprobs().
+ *
+ * As with the calls above: they own no memory, keep nothing between calls, read
+ * nothing before the work ahead of them in the stream has completed, and their
+ * buffers must not overlap, except as said.
+ */
+
+/*
+ * Rows of K values (a multiple of 32; M and K at most 2^30) as codes:
+ *     s = max(floor(log2(max|x|)) - 2, -126) for each block of 32
+ *     scale code = s + 127 (1..252)
+ *     code = x / 2^s rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with its
+ *            sign, ties to the even code, at most 6
+ * exactly.  A block that holds a NaN or an infinity has scale code 255 (not a
+ * number) and codes 0.
+ *   x       bf16, f16 or f32 (x_type), rows x_stride elements apart (x_stride >= K)
+ *   codes   [M][K / 2] bytes, 16-byte aligned;  scale  [M][K / 32] bytes
+ */
+SPLITK_API int splitk_quantize_mx4(const void *x, int x_type, long long x_stride, void *codes,
+                                   void *scale, int M, int K, splitk_stream_t stream);
+
+/*
+ * The values that codes stand for: [M][K] bf16, f16 or f32 (out_type), 16-byte
+ * aligned.  In bf16 and f32 they are exact (but for scale codes 253 and 254, whose
+ * largest values pass both ranges and are infinite); scale code 0 is 2^-127, 255 NaN.
+ */
+SPLITK_API int splitk_dequantize_mx4(const void *codes, const void *scale, void *out, int out_type,
+                                     int M, int K, splitk_stream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and codes, for M rows (tokens) of D
+ * features (a multiple of 32), each at most 2^30:
+ *     y = x[m] + residual[m]                               (f32)
+ *     residual_out[m] = y                                  (rounded to its type)
+ *     n = y * weight * (1 / sqrt(mean(y^2) + eps))         (f32, in this order)
+ *     codes and scales of n as in splitk_quantize_mx4()
+ * Arguments as in splitk_rmsnorm_i8(), codes and scale as above.  A row that holds
+ * a NaN or an infinity, or whose sum of squares passes the f32 range, has scale
+ * codes 255.
+ */
+SPLITK_API int splitk_rmsnorm_mx4(const void *x, long long x_stride, const void *residual,
+                                  void *residual_out, int residual_type, const void *weight,
+                                  int weight_type, float eps, void *codes, void *scale, int M,
+                                  int D, splitk_stream_t stream);
+
+/*
+ * Matrix product of two operands in codes:
+ *     C[l][m][n] = round( sum_k A[l][n][k] * B[l][m][k]  + bias[l][n] )
+ * A and B the values that their codes and scales stand for.
+ *   a_q      [L][N][K / 2] weight codes, 16-byte aligned;  a_scale  [L][N][K / 32]
+ *   b_q      [L][M][K / 2] token codes, 16-byte aligned;   b_scale  [L][M][K / 32]
+ *   bias     [L][N] bf16, or NULL
+ *   c        [L][M][N] bf16 or f32 (c_type)
+ * K must be a multiple of 32; K and M are at most 2^30, and the limits of N and L
+ * are those of splitk_gemm_bf16().  Products are exact; sums are f32, whose additions
+ * may truncate.  A row of A with a scale code 255 makes its column of C NaN, a row of
+ * B its row.
+ */
+SPLITK_API int splitk_gemm_mx4(const void *a_q, const void *a_scale, const void *b_q,
+                               const void *b_scale, const void *bias, void *c, int c_type, int M,
+                               int N, int K, int L, splitk_stream_t stream);
+
+/* How splitk_adjust_logits() changes the logits; NULL and 0 leave a part out. */
+typedef struct splitk_adjust_t {
+    const long long *history;        /* [M][history_length] tokens so far             */
+    const long long *lengths;        /* [M] how many of them each row has, or NULL: all;
+                                        taken as 0..history_length                    */
+    const long long *prompt_lengths; /* [M] how many of those are the prompt's, or
+                                        NULL: none                                    */
+    const float *repetition;         /* [M] > 0                                       */
+    const float *presence;           /* [M]                                           */
+    const float *frequency;          /* [M]                                           */
+    const long long *bias_ids;       /* [M][bias_count] tokens                        */
+    const float *bias_values;        /* [M][bias_count]                               */
+    const int *allowed;              /* [M][(V + 31) / 32]: bit v % 32 of word v / 32
+                                        set where token v may come next               */
+    int history_length;              /* at most 2^30                                  */
+    int bias_count;                  /* at most 1024                                  */
+} splitk_adjust_t;
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on M rows of V logits
+ * (V <= 2^22), each step an f32 operation of its own:
+ *     in the row's history:       x = x > 0 ? x / repetition : x * repetition
+ *     behind its prompt, `count`
+ *     times there:                x = x - frequency * count;  x = x - presence
+ *     among its bias_ids:         x = x + bias
+ *     not allowed:                x = -inf
+ * rounded once more to the logits' type.  A token that is listed more than once
+ * among bias_ids has the sum of its biases, added in the list's order.  Tokens
+ * outside 0..V-1 (padding) count nowhere.  Logits that are -inf or NaN stay so
+ * unless the above changes them; a row that allows nothing is -inf throughout.
+ *   logits  bf16, f16 or f32 (type), rows `stride` elements apart (stride >= V)
+ *   out     of the same type, rows out_stride apart; may be `logits` itself, at the
+ *           same stride
+ */
+SPLITK_API int splitk_adjust_logits(const void *logits, int type, long long stride,
+                                    const splitk_adjust_t *how, void *out, long long out_stride,
+                                    int M, int V, splitk_stream_t stream);
+
+/*
  * Diagnostic record of the first bounded wait that ran out on the current
  * device since the last read (the Muse Spark AMD dev page's _spin_bounded:
  * every wait is bounded, the first timeout leaves a record and a sticky
@@ -590,7 +699,7 @@ SPLITK_API int splitk_set_wait_limit_ns(uint64_t ns);
  * reports SPLITK_ERR_TIMEOUT (the output is then undefined); in
  * splitk_gemm_i8() of more than 8 tokens, which then runs on pairs of CTAs,
  * the second of a pair does not report its tiles, and the first one's wait for
- * them runs out.  No GPU fault is involved: nothing is stored remotely and every
+ * them runs out; in splitk_gemm_mx4() the tiles' scales are not reported.  No GPU fault is involved: nothing is stored remotely and every
  * wait stays bounded.
  * 0 turns injection off.
  */

@@ -31,6 +31,7 @@ __all__ = [
     "splitk_plan_w4a16", "splitk_plan_w4a16_for", "splitk_gemm_w4a16", "splitk_gemm_w4a16_planned",
     "splitk_plan_w8a16", "splitk_plan_w8a16_for", "splitk_gemm_w8a16", "splitk_gemm_w8a16_planned",
     "splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs",
+    "splitk_quantize_mx4", "splitk_dequantize_mx4", "splitk_rmsnorm_mx4", "splitk_gemm_mx4", "splitk_adjust_logits",
     "splitk_get_fault",
     "splitk_get_status",
     "splitk_set_wait_limit_ns", "splitk_debug_inject", "splitk_release", "splitk_cache_info",
@@ -95,6 +96,13 @@ class Fault(ctypes.Structure):
         d = {k: getattr(self, k) for k, _ in self._fields_}
         d["block"] = list(self.block)
         return d
+
+
+class Adjust(ctypes.Structure):
+    """splitk_adjust_t: how splitk_adjust_logits changes the logits."""
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "history", "lengths", "prompt_lengths", "repetition", "presence", "frequency", "bias_ids", "bias_values",
+        "allowed")] + [("history_length", ctypes.c_int), ("bias_count", ctypes.c_int)]
 
 
 _lib = None
@@ -164,6 +172,16 @@ def load_library():
     lib.splitk_gemm_i8.restype = i
     lib.splitk_logprobs.argtypes = [vp, i, ll, vp, vp, vp, i, vp, vp, i, i, vp]
     lib.splitk_logprobs.restype = i
+    lib.splitk_quantize_mx4.argtypes = [vp, i, ll, vp, vp, i, i, vp]
+    lib.splitk_quantize_mx4.restype = i
+    lib.splitk_dequantize_mx4.argtypes = [vp, vp, vp, i, i, i, vp]
+    lib.splitk_dequantize_mx4.restype = i
+    lib.splitk_rmsnorm_mx4.argtypes = [vp, ll, vp, vp, i, vp, i, f, vp, vp, i, i, vp]
+    lib.splitk_rmsnorm_mx4.restype = i
+    lib.splitk_gemm_mx4.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+    lib.splitk_gemm_mx4.restype = i
+    lib.splitk_adjust_logits.argtypes = [vp, i, ll, ctypes.POINTER(Adjust), vp, ll, i, i, vp]
+    lib.splitk_adjust_logits.restype = i
     lib.splitk_get_fault.argtypes = [ctypes.POINTER(Fault)]
     lib.splitk_get_fault.restype = i
     lib.splitk_get_status.argtypes = []
@@ -610,8 +628,10 @@ def splitk_version() -> int:
     return int(load_library().splitk_version())
 
 
-# ---------------------------------------------------------------- 8-bit codes, log probabilities
-_OPERATORS = ("splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs")
+# ---------------------------------------------------------------- codes of 8 and 4 bits, logits
+_OPERATORS = ("splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs",
+              "splitk_quantize_mx4", "splitk_dequantize_mx4", "splitk_rmsnorm_mx4", "splitk_gemm_mx4",
+              "splitk_adjust_logits")
 
 
 def __getattr__(name):

@@ -43,6 +43,8 @@ const char* name_of(ScalarType t) {
     case ScalarType::Float: return "float32";
     case ScalarType::Char: return "int8";
     case ScalarType::Long: return "int64";
+    case ScalarType::Byte: return "uint8";
+    case ScalarType::Int: return "int32";
     default: return c10::toString(t);
   }
 }
@@ -362,8 +364,258 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// [.., K] as codes and scales: the shapes of both.
+struct CodeShapes {
+  at::SmallVector<int64_t, 3> codes, scale;
+  CodeShapes(at::IntArrayRef values) : codes(values.begin(), values.end()), scale(values.begin(), values.end()) {
+    codes.back() = values.back() / 2;
+    scale.back() = values.back() / 32;
+  }
+};
+
+// A type named by a torch.dtype, or `otherwise` where it is None.
+ScalarType type_or(PyObject* o, const char* name, ScalarType otherwise) {
+  if (o == Py_None) return otherwise;
+  if (!THPDtype_Check(o)) type_error(std::string(name) + " must be a torch.dtype");
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+void want_width(int64_t k) {
+  if (k < 1 || k % 32 != 0) value_error("rows must be a multiple of 32 wide, not " + std::to_string(k));
+}
+
+// (x, codes, scale, stream)
+PyObject* quantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("quantize_mx4", n, 4, [&]() -> PyObject* {
+    const Tensor& x = required(a[0], "x");
+    Output codes{optional(a[1], "codes"), {}}, scale{optional(a[2], "scale"), {}};
+    const Rows r(x, "x");
+    want_type(x, "x", {ScalarType::BFloat16, ScalarType::Half, ScalarType::Float});
+    want_width(r.width);
+    const at::Device device = x.device();
+    want_gpu(device);
+    const CodeShapes shapes(x.sizes());
+    codes.check("codes", shapes.codes, ScalarType::Byte, device);
+    scale.check("scale", shapes.scale, ScalarType::Byte, device);
+    const Stream stream = stream_of(a[3], device);
+    int rc;
+    {
+      const Enqueue enqueue(device, stream);
+      rc = splitk_quantize_mx4(x.data_ptr(), code_of(x.scalar_type()), r.stride,
+                               codes.data(shapes.codes, ScalarType::Byte, device),
+                               scale.data(shapes.scale, ScalarType::Byte, device), as_int(r.rows), as_int(r.width),
+                               stream.handle());
+    }
+    if (rc != SPLITK_OK) return PyLong_FromLong(rc);
+    return Py_BuildValue("NN", codes.wrap(), scale.wrap());
+  });
+}
+
+// (codes, scale, out, out_dtype, stream)
+PyObject* dequantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("dequantize_mx4", n, 5, [&]() -> PyObject* {
+    const Tensor &codes = required(a[0], "codes"), &scale = required(a[1], "scale");
+    Output out{optional(a[2], "out"), {}};
+    want_type(codes, "codes", {ScalarType::Byte});
+    want_type(scale, "scale", {ScalarType::Byte});
+    if (codes.dim() != 2 && codes.dim() != 3) value_error("codes are [M, K / 2] or [L, M, K / 2]");
+    at::SmallVector<int64_t, 3> shape(codes.sizes().begin(), codes.sizes().end());
+    shape.back() *= 2;
+    want_width(shape.back());
+    const CodeShapes shapes(shape);
+    const at::Device device = codes.device();
+    if (!codes.is_contiguous()) value_error("codes must be contiguous");
+    want_whole(scale, "scale", shapes.scale, ScalarType::Byte, device);
+    want_gpu(device);
+    const ScalarType type = type_or(a[3], "out_dtype", out.given ? out.given->scalar_type() : ScalarType::BFloat16);
+    if (type != ScalarType::BFloat16 && type != ScalarType::Half && type != ScalarType::Float) {
+      type_error(std::string("out must be bfloat16, float16 or float32, not ") + name_of(type));
+    }
+    out.check("out", shape, type, device);
+    const Stream stream = stream_of(a[4], device);
+    int rc;
+    {
+      const Enqueue enqueue(device, stream);
+      rc = splitk_dequantize_mx4(codes.data_ptr(), scale.data_ptr(), out.data(shape, type, device), code_of(type),
+                                 as_int(codes.numel() / codes.sizes().back()), as_int(shape.back()), stream.handle());
+    }
+    if (rc != SPLITK_OK) return PyLong_FromLong(rc);
+    return out.wrap();
+  });
+}
+
+// (x, weight, residual, eps, codes, scale, residual_out, stream)
+PyObject* rmsnorm_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("rmsnorm_mx4", n, 8, [&]() -> PyObject* {
+    const Tensor &x = required(a[0], "x"), &weight = required(a[1], "weight");
+    const Tensor* residual = optional(a[2], "residual");
+    const double eps = PyFloat_AsDouble(a[3]);
+    if (eps == -1.0 && PyErr_Occurred()) throw python_error();
+    Output codes{optional(a[4], "codes"), {}}, scale{optional(a[5], "scale"), {}}, out{optional(a[6], "residual_out"), {}};
+    const Rows r(x, "x");
+    want_type(x, "x", {ScalarType::BFloat16});
+    want_width(r.width);
+    want_type(weight, "weight", {ScalarType::BFloat16, ScalarType::Float});
+    if (weight.sizes() != at::IntArrayRef{r.width} || !weight.is_contiguous()) {
+      value_error("weight must be a contiguous tensor of shape " + shape_text({r.width}));
+    }
+    const at::Device device = x.device();
+    want_device(&weight, "weight", device);
+    want_device(residual, "residual", device);
+    want_gpu(device);
+    const at::IntArrayRef shape = x.sizes();
+    const CodeShapes shapes(shape);
+    ScalarType r_type = ScalarType::BFloat16;
+    if (residual != nullptr) {
+      want_type(*residual, "residual", {ScalarType::BFloat16, ScalarType::Float});
+      r_type = residual->scalar_type();
+      want_whole(*residual, "residual", shape, r_type, device);
+      out.check("residual_out", shape, r_type, device);
+    } else if (out.given != nullptr) {
+      value_error("residual_out needs a residual");
+    }
+    codes.check("codes", shapes.codes, ScalarType::Byte, device);
+    scale.check("scale", shapes.scale, ScalarType::Byte, device);
+    const Stream stream = stream_of(a[7], device);
+    int rc;
+    {
+      const Enqueue enqueue(device, stream);
+      rc = splitk_rmsnorm_mx4(x.data_ptr(), r.stride, residual ? residual->data_ptr() : nullptr,
+                              residual ? out.data(shape, r_type, device) : nullptr, code_of(r_type), weight.data_ptr(),
+                              code_of(weight.scalar_type()), (float)eps, codes.data(shapes.codes, ScalarType::Byte, device),
+                              scale.data(shapes.scale, ScalarType::Byte, device), as_int(r.rows), as_int(r.width),
+                              stream.handle());
+    }
+    if (rc != SPLITK_OK) return PyLong_FromLong(rc);
+    return Py_BuildValue("NNN", codes.wrap(), scale.wrap(), residual ? out.wrap() : none());
+  });
+}
+
+// (a_q, a_scale, b_q, b_scale, c, bias, out_dtype, stream)
+PyObject* gemm_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gemm_mx4", n, 8, [&]() -> PyObject* {
+    const Tensor &a_q = required(a[0], "a_q"), &a_scale = required(a[1], "a_scale"), &b_q = required(a[2], "b_q"),
+                 &b_scale = required(a[3], "b_scale");
+    Output c{optional(a[4], "c"), {}};
+    const Tensor* bias = optional(a[5], "bias");
+    want_type(a_q, "a_q", {ScalarType::Byte});
+    want_type(b_q, "b_q", {ScalarType::Byte});
+    want_type(a_scale, "a_scale", {ScalarType::Byte});
+    want_type(b_scale, "b_scale", {ScalarType::Byte});
+    const int64_t dims = a_q.dim();
+    if ((dims != 2 && dims != 3) || b_q.dim() != dims) {
+      value_error("a_q is [L, N, K / 2] or [N, K / 2]; b_q is [L, M, K / 2] or [M, K / 2]");
+    }
+    const at::IntArrayRef as = a_q.sizes(), bs = b_q.sizes();
+    const int64_t L = dims == 3 ? as[0] : 1, N = as[dims - 2], M = bs[dims - 2], K = 2 * as[dims - 1];
+    want_width(K);
+    at::SmallVector<int64_t, 3> a_rows(as.begin(), as.end()), b_rows(bs.begin(), bs.end());
+    a_rows.back() = b_rows.back() = K / 32;
+    const int64_t batched[3] = {L, M, N};
+    const at::IntArrayRef outputs(batched + (3 - dims), dims);
+    if (2 * bs[dims - 1] != K || (dims == 3 && bs[0] != L) || a_scale.sizes() != at::IntArrayRef(a_rows) ||
+        b_scale.sizes() != at::IntArrayRef(b_rows)) {
+      value_error("shape mismatch: a_q" + shape_text(as) + " a_scale" + shape_text(a_scale.sizes()) + " b_q" +
+                  shape_text(bs) + " b_scale" + shape_text(b_scale.sizes()));
+    }
+    if (!a_q.is_contiguous() || !a_scale.is_contiguous() || !b_q.is_contiguous() || !b_scale.is_contiguous()) {
+      value_error("operands must be contiguous");
+    }
+    const at::Device device = a_q.device();
+    want_device(&a_scale, "a_scale", device);
+    want_device(&b_q, "b_q", device);
+    want_device(&b_scale, "b_scale", device);
+    want_device(bias, "bias", device);
+    want_gpu(device);
+    if (bias != nullptr) want_whole(*bias, "bias", as.slice(0, dims - 1), ScalarType::BFloat16, device);
+    const ScalarType type = type_or(a[6], "out_dtype", c.given ? c.given->scalar_type() : ScalarType::BFloat16);
+    if (type != ScalarType::BFloat16 && type != ScalarType::Float) {
+      type_error(std::string("c must be bfloat16 or float32, not ") + name_of(type));
+    }
+    c.check("c", outputs, type, device);
+    const Stream stream = stream_of(a[7], device);
+    int rc;
+    {
+      const Enqueue enqueue(device, stream);
+      rc = splitk_gemm_mx4(a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(),
+                           bias ? bias->data_ptr() : nullptr, c.data(outputs, type, device), code_of(type), as_int(M),
+                           as_int(N), as_int(K), as_int(L), stream.handle());
+    }
+    if (rc != SPLITK_OK) return PyLong_FromLong(rc);
+    return c.wrap();
+  });
+}
+
+// (logits, history, lengths, prompt_lengths, repetition, presence, frequency, bias_ids, bias_values, allowed, out,
+// stream)
+PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("adjust_logits", n, 12, [&]() -> PyObject* {
+    const Tensor& logits = required(a[0], "logits");
+    const Rows r(logits, "logits");
+    const ScalarType type = logits.scalar_type();
+    want_type(logits, "logits", {ScalarType::BFloat16, ScalarType::Half, ScalarType::Float});
+    const at::Device device = logits.device();
+    const at::IntArrayRef rows = logits.sizes().slice(0, logits.dim() - 1);
+    // an argument with a value for each row, or (`wide`) several
+    const auto per_row = [&](int i, const char* name, ScalarType t, int64_t* wide) -> const void* {
+      const Tensor* v = optional(a[i], name);
+      if (v == nullptr) return nullptr;
+      at::SmallVector<int64_t, 3> shape(rows.begin(), rows.end());
+      if (wide != nullptr) {
+        if (*wide < 0) *wide = v->dim() > 0 ? v->size(-1) : 0;
+        shape.push_back(*wide);
+      }
+      want_whole(*v, name, shape, t, device);
+      return v->data_ptr();
+    };
+    int64_t length = -1, biases = -1, words = (r.width + 31) / 32;
+    splitk_adjust_t how{};
+    how.history = static_cast<const long long*>(per_row(1, "history", ScalarType::Long, &length));
+    how.lengths = static_cast<const long long*>(per_row(2, "lengths", ScalarType::Long, nullptr));
+    how.prompt_lengths = static_cast<const long long*>(per_row(3, "prompt_lengths", ScalarType::Long, nullptr));
+    how.repetition = static_cast<const float*>(per_row(4, "repetition", ScalarType::Float, nullptr));
+    how.presence = static_cast<const float*>(per_row(5, "presence", ScalarType::Float, nullptr));
+    how.frequency = static_cast<const float*>(per_row(6, "frequency", ScalarType::Float, nullptr));
+    how.bias_ids = static_cast<const long long*>(per_row(7, "bias_ids", ScalarType::Long, &biases));
+    how.bias_values = static_cast<const float*>(per_row(8, "bias_values", ScalarType::Float, &biases));
+    how.allowed = static_cast<const int*>(per_row(9, "allowed", ScalarType::Int, &words));
+    if (a[1] == Py_None) {
+      for (int i = 2; i <= 6; ++i) {
+        if (a[i] != Py_None) value_error("lengths and penalties need a history");
+      }
+    }
+    if ((a[7] == Py_None) != (a[8] == Py_None)) value_error("bias_ids and bias_values belong together");
+    // (an empty history has no memory, and no penalties)
+    if (length == 0) how.lengths = how.prompt_lengths = nullptr, how.repetition = how.presence = how.frequency = nullptr;
+    how.history_length = length < 0 ? 0 : as_int(length);
+    how.bias_count = biases < 0 ? 0 : as_int(biases);
+    Output out{optional(a[10], "out"), {}};
+    int64_t out_stride = r.width;
+    if (out.given != nullptr) {
+      if (out.given->sizes() != logits.sizes() || out.given->scalar_type() != type) {
+        value_error(std::string("out must be a ") + name_of(type) + " tensor of shape " + shape_text(logits.sizes()));
+      }
+      want_device(out.given, "out", device);
+      const Rows o(*out.given, "out");
+      out_stride = o.stride;
+    }
+    want_gpu(device);
+    const Stream stream = stream_of(a[11], device);
+    int rc;
+    {
+      const Enqueue enqueue(device, stream);
+      rc = splitk_adjust_logits(logits.data_ptr(), code_of(type), r.stride, &how, out.data(logits.sizes(), type, device),
+                                out_stride, as_int(r.rows), as_int(r.width), stream.handle());
+    }
+    if (rc != SPLITK_OK) return PyLong_FromLong(rc);
+    return out.wrap();
+  });
+}
+
 #define FASTCALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FASTCALL(rmsnorm_i8), FASTCALL(quantize_i8), FASTCALL(gemm_i8), FASTCALL(logprobs),
+                         FASTCALL(quantize_mx4), FASTCALL(dequantize_mx4), FASTCALL(rmsnorm_mx4), FASTCALL(gemm_mx4),
+                         FASTCALL(adjust_logits),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

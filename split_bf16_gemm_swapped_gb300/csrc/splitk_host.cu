@@ -37,7 +37,6 @@ static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratch
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMapPoolSlots = 4096;     // 512 KiB of device tensor maps
 constexpr size_t kBMapCacheMax = 1024;
 
@@ -826,6 +825,7 @@ struct DeviceState {
   // for the others nor depends on them.
   bool i8_ready = false, logprobs_ready = false;
   int i8_clusters[4] = {}, row_clusters[3] = {};           // see DeviceSize
+  FaultReader fault_readers[kMaxFaultReaders] = {};        // see add_fault_reader()
   int max_clusters[9] = {};        // persistent kernel: clusters of 2, 4, 8 resident at once (0: unknown)
 };
 
@@ -1218,7 +1218,8 @@ template <class F>
 int require(DeviceSize* out, bool DeviceState::*ready, F prepare) {
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
-  const int rc = current_device(&st, nullptr);
+  int device = 0;
+  const int rc = current_device(&st, &device);
   if (rc != SPLITK_OK) return rc;
   if (ready && !(st->*ready)) {
     if (prepare(*st) != cudaSuccess) {
@@ -1229,7 +1230,7 @@ int require(DeviceSize* out, bool DeviceState::*ready, F prepare) {
   }
   *out = DeviceSize{st->num_sms, st->smem_per_sm, st->smem_optin,
                     {st->i8_clusters[0], st->i8_clusters[1], st->i8_clusters[2], st->i8_clusters[3]},
-                    {st->row_clusters[0], st->row_clusters[1], st->row_clusters[2]}};
+                    {st->row_clusters[0], st->row_clusters[1], st->row_clusters[2]}, device};
   return SPLITK_OK;
 }
 
@@ -1244,6 +1245,17 @@ int require_i8(DeviceSize* out) {
 }
 int require_logprobs(DeviceSize* out) {
   return require(out, &DeviceState::logprobs_ready, [](DeviceState& st) { return prepare_logprobs(st.row_clusters); });
+}
+
+void add_fault_reader(int device, FaultReader read) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  for (FaultReader& r : g_dev[device].fault_readers) {
+    if (r == read) return;
+    if (r == nullptr) {
+      r = read;
+      return;
+    }
+  }
 }
 
 bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows) {
@@ -1628,6 +1640,14 @@ SPLITK_API int splitk_get_fault(splitk_fault_t* out) {
     }
     if (words[0] == 0) std::memcpy(words, words_p, sizeof(words));
     if (words[0] == 0) std::memcpy(words, words_i, sizeof(words));
+    for (int r = 0; dev >= 0 && dev < kMaxDevices && r < kMaxFaultReaders && g_dev[dev].fault_readers[r]; ++r) {
+      int words_r[kFaultWords] = {0};
+      if (g_dev[dev].fault_readers[r](words_r) != cudaSuccess) {
+        cudaGetLastError();
+        return SPLITK_ERR_CUDA;
+      }
+      if (words[0] == 0) std::memcpy(words, words_r, sizeof(words));
+    }
   }
   if (out) {
     out->code = words[0];

@@ -64,6 +64,9 @@ __host__ __device__ constexpr uint32_t tmem_cols_for(int mma_n, int tmem_tiles, 
                                        : tmem_tile_col0(mma_n, issuers) + kTmemTileCols * (uint32_t)tmem_tiles);
 }
 
+// Devices of a process, by index.
+constexpr int kMaxDevices = 64;
+
 // Fault record in device memory (one per device, see splitk_fault_t).
 constexpr int kFaultWords = 8;
 
@@ -173,10 +176,18 @@ struct DeviceSize {
   size_t smem_optin;
   int i8_clusters[4];         // clusters of 1, 2, 3 and 4 CTA pairs of the 8-bit product resident at once
   int row_clusters[3];        // clusters of 2, 4 and 8 CTAs of the log probabilities resident at once
+  int device;                 // its index
 };
 int require_device(DeviceSize* out);
 int require_i8(DeviceSize* out);
 int require_logprobs(DeviceSize* out);
+
+// Defined in splitk_host.cu: a kernel file whose kernels are prepared at their
+// first use on a device adds what reads and clears its fault record there, for
+// splitk_get_fault().
+using FaultReader = cudaError_t (*)(int* out_words);
+constexpr int kMaxFaultReaders = 4;
+void add_fault_reader(int device, FaultReader read);
 
 // Defined in splitk_host.cu: a map of [L][rows][K] bytes read in boxes of 128
 // bytes of K by `box_rows` rows, 128-byte swizzle, zeros past the ends; and

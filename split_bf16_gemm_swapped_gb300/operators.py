@@ -1,5 +1,6 @@
 """The operators around the decode projection: residual addition + RMS norm to
-8-bit codes, quantisation, the product of 8-bit codes, log probabilities.
+8-bit codes, quantisation, the product of 8-bit codes, log probabilities; the
+same in microscaled 4-bit codes, and the adjustment of logits.
 
 As in the package's other calls, PyTorch supplies device memory and streams
 and every step runs in the library's kernels (``include/splitk.h`` says what
@@ -20,7 +21,9 @@ import threading
 
 from . import SplitKError, _build, load_library
 
-__all__ = ["splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs"]
+__all__ = ["splitk_rmsnorm_i8", "splitk_quantize_i8", "splitk_gemm_i8", "splitk_logprobs",
+           "splitk_quantize_mx4", "splitk_dequantize_mx4", "splitk_rmsnorm_mx4", "splitk_gemm_mx4",
+           "splitk_adjust_logits"]
 
 
 def _load():
@@ -115,4 +118,80 @@ def splitk_logprobs(logits, tokens=None, top_k: int = 0, logprob=None, entropy=N
     out = _native.logprobs(logits, tokens, top_k, logprob, entropy, top_ids, top_logprobs, stream)
     if type(out) is int:
         raise SplitKError(out, "splitk_logprobs")
+    return out
+
+
+def splitk_quantize_mx4(x, codes=None, scale=None, stream=None):
+    """Rows to microscaled 4-bit codes, the format of splitk_gemm_w4a16's weights:
+    E2M1 codes, two a byte and the first in the low nibble, and an E8M0 scale code
+    for 32 of them: 2**(floor(log2(max|x|)) - 2), at least 2**-126.  Values are rounded to the
+    nearest code, ties to even, and cut off at 6 scales.
+
+    x [M, K] (rows any distance apart) or contiguous [L, M, K], bfloat16, float16
+    or float32, K a multiple of 32.  Returns (codes uint8 [..., K/2], scale uint8
+    [..., K/32])."""
+    out = _native.quantize_mx4(x, codes, scale, stream)
+    if type(out) is int:
+        raise SplitKError(out, "splitk_quantize_mx4")
+    return out
+
+
+def splitk_dequantize_mx4(codes, scale, out=None, out_dtype=None, stream=None):
+    """The values that codes and scales stand for: [..., K] bfloat16 (or float16 or
+    float32, where out_dtype or the out given says so).  codes uint8 [M, K/2] or
+    [L, M, K/2], scale uint8 [..., K/32], contiguous."""
+    out = _native.dequantize_mx4(codes, scale, out, out_dtype, stream)
+    if type(out) is int:
+        raise SplitKError(out, "splitk_dequantize_mx4")
+    return out
+
+
+def splitk_rmsnorm_mx4(x, weight, residual=None, eps: float = 1e-6, codes=None, scale=None, residual_out=None,
+                       stream=None):
+    """Residual addition, RMS norm and microscaled 4-bit codes: y = x + residual,
+    n = y * weight / sqrt(mean(y^2) + eps) in float32, codes and scales of n as in
+    splitk_quantize_mx4.
+
+    Arguments as in splitk_rmsnorm_i8, D a multiple of 32.  Returns (codes uint8
+    [..., D/2], scale uint8 [..., D/32], residual_out)."""
+    out = _native.rmsnorm_mx4(x, weight, residual, eps, codes, scale, residual_out, stream)
+    if type(out) is int:
+        raise SplitKError(out, "splitk_rmsnorm_mx4")
+    return out
+
+
+def splitk_gemm_mx4(a_q, a_scale, b_q, b_scale, c=None, bias=None, out_dtype=None, stream=None):
+    """c = b @ a^T + bias with both operands in microscaled 4-bit codes.
+
+    a_q uint8 [L, N, K/2] or [N, K/2] with a_scale uint8 [..., K/32], b_q [L, M,
+    K/2] or [M, K/2] with b_scale, contiguous, K a multiple of 32; bias [L, N] or [N]
+    bfloat16.  Returns c [L, M, N] or [M, N]: bfloat16, or float32 where out_dtype
+    or the c given says so."""
+    out = _native.gemm_mx4(a_q, a_scale, b_q, b_scale, c, bias, out_dtype, stream)
+    if type(out) is int:
+        raise SplitKError(out, "splitk_gemm_mx4")
+    return out
+
+
+def splitk_adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None, presence=None,
+                         frequency=None, bias_ids=None, bias_values=None, allowed=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks.  For a logit x:
+    a token of the row's history has x / repetition where x > 0, else x *
+    repetition; one that is there `count` times behind the prompt then has x -
+    frequency * count - presence; one of its bias_ids x + bias (listed twice: the
+    sum); one that is not allowed -inf.
+
+    logits [M, V] (rows any distance apart) or contiguous [L, M, V], bfloat16,
+    float16 or float32.  For each row (shapes with M for [L, M], too), contiguous:
+    history int64 [M, H], of which the first `lengths` (int64 [M], all without) are
+    tokens and the first `prompt_lengths` (int64 [M], none without) the prompt's;
+    repetition, presence and frequency float32 [M]; bias_ids int64 and bias_values
+    float32 [M, B], B at most 1024; allowed int32 [M, ceil(V/32)], bit v % 32 of
+    word v // 32 set where token v may come next.  Tokens outside the vocabulary
+    (padding) count nowhere.  Returns out, of the logits' type and shape; it may be
+    the logits themselves (changed in place)."""
+    out = _native.adjust_logits(logits, history, lengths, prompt_lengths, repetition, presence, frequency, bias_ids,
+                                bias_values, allowed, out, stream)
+    if type(out) is int:
+        raise SplitKError(out, "splitk_adjust_logits")
     return out
