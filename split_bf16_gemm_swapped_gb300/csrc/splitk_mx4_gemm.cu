@@ -2,16 +2,24 @@
 // (splitk_mx4.cuh) on the tensor cores' own instruction for them: E2M1 codes and
 // E8M0 scales go in as they are, nothing is converted.
 //
-// A CTA owns 128 weight rows (the MMA's M side) and kTok tokens (its N side).  TMA
-// brings codes, 256 of K wide, from both operands into a ring of shared memory
-// (K-major, 128-byte swizzle).  Scale warps bring the tiles' scales into shared
-// memory in the order that a copy into tensor memory wants: for 128 rows and four
-// blocks of K, 512 bytes, row r's four codes at 16 (r % 32) + 4 (r / 32).  The
-// issuing thread copies them (tcgen05.cp, to all four lane quadrants) into columns
-// of the tile's own and issues four MMAs of K = 64.
+// A pair of CTAs owns 256 weight rows (the M side of a cta_group::2 MMA, 128 in each
+// CTA's tensor memory) and kTok tokens (its N side, half of them in each CTA's
+// shared memory).  TMA brings codes, 256 of K wide, from both operands into a ring of
+// shared memory (K-major, 128-byte swizzle); a tile's copies of both CTAs report to
+// the leader.  Scale warps bring the tiles' scales into shared memory in the order
+// that a copy into tensor memory wants: for 128 rows and four blocks of K, 512 bytes,
+// row r's four codes at 16 (r % 32) + 4 (r / 32).  In the leader one thread copies
+// them (tcgen05.cp, to all four lane quadrants of both CTAs) into columns of the
+// tile's own, another issues the tile's four MMAs of K = 64 for both.
 //
-// `split` CTAs of a cluster may share one output tile, each taking a contiguous
-// run of K tiles; each leaves its f32 sums in its own shared memory and then adds
+// Why pairs and two issuing threads: a tcgen05 instruction takes its thread ~46
+// clocks to issue whatever its size, and a tile of few tokens is four copies and four
+// MMAs (with one thread and one CTA a tile, 0.44 us; the copies' share was 0.1, the
+// MMAs' 0.09).  For many tokens a CTA alone would bring 48 KiB a tile for 256 tokens,
+// which takes 0.45 us from L2; a pair brings 32 for each.
+//
+// `split` pairs of a cluster may share one output tile, each taking a contiguous run
+// of K tiles; each CTA leaves its f32 sums in its own shared memory and then adds
 // one slice of the tokens over the ranks in order.
 
 #include <cuda.h>
@@ -30,21 +38,31 @@ namespace splitk {
 
 namespace {
 
-constexpr int kMxThreads = 256;
-constexpr int kScale0 = 4, kScaleWarps = 4;          // the warps that bring scales (and store the output)
+// Warps: 0 copies of codes, 1 MMAs, 2 copies of scales into tensor memory, 3 set-up,
+// then those that bring scales and those that store the output.
+constexpr int kScale0 = 4, kScaleWarps = 4, kOut0 = kScale0 + kScaleWarps, kOutWarps = 4;
+constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
 constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
 constexpr int kMxStages = 10;                        // at most
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
 constexpr uint32_t kMxBarBytes = 512;
-constexpr int kMaxSplit = 8;
+constexpr int kOutTokens = 32;                       // of a chunk that an output warp stores at once
+constexpr int kMaxSplit = 4;                         // pairs of a cluster
+constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
 
-__host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok * (kTileK / 2); }
+// (of the half of the tokens that a CTA brings)
+__host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok / 2 * (kTileK / 2); }
 __host__ __device__ constexpr int groups_b(int tok) { return (tok + 127) / 128; }     // of 128 tokens
 __host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAtom * (1u + groups_b(tok)); }
 __host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kCodesA + codes_b(tok) + scales_of(tok); }
 __host__ __device__ constexpr uint32_t mx_acc_cols(int tok) { return tok < 32 ? 32u : (uint32_t)tok; }
 __host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a stage
+
+// Chunks of 32 weight rows by kOutTokens tokens on their way out, two for each output
+// warp, in kernels for many tokens.
+__host__ __device__ constexpr bool out_boxes(int tok) { return tok >= 128; }
+__host__ __device__ constexpr uint32_t out_bytes(int tok) { return out_boxes(tok) ? kOutWarps * 2u * kOutTokens * 32u * 4u : 0u; }
 
 // kind::mxf4: E2M1 operands, both K-major, E8M0 scales for each 32, f32 accumulator;
 // the scales of a K = 64 step are the lower (id 0) or upper (id 2) half of a word.
@@ -52,19 +70,71 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27) | (id << 29);
 }
 
+// D[tmem] (+)= A B^T over the pair of CTAs.
 __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
                                          uint32_t b_scale, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
       : "memory");
 }
 
-// 32 rows of 16 bytes (unswizzled) into four columns of each lane quadrant.
+// 32 rows of 16 bytes (unswizzled) of each CTA into four columns of its lane quadrants.
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+// The arrival of what this thread has issued so far: on its CTA's barrier, or on the
+// same one of all CTAs of a mask.
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t cta_mask) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\t"
+      "cvt.u16.u32 m, %1;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+      "r"(cta_mask)
+      : "memory");
+}
+
+// A box into this CTA's shared memory that reports to a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t cluster_bar,
+                                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar), "l"(policy)
+      : "memory");
+}
+
+// A box of shared memory to global memory, in this thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
+               "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// At most `kLeft` of this thread's stores have not read their shared memory yet, or
+// none is not in global memory.
+template <int kLeft>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 // Shared-memory descriptor of such rows: no swizzle, eight rows (128 bytes) apart.
@@ -85,25 +155,68 @@ struct MxParams {
   bool c_f32;
   int M, N, K, L;
   int split, stages;
+  int tile0, tile_end;      // the launch's tiles
   uint32_t tmem_cols;
-  int a_align, b_align;     // of the scales' rows: 8, 4 or 1 bytes
+  bool c_boxes;             // C may be stored by TMA (c_map)
+  int align;                // of the scales' rows: 16, 8, 4 or 1 bytes
   unsigned long long limit_ns;
   unsigned inject;
 };
 
-// The scale codes of 8 blocks of K of one row (two words of four), 127 past K.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int at, int blocks, int align) {
-  constexpr uint32_t kOnes = 0x7F7F7F7Fu;
-  if (align == 8) return *reinterpret_cast<const uint2*>(row + at);       // (blocks a multiple of 8)
-  if (align == 4) {
-    return make_uint2(*reinterpret_cast<const uint32_t*>(row + at),
-                      at + 4 < blocks ? *reinterpret_cast<const uint32_t*>(row + at + 4) : kOnes);
-  }
-  uint32_t w[2] = {0u, 0u};
+// K tiles of a batch of scales: 8 bytes of a row each; a sector where registers allow.
+__host__ __device__ constexpr int batch_of(int tok) { return tok >= 128 ? 2 : 4; }
+
+// The scale codes of a batch of K tiles: two words of four for each row and tile.
+template <int kBatch>
+struct ScaleRow {
+  uint32_t w[2 * kBatch];
+  // Codes [at, limit) of the row at `row`, 127 past the limit (its codes there are
+  // zeros).  kAlign: what the addresses row + at are multiples of.  Words at odd
+  // addresses come from the two aligned ones around them, where all their bytes are
+  // within the array [first, end).
+  template <int kAlign>
+  __device__ __forceinline__ void load(const uint8_t* row, int at, int limit, const uint8_t* first, const uint8_t* end) {
+    constexpr uint32_t kOnes = 0x7F7F7F7Fu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i / 4] |= (at + i < blocks ? (uint32_t)row[at + i] : 127u) << (8 * (i % 4));
-  return make_uint2(w[0], w[1]);
-}
+    for (int i = 0; i < 2 * kBatch; ++i) w[i] = kOnes;
+    if constexpr (kAlign >= 4) {
+      constexpr int kWords = kAlign / 4;
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; i += kWords) {
+        if (at + 4 * i >= limit) continue;             // (the limit is a multiple of kAlign, or ends the row)
+        if constexpr (kWords == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + at + 4 * i);
+          w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        } else if constexpr (kWords == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + at + 4 * i);
+          w[i] = v.x, w[i + 1] = v.y;
+        } else {
+          w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kBatch; ++i) {
+        const int n = limit - (at + 4 * i);
+        if (n <= 0) continue;
+        const uint8_t* p = row + at + 4 * i;
+        const uint8_t* low = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)3);
+        uint32_t v = 0u;
+        if (low >= first && low + 8 <= end) {
+          const uint32_t* two = reinterpret_cast<const uint32_t*>(low);
+          v = __funnelshift_r(two[0], two[1], 8u * (uint32_t)(p - low));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j < n) v |= (uint32_t)p[j] << (8 * j);
+          }
+        }
+        const uint32_t kept = n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+        w[i] = (v & kept) | (kOnes & ~kept);
+      }
+    }
+  }
+};
 
 // One output from its sum.
 __device__ __forceinline__ void store_mx(const MxParams& p, long long at, float v) {
@@ -114,188 +227,360 @@ __device__ __forceinline__ void store_mx(const MxParams& p, long long at, float 
   }
 }
 
+// A thread's weight row of `cols` consecutive tokens, `pitch` bytes apart from `to`
+// on.  (Sixteen stores without a branch between them: with a choice of type and a
+// check for each, a warp took 125 clocks a store, and 256 tokens 17 us.)
+template <bool kF32>
+__device__ __forceinline__ void store_tokens(uint8_t* to, long long pitch, const uint32_t (&v)[16], float bias, int cols) {
+  const auto one = [&](uint8_t* at, uint32_t bits) {
+    const float r = __uint_as_float(bits) + bias;
+    if (kF32) {
+      *reinterpret_cast<float*>(at) = r;
+    } else {
+      *reinterpret_cast<uint16_t*>(at) = (uint16_t)dev::pack_bf16x2(r, 0.0f);
+    }
+  };
+  if (cols == 16) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e, to += pitch) one(to, v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e, to += pitch) {
+      if (e < cols) one(to, v[e]);
+    }
+  }
+}
+
+// One output tile of a pair: its place and K tiles.
+struct MxTile {
+  int m0, n0, l, k_tiles, kt0;
+  template <int kTok>
+  __device__ __forceinline__ static MxTile at(const MxParams& p, int tile, int rank, int half) {
+    const int m_tiles = (p.M + kTok - 1) / kTok, n_tiles = (p.N + 2 * kMmaM - 1) / (2 * kMmaM);
+    const int total = (p.K + kTileK - 1) / kTileK, each = total / p.split, extra = total % p.split;
+    MxTile t;
+    t.m0 = (tile % m_tiles) * kTok;
+    t.n0 = (2 * (tile / m_tiles % n_tiles) + half) * kMmaM;
+    t.l = tile / m_tiles / n_tiles;
+    t.k_tiles = each + (rank < extra ? 1 : 0);
+    t.kt0 = rank * each + (rank < extra ? rank : extra);
+    return t;
+  }
+};
+
+// What the scale warps work with.
+struct ScaleRing {
+  uint32_t slots, bar_scale_of_leader, bar_free, bar_turn;
+  int stages;
+  Waiter waiter;
+};
+
+// One scale warp's batches of a tile; `batch` and `used` count the CTA's batches and
+// K tiles before it.  A lane has rows lane + 32 g of each group of 128: for each
+// word of K their four codes lie side by side in shared memory, one 16-byte store.
+// A batch's loads are under way while other warps' batches are stored, and while the
+// ring's slots become free.  Batches are stored in order: a warp ahead by two rounds
+// of the ring would take the phase before the last for the last.
+template <int kTok, int kAlign>
+__device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing& r, const MxTile& t, int batch, int used,
+                                             int warp, int lane) {
+  constexpr int kGroups = groups_b(kTok), kLive = kTok >= 128 ? 4 : (kTok + 31) / 32;     // 32s of tokens in a group
+  constexpr int kBatch = batch_of(kTok);
+  const int blocks = p.K / kMxBlock, limit = min(blocks, (t.kt0 + t.k_tiles) * (kTileK / kMxBlock));
+  const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
+  for (int first = 0; first < t.k_tiles; first += kBatch, ++batch) {
+    if (batch % kScaleWarps != warp) continue;
+    const int at = (t.kt0 + first) * (kTileK / kMxBlock);
+    ScaleRow<kBatch> a[4], b[kGroups][kLive];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int n = t.n0 + lane + 32 * g;
+      a[g].template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? limit : 0, p.a_scale, a_end);
+    }
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+#pragma unroll
+      for (int g = 0; g < kLive; ++g) {
+        const int o = 128 * q + lane + 32 * g, m = t.m0 + o;
+        b[q][g].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? limit : 0,
+                                      p.b_scale, b_end);
+      }
+    }
+    if (batch > 0 && !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_turn + 8u * warp, (uint32_t)((batch - 1) / kScaleWarps) & 1u,
+                                                                    kRoleEpiDecode, first))) {
+      return false;
+    }
+    RingPos pos = RingPos::at(used + first, r.stages);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i, pos.advance(1, r.stages)) {
+      const int kt = first + i;
+      if (kt >= t.k_tiles) break;
+      const uint32_t s = (uint32_t)pos.index;
+      if (used + kt >= r.stages &&
+          !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_free + 8u * s, pos.phase ^ 1u, kRoleEpiDecode, kt))) return false;
+      const uint32_t dst = r.slots + s * scales_of(kTok) + 16u * lane;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int j = 2 * i + w;
+        dev::st_shared_v4(dst + w * kScaleAtom, a[0].w[j], a[1].w[j], a[2].w[j], a[3].w[j]);
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+          dev::st_shared_v4(dst + (2u + w * kGroups + q) * kScaleAtom, b[q][0].w[j], kLive > 1 ? b[q][1 % kLive].w[j] : 0u,
+                            kLive > 2 ? b[q][2 % kLive].w[j] : 0u, kLive > 3 ? b[q][3 % kLive].w[j] : 0u);
+        }
+      }
+      dev::fence_proxy_async_shared();
+      __syncwarp();
+      // (released at cluster scope, where the leader's copying thread acquires it)
+      if (lane == 0 && (p.inject & kInjectSkipPublish) == 0) {
+        dev::fence_release_shared_cluster();
+        dev::mbar_arrive_remote_relaxed(r.bar_scale_of_leader + 8u * s);
+      }
+    }
+    if (lane == 0) dev::mbar_arrive(r.bar_turn + 8u * ((warp + 1) % kScaleWarps));
+  }
+  return true;
+}
+
+// A cluster takes tiles gridDim.x / cluster size apart; with split > 1 one alone
+// (its sums go where the ring was).
 template <int kTok>
 __global__ void __launch_bounds__(kMxThreads, 1)
-    mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const MxParams p) {
+    mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+               const __grid_constant__ CUtensorMap c_map, const MxParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (dev::smem_u32(smem_raw) + (kAlignSlack - 1)) & ~(kAlignSlack - 1);
   const int stages = p.stages, split = p.split;
   const uint32_t s_a = base;
   const uint32_t s_b = s_a + (uint32_t)stages * kCodesA;
   const uint32_t s_s = s_b + (uint32_t)stages * codes_b(kTok);
-  const uint32_t s_bar = s_s + (uint32_t)stages * scales_of(kTok);
-  const uint32_t bar_full = s_bar;                          // [kMxStages] the codes landed
-  const uint32_t bar_scale = s_bar + 8u * kMxStages;        // [kMxStages] the scales are there
-  const uint32_t bar_free = s_bar + 16u * kMxStages;        // [kMxStages] the MMAs have read both
-  const uint32_t bar_acc = s_bar + 24u * kMxStages;         // the accumulator is complete
-  const uint32_t slot_tmem = bar_acc + 8u, slot_abort = bar_acc + 12u;
+  const uint32_t s_out = s_s + (uint32_t)stages * scales_of(kTok);
+  const uint32_t s_bar = s_out + out_bytes(kTok);
+  const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes landed
+  const uint32_t bar_scale = bar_full + 8u * kMxStages;     // [kMxStages] leader: both CTAs' scales are there
+  const uint32_t bar_copied = bar_scale + 8u * kMxStages;   // [kMxStages] leader: and in tensor memory
+  const uint32_t bar_free = bar_copied + 8u * kMxStages;    // [kMxStages] the MMAs have read all of it
+  const uint32_t bar_acc = bar_free + 8u * kMxStages;       // a tile's accumulator is complete
+  const uint32_t bar_read = bar_acc + 8u;                   // leader: both CTAs' output warps have read it
+  const uint32_t bar_turn = bar_read + 8u;                  // [kScaleWarps] the batch before the warp's next is stored
+  const uint32_t slot_tmem = bar_turn + 8u * kScaleWarps, slot_abort = slot_tmem + 4u;
 
   const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
-  const int rank = split > 1 ? (int)dev::cluster_ctarank() : 0;
-  const int tile = (int)blockIdx.x / split;
-  const int m_tiles = (p.M + kTok - 1) / kTok, n_tiles = (p.N + kMmaM - 1) / kMmaM;
-  const int m0 = (tile % m_tiles) * kTok, l = tile / m_tiles / n_tiles, n0 = (tile / m_tiles % n_tiles) * kMmaM;
-  const int total = (p.K + kTileK - 1) / kTileK;
-  const int each = total / split, extra = total % split;
-  const int k_tiles = each + (rank < extra ? 1 : 0);
-  const int kt0 = rank * each + (rank < extra ? rank : extra);
+  // cluster rank 2 r + half: CTA `half` of the pair that takes K slice r
+  const int cta = (int)dev::cluster_ctarank(), half = cta & 1, rank = cta >> 1;
+  const int tile0 = p.tile0 + (int)blockIdx.x / (2 * split), step = (int)gridDim.x / (2 * split);
   const Waiter waiter{slot_abort, p.limit_ns};
 
   if (warp == 3 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
       dev::mbar_init(bar_full + 8u * s, 1u);
-      dev::mbar_init(bar_scale + 8u * s, 1u);
+      dev::mbar_init(bar_scale + 8u * s, 2u);
+      dev::mbar_init(bar_copied + 8u * s, 1u);
       dev::mbar_init(bar_free + 8u * s, 1u);
     }
     dev::mbar_init(bar_acc, 1u);
+    dev::mbar_init(bar_read, 2u * kOutWarps);
+    for (int i = 0; i < kScaleWarps; ++i) dev::mbar_init(bar_turn + 8u * i, 1u);
     dev::st_shared_u32(slot_abort, 0u);
     dev::fence_barrier_init();
   } else if (warp == 2) {
-    dev::tmem_alloc(slot_tmem, p.tmem_cols);
-    dev::tmem_relinquish();
+    tmem_alloc_pair(slot_tmem, p.tmem_cols);
     dev::tc_fence_before();
   } else if (warp == 0 && lane == 0) {
     dev::tensormap_prefetch(&a_map);
     dev::tensormap_prefetch(&b_map);
   }
-  __syncthreads();
+  __syncwarp();
+  dev::cluster_arrive_release();
+  dev::cluster_wait_acquire();
   dev::tc_fence_after();
   // The next kernel may come once this CTA holds its tensor memory.
   dev::griddep_launch_dependents();
+  const MxTile tile_first = MxTile::at<kTok>(p, tile0, rank, half);
   // While the work ahead in the stream completes, the ring's first weight tiles come
   // to L2 (which is where a kernel's writes would change them: nothing is read early).
-  if (warp == 0 && lane < min(stages, k_tiles)) dev::tma_prefetch_3d(&a_map, (kt0 + lane) * (kTileK / 2), n0, l);
+  if (warp == 0 && lane < min(stages, tile_first.k_tiles)) {
+    dev::tma_prefetch_3d(&a_map, (tile_first.kt0 + lane) * (kTileK / 2), tile_first.n0, tile_first.l);
+  }
   dev::griddep_wait();
   const uint32_t tmem = dev::ld_shared_u32(slot_tmem);
+  const uint32_t leader = (uint32_t)(cta & ~1);
 
-  const int live = min(kTok, p.M - m0);
   int issued = 0;
   if (warp == 0) {
     if (lane == 0) {
-      const uint64_t stream_once = dev::policy_evict_first(), keep = dev::policy_evict_normal();
-      const uint64_t policy_a = m_tiles == 1 ? stream_once : keep;
+      const uint64_t keep = dev::policy_evict_normal(), policy_a = p.M <= kTok ? dev::policy_evict_first() : keep;
+      const uint32_t full_of_leader = dev::mapa(bar_full, leader);
       RingPos pos{0, 0u};
-      for (int kt = 0; kt < k_tiles; ++kt, pos.advance(1, stages)) {
-        const uint32_t s = (uint32_t)pos.index;
-        if (kt >= stages && !waiter.wait<false>(bar_free + 8u * s, pos.phase ^ 1u, kRoleWeightTma, kt)) break;
-        dev::mbar_arrive_expect_tx(bar_full + 8u * s, kCodesA + codes_b(kTok));
-        dev::tma_load_3d_hint(s_a + s * kCodesA, &a_map, (kt0 + kt) * (kTileK / 2), n0, l, bar_full + 8u * s, policy_a);
-        dev::tma_load_3d_hint(s_b + s * codes_b(kTok), &b_map, (kt0 + kt) * (kTileK / 2), m0, l, bar_full + 8u * s, keep);
-        ++issued;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
+        const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
+        for (int kt = 0; kt < t.k_tiles; ++kt, pos.advance(1, stages)) {
+          const uint32_t s = (uint32_t)pos.index;
+          if (issued >= stages && !waiter.wait<false>(bar_free + 8u * s, pos.phase ^ 1u, kRoleWeightTma, kt)) {
+            ok = false;
+            break;
+          }
+          if (half == 0) dev::mbar_arrive_expect_tx(bar_full + 8u * s, 2u * (kCodesA + codes_b(kTok)));
+          tma_load_pair(s_a + s * kCodesA, &a_map, (t.kt0 + kt) * (kTileK / 2), t.n0, t.l, full_of_leader + 8u * s, policy_a);
+          tma_load_pair(s_b + s * codes_b(kTok), &b_map, (t.kt0 + kt) * (kTileK / 2), t.m0 + half * (kTok / 2), t.l,
+                        full_of_leader + 8u * s, keep);
+          ++issued;
+        }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (half == 0 && lane == 0) {
       RingPos pos{0, 0u};
+      const uint32_t both = 3u << (2 * rank);
       const uint64_t a_desc = dev::smem_desc_sw128(s_a), b_desc = dev::smem_desc_sw128(s_b);
-      const uint64_t s_desc = smem_desc_rows16(s_s);
-      for (int kt = 0; kt < k_tiles; ++kt, pos.advance(1, stages)) {
-        const uint32_t s = (uint32_t)pos.index;
-        if (!waiter.wait<false>(bar_scale + 8u * s, pos.phase, kRoleMma, kt)) break;
-        const uint32_t t_a = tmem + mx_acc_cols(kTok) + s * scale_cols(kTok), t_b = t_a + 8u;
-        dev::tc_fence_after();
+      uint32_t turn = 0u;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < p.tile_end; tile += step, ++turn) {
+        const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
+        ok = turn == 0u || waiter.wait<true>(bar_read, (turn - 1u) & 1u, kRoleMmaAccFree, (int)turn);
+        for (int kt = 0; ok && kt < t.k_tiles; ++kt, pos.advance(1, stages)) {
+          const uint32_t s = (uint32_t)pos.index;
+          if (!waiter.wait<true>(bar_full + 8u * s, pos.phase, kRoleMma, kt) ||
+              !waiter.wait<false>(bar_copied + 8u * s, pos.phase, kRoleMma, kt)) {
+            ok = false;
+            break;
+          }
+          dev::tc_fence_after();
+          const uint32_t t_a = tmem + mx_acc_cols(kTok) + s * scale_cols(kTok), t_b = t_a + 8u;
+          const uint64_t a_d = dev::smem_desc_advance(a_desc, s * kCodesA), b_d = dev::smem_desc_advance(b_desc, s * codes_b(kTok));
 #pragma unroll
-        for (int i = 0; i < 2 * (1 + groups_b(kTok)); ++i) {
-          tmem_cp_scales(t_a + 4u * i, dev::smem_desc_advance(s_desc, s * scales_of(kTok) + kScaleAtom * i));
+          for (int j = 0; j < 4; ++j) {
+            mma_mxf4(tmem, dev::smem_desc_advance(a_d, 32u * j), dev::smem_desc_advance(b_d, 32u * j),
+                     j % 2 == 0 ? idesc_mxf4(2 * kMmaM, kTok, 0u) : idesc_mxf4(2 * kMmaM, kTok, 2u), t_a + 4u * (j / 2),
+                     t_b + 4u * groups_b(kTok) * (j / 2), (kt != 0 || j != 0) ? 1u : 0u);
+          }
+          commit_pair(bar_free + 8u * s, both);
         }
-        if (!waiter.wait<false>(bar_full + 8u * s, pos.phase, kRoleMma, kt)) break;
-        const uint64_t a_d = dev::smem_desc_advance(a_desc, s * kCodesA), b_d = dev::smem_desc_advance(b_desc, s * codes_b(kTok));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma_mxf4(tmem, dev::smem_desc_advance(a_d, 32u * j), dev::smem_desc_advance(b_d, 32u * j),
-                   j % 2 == 0 ? idesc_mxf4(kMmaM, kTok, 0u) : idesc_mxf4(kMmaM, kTok, 2u), t_a + 4u * (j / 2),
-                   t_b + 4u * groups_b(kTok) * (j / 2), (kt != 0 || j != 0) ? 1u : 0u);
-        }
-        dev::mma_commit(bar_free + 8u * s);
+        commit_pair(bar_acc, both);
       }
-      dev::mma_commit(bar_acc);
+      // after a failed wait, MMAs in flight land before the pair gives up its memory
+      if (!ok) drain_wait(bar_acc, (turn - 1u) & 1u, kDrainNs);
     }
     __syncwarp();
-  } else if (warp >= kScale0) {
-    // A lane has rows lane + 32 g of each group of 128: for each word of K their four
-    // scales lie side by side, one 16-byte store.  A warp takes every kScaleWarps-th
-    // K tile; its loads are under way while it waits for the slot.
-    const int blocks = p.K / kMxBlock;
-    const uint8_t* a_rows = p.a_scale + (long long)l * p.N * blocks;
-    const uint8_t* b_rows = p.b_scale + (long long)l * p.M * blocks;
-    RingPos pos = RingPos::at(warp - kScale0, stages);
-    for (int kt = warp - kScale0; kt < k_tiles; kt += kScaleWarps) {
-      const uint32_t s = (uint32_t)pos.index;
-      const int at = (kt0 + kt) * (kTileK / kMxBlock);
-      uint2 a[4], b[groups_b(kTok)][4];
+  } else if (warp == 2) {
+    if (half == 0 && lane == 0) {
+      RingPos pos{0, 0u};
+      const uint64_t s_desc = smem_desc_rows16(s_s);
+      bool ok = true;
+      for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
+        const int k_tiles = MxTile::at<kTok>(p, tile, rank, half).k_tiles;
+        for (int kt = 0; kt < k_tiles; ++kt, pos.advance(1, stages)) {
+          const uint32_t s = (uint32_t)pos.index;
+          if (!waiter.wait<true>(bar_scale + 8u * s, pos.phase, kRoleMma, kt)) {
+            ok = false;
+            break;
+          }
+          dev::tc_fence_after();
+          const uint32_t t_a = tmem + mx_acc_cols(kTok) + s * scale_cols(kTok);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = n0 + lane + 32 * g;
-        a[g] = n < p.N ? load_scales(a_rows + (long long)n * blocks, at, blocks, p.a_align) : make_uint2(0u, 0u);
-      }
-#pragma unroll
-      for (int q = 0; q < groups_b(kTok); ++q) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int m = m0 + 128 * q + lane + 32 * g;
-          const bool in = 128 * q + 32 * g < kTok && m < p.M;
-          b[q][g] = in ? load_scales(b_rows + (long long)m * blocks, at, blocks, p.b_align) : make_uint2(0u, 0u);
+          for (int i = 0; i < 2 * (1 + groups_b(kTok)); ++i) {
+            tmem_cp_scales(t_a + 4u * i, dev::smem_desc_advance(s_desc, s * scales_of(kTok) + kScaleAtom * i));
+          }
+          commit_here(bar_copied + 8u * s);
         }
       }
-      if (kt >= stages &&
-          !__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_free + 8u * s, pos.phase ^ 1u, kRoleEpiDecode, kt))) break;
-      const uint32_t dst = s_s + s * scales_of(kTok) + 16u * lane;
-      dev::st_shared_v4(dst, a[0].x, a[1].x, a[2].x, a[3].x);
-      dev::st_shared_v4(dst + kScaleAtom, a[0].y, a[1].y, a[2].y, a[3].y);
-#pragma unroll
-      for (int q = 0; q < groups_b(kTok); ++q) {
-        dev::st_shared_v4(dst + (2u + q) * kScaleAtom, b[q][0].x, b[q][1].x, b[q][2].x, b[q][3].x);
-        dev::st_shared_v4(dst + (2u + groups_b(kTok) + q) * kScaleAtom, b[q][0].y, b[q][1].y, b[q][2].y, b[q][3].y);
-      }
-      dev::fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0 && (p.inject & kInjectSkipPublish) == 0) dev::mbar_arrive(bar_scale + 8u * s);
-      for (int i = 0; i < kScaleWarps; ++i) pos.advance(1, stages);
     }
-  }
-
-  // ---- epilogue: a warp a TMEM lane quadrant, thread = weight row
-  const int row = (warp & 3) * 32 + lane, n = n0 + row;
-  waiter.wait<false>(bar_acc, 0u, kRoleEpiMma, 0);
-  __syncthreads();
-  dev::tc_fence_after();
-  if (warp >= kScale0) {
-    const float bias = p.bias && n < p.N ? __uint_as_float((uint32_t)p.bias[(long long)l * p.N + n] << 16) : 0.0f;
-    const uint32_t t_row = tmem + ((uint32_t)(row & ~31) << 16);
-    for (int g = 0; g * 16 < live; ++g) {
-      uint32_t v[16];
-      __syncwarp();
-      if (kTok < 16) {
-        uint32_t u[4];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          dev::tmem_ld_x4(t_row + 4u * q, u[0], u[1], u[2], u[3]);
+    __syncwarp();
+  } else if (warp >= kScale0 && warp < kOut0) {
+    const ScaleRing ring{s_s, dev::mapa(bar_scale, leader), bar_free, bar_turn, stages, waiter};
+    int batch = 0, used = 0;
+    bool ok = true;
+    for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
+      const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
+      // (each K tile is 8 bytes of a row)
+      const int align = p.align >= 16 && t.kt0 % 2 != 0 ? 8 : p.align, own = warp - kScale0;
+      switch (align) {
+        case 16: ok = bring_scales<kTok, 16>(p, ring, t, batch, used, own, lane); break;
+        case 8: ok = bring_scales<kTok, 8>(p, ring, t, batch, used, own, lane); break;
+        case 4: ok = bring_scales<kTok, 4>(p, ring, t, batch, used, own, lane); break;
+        default: ok = bring_scales<kTok, 1>(p, ring, t, batch, used, own, lane); break;
+      }
+      batch += (t.k_tiles + batch_of(kTok) - 1) / batch_of(kTok);
+      used += t.k_tiles;
+    }
+  } else if (warp >= kOut0) {
+    // ---- output: warp kOut0 + w has TMEM lane quadrant w, thread = weight row
+    const int quad = warp - kOut0, row = quad * 32 + lane;
+    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t read_of_leader = dev::mapa(bar_read, leader);
+    const uint32_t s_mine = s_out + (uint32_t)quad * (out_bytes(kTok) / kOutWarps);
+    uint32_t turn = 0u, chunk = 0u;
+    for (int tile = tile0; tile < p.tile_end; tile += step, ++turn) {
+      const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
+      const int n = t.n0 + row, live = min(kTok, p.M - t.m0);
+      const float bias = p.bias && n < p.N ? __uint_as_float((uint32_t)p.bias[(long long)t.l * p.N + n] << 16) : 0.0f;
+      if (!__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_acc, turn & 1u, kRoleEpiMma, (int)turn))) break;
+      dev::tc_fence_after();
+      if (out_boxes(kTok) && p.c_boxes && split == 1) {
+        const int n_box = t.n0 + quad * 32;
+        for (int g = 0; g * kOutTokens < live; ++g, ++chunk) {
+          uint32_t v[2][16];
+          dev::tmem_ld_x16(t_row + (uint32_t)(g * kOutTokens), v[0]);
+          dev::tmem_ld_x16(t_row + (uint32_t)(g * kOutTokens) + 16u, v[1]);
+          if (lane == 0) tma_store_wait_read<1>();           // the chunk before the last has left its place
           dev::tmem_wait_ld();
+          __syncwarp();
+          const uint32_t to = s_mine + (chunk & 1u) * (kOutTokens * 32u * 4u);
+          if (p.c_f32) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * q + e] = u[e], v[8 + 4 * q + e] = 0u;
+            for (int e = 0; e < kOutTokens; ++e) dev::st_shared_f32(to + 128u * e + 4u * lane, __uint_as_float(v[e / 16][e % 16]) + bias);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kOutTokens; ++e) {
+              st_shared_u16(to + 64u * e + 2u * lane, dev::pack_bf16x2(__uint_as_float(v[e / 16][e % 16]) + bias, 0.0f));
+            }
+          }
+          dev::fence_proxy_async_shared();
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if ((g + 1) * kOutTokens >= live) dev::mbar_arrive_remote_relaxed(read_of_leader);    // all of it is read
+            if (n_box < p.N) tma_store_3d(&c_map, to, n_box, t.m0 + g * kOutTokens, t.l);
+          }
         }
-      } else {
-        load_acc16(t_row + 16u * g, 0u, false, v);
+        continue;
       }
-      const int cols = min(16, live - g * 16);
-      if (split > 1) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (e < cols) dev::st_shared_u32(base + (uint32_t)((g * 16 + e) * kMmaM + row) * 4u, v[e]);
+      for (int g = 0; g * 16 < live; ++g) {
+        uint32_t v[16];
+        __syncwarp();
+        load_acc16(t_row + 16u * g, 0u, false, v);
+        if ((g + 1) * 16 >= live) {                          // the accumulator may be written again
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive_remote_relaxed(read_of_leader);
         }
-      } else if (n < p.N) {
-        const long long at = ((long long)l * p.M + m0 + g * 16) * p.N + n;
+        const int cols = min(16, live - g * 16);
+        if (split > 1) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (e < cols) store_mx(p, at + (long long)e * p.N, p.bias ? __uint_as_float(v[e]) + bias : __uint_as_float(v[e]));
+          for (int e = 0; e < 16; ++e) {
+            if (e < cols) dev::st_shared_u32(base + (uint32_t)((g * 16 + e) * kMmaM + row) * 4u, v[e]);
+          }
+        } else if (n < p.N) {
+          const int size = p.c_f32 ? 4 : 2;
+          uint8_t* to = static_cast<uint8_t*>(p.c) + (((long long)t.l * p.M + t.m0 + g * 16) * p.N + n) * size;
+          if (p.c_f32) {
+            store_tokens<true>(to, (long long)p.N * 4, v, bias, cols);
+          } else {
+            store_tokens<false>(to, (long long)p.N * 2, v, bias, cols);
+          }
         }
       }
     }
+    if (lane == 0 && chunk > 0u) tma_store_wait();
   }
+  __syncwarp();
+
   if (split > 1) {
     // this rank's slice of the tokens, a column a warp and four weight rows a lane
-    __syncwarp();
+    const MxTile& t = tile_first;
+    const int live = min(kTok, p.M - t.m0);
     dev::cluster_arrive_release();
     dev::cluster_wait_acquire();
     const int c0 = live * rank / split, c1 = live * (rank + 1) / split;
@@ -304,80 +589,80 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       float v[4];
       for (int r = 0; r < split; ++r) {
         float part[4];
-        dev::ld_cluster_f32x4(dev::mapa(base + (uint32_t)(col * kMmaM + r4) * 4u, (uint32_t)r), part);
+        dev::ld_cluster_f32x4(dev::mapa(base + (uint32_t)(col * kMmaM + r4) * 4u, (uint32_t)(2 * r + half)), part);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = r == 0 ? part[e] : v[e] + part[e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int nn = n0 + r4 + e;
+        const int nn = t.n0 + r4 + e;
         if (nn >= p.N) continue;
-        const float b = p.bias ? __uint_as_float((uint32_t)p.bias[(long long)l * p.N + nn] << 16) : 0.0f;
-        store_mx(p, ((long long)l * p.M + m0 + col) * p.N + nn, p.bias ? v[e] + b : v[e]);
+        const float b = p.bias ? __uint_as_float((uint32_t)p.bias[(long long)t.l * p.N + nn] << 16) : 0.0f;
+        store_mx(p, ((long long)t.l * p.M + t.m0 + col) * p.N + nn, p.bias ? v[e] + b : v[e]);
       }
     }
   }
 
-  // ---- teardown.  After a failed wait, copies and MMAs in flight land (for a
-  // bounded time) before the CTA gives up its memory.
-  if (dev::ld_shared_u32(slot_abort) != 0u) {
-    const unsigned long long drain_ns = 10000000ull;   // 10 ms
-    if (threadIdx.x == 0) {
-      for (int s = 0; s < issued && s < stages; ++s) {
-        drain_wait(bar_full + 8u * s, (uint32_t)(((issued - 1 - s) / stages) & 1), drain_ns);
-      }
+  // ---- teardown.  After a failed wait, copies in flight land (for a bounded time)
+  // before the pair gives up its memory: the leader sees both CTAs' copies, and the
+  // other one leaves only after it.
+  if (threadIdx.x == 0 && half == 0 && dev::ld_shared_u32(slot_abort) != 0u) {
+    for (int s = 0; s < issued && s < stages; ++s) {
+      drain_wait(bar_full + 8u * s, (uint32_t)(((issued - 1 - s) / stages) & 1), kDrainNs);
     }
-    if (warp == 2) drain_wait(bar_acc, 0u, drain_ns);
   }
-  // No CTA leaves while another of the cluster may still read its shared memory.
+  // No CTA leaves, or frees tensor memory, while another of the cluster may still read
+  // its shared memory, arrive on its barriers or run MMAs on it.
   dev::tc_fence_before();
   __syncwarp();
-  if (split > 1) {
-    dev::cluster_arrive_release();
-    dev::cluster_wait_acquire();
-  } else {
-    __syncthreads();
-  }
+  dev::cluster_arrive_release();
+  dev::cluster_wait_acquire();
   if (warp == 2) {
     dev::tc_fence_after();
-    dev::tmem_dealloc(tmem, p.tmem_cols);
+    tmem_dealloc_pair(tmem, p.tmem_cols);
   }
 }
 
 // ---------------------------------------------------------------- launch
+// How a product runs: tiles of 256 weight rows by `tokens`, counted tokens first,
+// then rows, then batches; the first `whole` of them on pairs of CTAs that take one
+// after another, the others on `split` pairs each.
 struct MxPlan {
-  int tokens, split, stages;
+  int tokens;
+  int whole;
+  int split;
+};
+struct MxRing {
+  int stages;
   uint32_t tmem_cols;
   size_t smem;
 };
 
-constexpr int kTokens[] = {8, 16, 32, 64, 128, 256};
+constexpr int kTokens[] = {16, 32, 64, 128, 256};
 
 // Shared memory of a CTA, at least its share of tensor memory in the SM's: CTAs
 // that fit one SM by shared memory, of whatever kernels, never wait for each
 // other's columns.
 size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& dev) {
-  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + kMxBarBytes;
+  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + out_bytes(tok) + kMxBarBytes;
   const size_t sums = split > 1 ? (size_t)kAlignSlack + (size_t)tok * kMmaM * 4 : 0;
   return std::max(std::max(ring, sums), std::min(dev.smem_per_sm * cols / 512, dev.smem_optin));
 }
 
-bool make_plan(int tokens, int split, int k_tiles, const DeviceSize& dev, MxPlan* out) {
-  const int mine = (k_tiles + split - 1) / split;
-  for (int stages = std::min(mine, kMxStages); stages >= 1; --stages) {
+// The ring for CTAs of `k_tiles` K tiles (of all their tiles).
+MxRing ring_of(int tokens, int split, long long k_tiles, const DeviceSize& dev) {
+  const int most = tokens <= 64 ? 6 : kMxStages;
+  for (int stages = (int)std::min<long long>(k_tiles, most); stages > 1; --stages) {
     const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)stages * scale_cols(tokens));
-    if (cols > 512u) continue;
     const size_t smem = mx_smem(tokens, stages, split, cols, dev);
-    if (smem > dev.smem_optin) continue;
-    *out = MxPlan{tokens, split, stages, cols, smem};
-    return true;
+    if (cols <= 512u && smem <= dev.smem_optin) return MxRing{stages, cols, smem};
   }
-  return false;
+  const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + scale_cols(tokens));
+  return MxRing{1, cols, mx_smem(tokens, 1, split, cols, dev)};
 }
 
 void* kernel_of(int tokens) {
   switch (tokens) {
-    case 8: return (void*)mx4_kernel<8>;
     case 16: return (void*)mx4_kernel<16>;
     case 32: return (void*)mx4_kernel<32>;
     case 64: return (void*)mx4_kernel<64>;
@@ -393,35 +678,77 @@ cudaError_t read_and_clear_fault_mx4(int* out_words) {
   return cudaMemcpyToSymbol(g_fault, zeros, sizeof(zeros));
 }
 
+// Clusters of 1, 2, 3 and 4 pairs resident at once, a CTA an SM.
+struct MxDevice {
+  bool ready;
+  int clusters[kMaxSplit];
+};
+
 // The current device's kernels, prepared at their first use.
-int prepare_mx4(int device, const DeviceSize& dev) {
+int prepare_mx4(const DeviceSize& dev, MxDevice* out) {
   static std::mutex mu;
-  static bool ready[kMaxDevices] = {};
+  static MxDevice devices[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
-  if (ready[device]) return SPLITK_OK;
-  for (int t : kTokens) {
-    if (cudaFuncSetAttribute(kernel_of(t), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dev.smem_optin) != cudaSuccess) {
+  MxDevice& d = devices[dev.device];
+  if (!d.ready) {
+    cudaError_t e = cudaSuccess;
+    for (int t : kTokens) {
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel_of(t), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dev.smem_optin);
+    }
+    for (int i = 0; e == cudaSuccess && i < kMaxSplit; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2u * (i + 1));
+      cfg.blockDim = dim3(kMxThreads);
+      cfg.dynamicSmemBytes = dev.smem_optin;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 2u * (i + 1);
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[i], kernel_of(256), &cfg);
+    }
+    if (e != cudaSuccess) {
       cudaGetLastError();
       return SPLITK_ERR_CUDA;
     }
+    add_fault_reader(dev.device, read_and_clear_fault_mx4);
+    d.ready = true;
   }
-  add_fault_reader(device, read_and_clear_fault_mx4);
-  ready[device] = true;
+  *out = d;
   return SPLITK_OK;
 }
 
-MxPlan plan_mx4(int M, int N, int K, int L, const DeviceSize& dev) {
+// What a launch of `tiles` tiles costs, in microseconds.
+double launch_us(long long tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
+  const int fit = d.clusters[split - 1];
+  if (tiles == 0) return 0.0;
+  if (fit <= 0 || split > k_tiles) return 1e30;
+  const double rounds = (double)((tiles + fit - 1) / fit);
+  const double step = tokens == 256 ? 0.43 : tokens == 128 ? 0.38 : 0.36;
+  const double each = step * ((k_tiles + split - 1) / split);
+  return rounds * each + (split > 1 ? rounds * 4.5 : 4.0 + (rounds - 1) * 0.5) + (split > 1 ? 0.3 : 0.0);
+}
+
+MxPlan plan_mx4(int M, int N, int K, int L, const MxDevice& d) {
   const int k_tiles = (K + kTileK - 1) / kTileK;
-  int tokens = 256;
-  for (int t : {128, 64, 32, 16, 8}) {
-    if (t >= M) tokens = t;
-  }
-  const long long tiles = (long long)((M + tokens - 1) / tokens) * ((N + kMmaM - 1) / kMmaM) * L;
-  int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= 2 * dev.num_sms && split * 2 <= k_tiles) split *= 2;
   MxPlan best{};
-  for (; split >= 1; --split) {
-    if (make_plan(tokens, split, k_tiles, dev, &best)) return best;
+  double least = 1e30;
+  for (int tokens : kTokens) {
+    if (tokens < 128 && tokens < M) continue;          // the smallest that holds M, or 128 or 256
+    if (tokens > 16 && tokens / 2 >= M) continue;
+    const long long tiles = (long long)((M + tokens - 1) / tokens) * ((N + 2 * kMmaM - 1) / (2 * kMmaM)) * L;
+    const double all = launch_us(tiles, tokens, k_tiles, 1, d);
+    if (all < least) least = all, best = MxPlan{tokens, (int)tiles, 1};
+    const long long rounds = d.clusters[0] > 0 ? tiles / d.clusters[0] : 0;
+    for (int split = 2; split <= kMaxSplit; ++split) {
+      for (long long whole : {0ll, rounds * d.clusters[0]}) {
+        const double us = launch_us(whole, tokens, k_tiles, 1, d) + launch_us(tiles - whole, tokens, k_tiles, split, d) -
+                          (whole > 0 ? 2.0 : 0.0);
+        if (us < least) least = us, best = MxPlan{tokens, (int)whole, split};
+      }
+    }
   }
   return best;
 }
@@ -429,14 +756,28 @@ MxPlan plan_mx4(int M, int N, int K, int L, const DeviceSize& dev) {
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
 
 template <int kTok>
-cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, const MxPlan& plan, cudaStream_t stream) {
-  CUtensorMap a_map, b_map;
-  if (!encode_codes(&a_map, a, p.K / 2, p.N, p.L, kMmaM) || !encode_codes(&b_map, b, p.K / 2, p.M, p.L, kTok)) {
+cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, const MxPlan& plan, const DeviceSize& dev,
+                       const MxDevice& d, cudaStream_t stream) {
+  CUtensorMap a_map, b_map, c_map = {};
+  if (!encode_codes(&a_map, a, p.K / 2, p.N, p.L, kMmaM) || !encode_codes(&b_map, b, p.K / 2, p.M, p.L, kTok / 2)) {
     return cudaErrorInvalidValue;
   }
-  const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + kMmaM - 1) / kMmaM) * p.L;
-  return launch_chained(mx4_kernel<kTok>, dim3((unsigned)(tiles * plan.split)), dim3(kMxThreads), plan.smem,
-                        (unsigned)plan.split, stream, a_map, b_map, p);
+  const bool boxes = out_boxes(kTok) && encode_output(&c_map, p.c, p.c_f32, p.N, p.M, p.L, 32, kOutTokens);
+  const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + 2 * kMmaM - 1) / (2 * kMmaM)) * p.L;
+  const int total = (p.K + kTileK - 1) / kTileK;
+  const auto launch = [&](int first, long long end, int split, long long clusters) {
+    const MxRing ring = ring_of(kTok, split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
+    MxParams q = p;
+    q.split = split, q.stages = ring.stages, q.tmem_cols = ring.tmem_cols;
+    q.tile0 = first, q.tile_end = (int)end, q.c_boxes = boxes;
+    return launch_chained(mx4_kernel<kTok>, dim3((unsigned)(clusters * 2 * split)), dim3(kMxThreads), ring.smem,
+                          (unsigned)(2 * split), stream, a_map, b_map, c_map, q);
+  };
+  if (plan.whole > 0) {
+    const cudaError_t e = launch(0, plan.whole, 1, std::min(plan.whole, d.clusters[0]));
+    if (e != cudaSuccess) return e;
+  }
+  return plan.whole < tiles ? launch(plan.whole, tiles, plan.split, tiles - plan.whole) : cudaSuccess;
 }
 
 }  // namespace
@@ -454,32 +795,39 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
   if (M < 1 || N < 1 || K < 1 || L < 1 || K % kMxBlock != 0 || L > 65535 || N > 65535 * 128 || K > (1 << 30) || M > (1 << 30)) {
     return SPLITK_ERR_INVALID_SHAPE;
   }
-  // a launch's CTAs: eight for each 8 tokens by 128 weight rows at most
-  if (((long long)M + 7) / 8 * ((N + 127) / 128) * L > (1ll << 27)) return SPLITK_ERR_INVALID_SHAPE;
+  // a launch's CTAs: eight for each 16 tokens by 256 weight rows at most
+  if (((long long)M + 15) / 16 * ((N + 255) / 256) * L > (1ll << 27)) return SPLITK_ERR_INVALID_SHAPE;
   if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(bias, 2) || !aligned(c, c_type == SPLITK_DTYPE_F32 ? 4u : 2u)) {
     return SPLITK_ERR_MISALIGNED;
   }
   DeviceSize dev;
   int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
-  rc = prepare_mx4(dev.device, dev);
+  MxDevice d;
+  rc = prepare_mx4(dev, &d);
   if (rc != SPLITK_OK) return rc;
-  const MxPlan plan = plan_mx4(M, N, K, L, dev);
-  if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;
+  const MxPlan plan = plan_mx4(M, N, K, L, d);
+  if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;      // no CTA pair of it fits the device
+  // (a CTA counts the K tiles of all its tiles)
+  if (((long long)plan.whole / std::max(d.clusters[0], 1) + 1) * ((K + kTileK - 1) / kTileK) > (1ll << 30)) {
+    return SPLITK_ERR_INVALID_SHAPE;
+  }
   const int blocks = K / kMxBlock;
-  const auto align = [&](const void* s) { return blocks % 8 == 0 && aligned(s, 8) ? 8 : blocks % 4 == 0 && aligned(s, 4) ? 4 : 1; };
+  const int align = blocks % 16 == 0 && aligned(a_scale, 16) && aligned(b_scale, 16) ? 16
+                    : blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
+                    : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4)   ? 4
+                                                                                      : 1;
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
-                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, plan.split, plan.stages,
-                   plan.tmem_cols, align(a_scale), align(b_scale), wait_limit_ns(), injected()};
+                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, false, align,
+                   wait_limit_ns(), injected()};
   const uint8_t *a = static_cast<const uint8_t*>(a_q), *b = static_cast<const uint8_t*>(b_q);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (plan.tokens) {
-    case 8: return launched(launch_mx4<8>(a, b, p, plan, s));
-    case 16: return launched(launch_mx4<16>(a, b, p, plan, s));
-    case 32: return launched(launch_mx4<32>(a, b, p, plan, s));
-    case 64: return launched(launch_mx4<64>(a, b, p, plan, s));
-    case 128: return launched(launch_mx4<128>(a, b, p, plan, s));
-    default: return launched(launch_mx4<256>(a, b, p, plan, s));
+    case 16: return launched(launch_mx4<16>(a, b, p, plan, dev, d, s));
+    case 32: return launched(launch_mx4<32>(a, b, p, plan, dev, d, s));
+    case 64: return launched(launch_mx4<64>(a, b, p, plan, dev, d, s));
+    case 128: return launched(launch_mx4<128>(a, b, p, plan, dev, d, s));
+    default: return launched(launch_mx4<256>(a, b, p, plan, dev, d, s));
   }
 }
 

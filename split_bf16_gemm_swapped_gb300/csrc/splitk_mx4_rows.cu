@@ -210,7 +210,7 @@ struct NormParams {
   const void* residual;     // bf16 or f32 [rows][width], or null
   void* residual_out;
   const void* weight;       // bf16 or f32 [width]
-  double mean_of;           // 1 / width
+  float mean_of;            // 1 / width
   float eps;
   uint8_t* codes;
   uint8_t* scale;
@@ -218,30 +218,51 @@ struct NormParams {
   bool x_vec, vec;          // 16-byte accesses to x; to the others
 };
 
-// The row's sum, in every thread of the row, in 64 bits: the mean is then the
-// exact one rounded to f32 for all but a few rows in a hundred (the threads' own
-// sums of 8 to 32 squares are f32, whose errors average out over the row), and so
-// codes do not depend on the order of additions.  A row is one warp (blockDim.x =
-// 32) or the whole CTA, which takes turns between two buffers.
-__device__ __forceinline__ double reduce_row(float own, int turn) {
-  double sum = own;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (blockDim.x == 32) return sum;
-  __shared__ double s_sum[2][32];
-  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, warps = (int)blockDim.x >> 5;
-  if (lane == 0) s_sum[turn][warp] = sum;
-  __syncthreads();
-  sum = lane < warps ? s_sum[turn][lane] : 0.0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  return sum;
+// A sum of squares as a whole number of 2^-shift.
+struct FixedSum {
+  int units;                // at most 2^31, of 32 addends below 2^26
+  int shift;
+  bool bad;                 // an addend was NaN or infinite
+};
+
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// v 2^e for |e| up to 252, in two factors that are normal numbers.
+__device__ __forceinline__ float scaled(float v, int e) { return v * power_of_two(e >> 1) * power_of_two(e - (e >> 1)); }
+
+// The sum over a warp of values >= 0, each rounded to the unit that lets the largest
+// have 26 bits: exact but for those roundings, whatever the order, in two
+// reductions of whole numbers (in f64, which has two lanes an SM, a row of 7168
+// took twice as long as its memory).
+__device__ __forceinline__ FixedSum warp_sum(float v) {
+  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));        // (NaN of either sign is above all)
+  FixedSum s;
+  s.bad = top >= 0x7F800000u;
+  s.shift = 25 - ((int)max(top >> 23, 1u) - 127);
+  s.units = __reduce_add_sync(0xFFFFFFFFu, s.bad ? 0 : __float2int_rn(scaled(v, s.shift)));
+  return s;
 }
 
-// A row whose sum of squares passes f32 has no codes.
-__device__ __forceinline__ float norm_factor(const NormParams& p, double sum) {
-  const float factor = 1.0f / sqrtf((float)(sum * p.mean_of) + p.eps);
-  return sum <= 3.4028234663852886e38 ? factor : __uint_as_float(0x7FC00000u);
+// 1 / sqrt(mean + eps) of the row, in every thread of it, from the threads' own sums
+// of 8 to 32 squares (f32, whose errors average out over the row).  The mean is the
+// exact one rounded to f32 for all but a few rows in a hundred, so codes do not
+// depend on the order of additions.  A row is one warp (blockDim.x = 32) or the whole
+// CTA, which takes turns between two buffers.  NaN for a row whose sum passes f32.
+__device__ __forceinline__ float row_factor(const NormParams& p, float own, int turn) {
+  FixedSum s = warp_sum(own);
+  if (blockDim.x != 32) {
+    __shared__ float s_sum[2][32];
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+    if (lane == 0) s_sum[turn][warp] = s.bad ? __uint_as_float(0x7FC00000u) : scaled((float)s.units, -s.shift);
+    __syncthreads();
+    s = warp_sum(lane < warps ? s_sum[turn][lane] : 0.0f);
+  }
+  // units 2^-shift / width, as the f32 quotient and what it leaves
+  const float hi = __int2float_rz(s.units), lo = (float)(s.units - (int)hi), inverse = p.mean_of, width = (float)p.width;
+  const float q = hi * inverse, mean = q + (fmaf(-q, width, hi) + lo) * inverse;
+  const float factor = 1.0f / sqrtf(scaled(mean, -s.shift) + p.eps);
+  const bool past = s.bad || !(scaled(hi, -s.shift) <= 3.4028234e38f);
+  return past ? __uint_as_float(0x7FC00000u) : factor;
 }
 
 // Values n of a thread's vector from y w: codes and scale stored.
@@ -313,7 +334,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) norm_kernel(const NormParams p
       if (e < p.width) norm_vector<kRes, kW>(p, xw[v], rw[v], base, e, true, z[v], sum);
     }
     if (kNext && row + stride < p.rows) load(row + stride);
-    const float factor = norm_factor(p, reduce_row(sum, turn));
+    const float factor = row_factor(p, sum, turn);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int e = (v * step + tid) * kVec;
@@ -332,40 +353,31 @@ __global__ void __launch_bounds__(kMaxRowThreads) long_norm_kernel(const NormPar
   dev::griddep_wait();
   const int row = (int)blockIdx.x, step = (int)blockDim.x * kVec;
   const long long base = (long long)row * p.width;
-  double total = 0.0;
   float z[kVec], sum = 0.0f, factor = 0.0f;
   Eight<kBf16> x;
   Eight<kRes ? kRes : 1> r;
   for (int pass = 0; pass < 2; ++pass) {
+    float low = 0.0f;                                   // what the thread's sum has lost (Kahan 1965)
     for (long long first = 0; first < p.width; first += step) {    // uniform: the blocks' lanes stay together
       const long long e = first + threadIdx.x * kVec;
       const bool in = e < p.width;
+      float part = 0.0f;
 #pragma unroll
       for (int j = 0; j < kVec; ++j) z[j] = 0.0f;
-      sum = 0.0f;
       if (in) {
         x.load(p.x, (long long)row * p.x_stride + e, p.x_vec);
         if (kRes != kNone) r.load(p.residual, base + e, p.vec);
-        norm_vector<kRes, kW>(p, x, r, base, (int)e, pass == 1, z, sum);
+        norm_vector<kRes, kW>(p, x, r, base, (int)e, pass == 1, z, part);
       }
       if (pass == 0) {
-        total += sum;
+        const float add = __fsub_rn(part, low), next = __fadd_rn(sum, add);
+        low = __fsub_rn(__fsub_rn(next, sum), add);
+        sum = next;
       } else {
         store_codes(p, base + e, in, z, factor);
       }
     }
-    if (pass == 0) {
-      // (the first pass's sums, of whole threads, are joined in 64 bits)
-      __shared__ double s_sum[kMaxRowThreads / 32];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-      if (threadIdx.x % 32 == 0) s_sum[threadIdx.x / 32] = total;
-      __syncthreads();
-      total = s_sum[threadIdx.x % 32];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-      factor = norm_factor(p, total);
-    }
+    if (pass == 0) factor = row_factor(p, sum, 0);
   }
 }
 
@@ -487,7 +499,7 @@ SPLITK_API int splitk_rmsnorm_mx4(const void* x, long long x_stride, const void*
   DeviceSize dev;
   rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
-  const NormParams p{x, x_stride, residual, residual_out, weight, 1.0 / D, eps, static_cast<uint8_t*>(codes),
+  const NormParams p{x, x_stride, residual, residual_out, weight, 1.0f / (float)D, eps, static_cast<uint8_t*>(codes),
                      static_cast<uint8_t*>(scale), M, D, aligned(x, 16) && x_stride % kVec == 0,
                      aligned(weight, 16) && aligned(residual, 16) && aligned(residual_out, 16)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
