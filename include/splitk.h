@@ -632,7 +632,7 @@ typedef struct splitk_adjust_t {
     const float *bias_values;        /* [M][bias_count]                               */
     const int *allowed;              /* [M][(V + 31) / 32]: bit v % 32 of word v / 32
                                         set where token v may come next               */
-    int history_length;              /* at most 2^29                                  */
+    int history_length;              /* at most 2^28                                  */
     int bias_count;                  /* at most 1024                                  */
 } splitk_adjust_t;
 

@@ -11,16 +11,21 @@
 //
 // each an f32 operation of its own, rounded once more to the logits' type.
 //
-// A CTA takes a span of one row's vocabulary.  It counts those of the row's history
-// that lie in the span in shared memory (whole numbers: any order gives the same),
-// while the span's logits are on their way to its threads' registers; a word of zero
-// says that a logit stays as it is.  Memory is the bound: each logit is read (but for
-// eight banned ones in a row, and in place for all that do not change) and written
-// once; the history is read once for each span, from L2.
+// A CTA takes a span of a row's vocabulary.  Its threads pass the logits on as they are
+// (banned ones as -inf, which need not be read), while they count those of the row's
+// history that lie in the span in shared memory (whole numbers: any order gives the
+// same) and list the tokens that they meet; then they go over the listed tokens one by
+// one.  Memory is the bound: each logit is read and written once, the history read
+// once for each span, from L2.  (Looking at every logit's count on its way took 224
+// instructions for eight of each of a warp's lanes, since some lane always has a
+// counted one: 256 x 131072 logits with histories of 4096 tokens 51-86 us.)
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "splitk.h"
 #include "splitk_device.cuh"
@@ -37,7 +42,7 @@ struct AdjustParams {
   long long stride, out_stride;
   void* out;
   splitk_adjust_t how;
-  int V, spans;
+  int V, spans;             // CTAs of a row
   bool in_place;
 };
 
@@ -65,278 +70,308 @@ __device__ __forceinline__ constexpr uint32_t minus_infinity() {
 }
 
 // A token's word: 2 for each time behind the prompt, 1 more (once) for one of the
-// prompt, kBiased for one that has a bias.
-constexpr uint32_t kBiased = 0x80000000u;
+// prompt, kBiased for one that has a bias, kTwice for one that has several.
+constexpr uint32_t kBiased = 0x80000000u, kTwice = 0x40000000u;
+constexpr int kMaxHistory = 1 << 28;       // counts stay below
 
-// A row's biases that lie in the span: slot and place in the list, in any order.
+// A row's biases that lie in the span: slot and place in the row's list, in any order.
 struct BiasList {
   int count;
   uint32_t entry[kMaxBias];                // place << 16 | slot
+  float value[kMaxBias];
+  __device__ __forceinline__ int place(int i) const { return (int)(entry[i] >> 16); }
+  __device__ __forceinline__ uint32_t slot(int i) const { return entry[i] & 0xFFFFu; }
 };
 
-// How a row's tokens change.
-struct Changes {
-  float repetition, presence, frequency;
-  const float* bias;
-  __device__ __forceinline__ Changes(const splitk_adjust_t& h, int row)
-      : repetition(h.repetition ? h.repetition[row] : 1.0f), presence(h.presence ? h.presence[row] : 0.0f),
-        frequency(h.frequency ? h.frequency[row] : 0.0f), bias(h.bias_values + (long long)row * h.bias_count) {}
-  // The sum of a slot's biases in the list's order.
-  __device__ __noinline__ float sum(const BiasList& list, uint32_t slot) const {
-    float total = 0.0f;
-    for (int last = -1, found = 0;; ++found) {
-      int next = kMaxBias;                 // the place after `last`
-      for (int i = 0; i < list.count; ++i) {
-        const int place = (int)(list.entry[i] >> 16);
-        if ((list.entry[i] & 0xFFFFu) == slot && place > last) next = min(next, place);
-      }
-      if (next == kMaxBias) return total;
-      total = found == 0 ? bias[next] : __fadd_rn(total, bias[next]);
-      last = next;
+// The sum of a slot's biases in the list's order, for its first one alone (entry
+// `first`): false for the others.
+__device__ __noinline__ bool bias_sum(const BiasList& list, int first, float* sum) {
+  const uint32_t slot = list.slot(first);
+  float total = list.value[first];
+  for (int last = list.place(first);;) {
+    int next = -1;                         // the entry of the place after `last`
+    for (int i = 0; i < list.count; ++i) {
+      if (list.slot(i) != slot) continue;
+      if (list.place(i) < list.place(first)) return false;
+      if (list.place(i) > last && (next < 0 || list.place(i) < list.place(next))) next = i;
     }
+    if (next < 0) break;
+    total = __fadd_rn(total, list.value[next]);
+    last = list.place(next);
   }
-  __device__ __forceinline__ float apply(float x, uint32_t word, const BiasList& list, uint32_t slot) const {
-    const uint32_t said = word & ~kBiased, count = said >> 1;
+  *sum = total;
+  return true;
+}
+
+// A row's numbers.
+struct RowNumbers {
+  float repetition, presence, frequency;
+  int length, prompt;
+  __device__ __forceinline__ RowNumbers(const splitk_adjust_t& h, int row) {
+    repetition = h.repetition ? h.repetition[row] : 1.0f;
+    presence = h.presence ? h.presence[row] : 0.0f;
+    frequency = h.frequency ? h.frequency[row] : 0.0f;
+    const long long most = h.history_length;
+    length = (int)(h.lengths ? max(0ll, min(h.lengths[row], most)) : most);
+    prompt = h.prompt_lengths ? (int)max(0ll, min(h.prompt_lengths[row], most)) : 0;
+  }
+  __device__ __forceinline__ float apply(float x, uint32_t word) const {
+    const uint32_t said = word & ~(kBiased | kTwice), count = said >> 1;
     if (said != 0u) x = x > 0.0f ? __fdiv_rn(x, repetition) : __fmul_rn(x, repetition);
     if (count != 0u) x = __fsub_rn(__fsub_rn(x, __fmul_rn(frequency, (float)count)), presence);
-    return (word & kBiased) != 0u ? __fadd_rn(x, sum(list, slot)) : x;
+    return x;
   }
 };
 
-// The words of the span [lo, lo + kSpan) and its biases; the caller's threads have
-// passed a barrier when it returns.
-template <int kThreads, int kSpan>
-__device__ __forceinline__ void mark(const splitk_adjust_t& h, int row, int lo, int V, uint32_t* words, BiasList& list) {
-  const int tid = (int)threadIdx.x;
-  for (int i = tid; i < kSpan / 4; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) list.count = 0;
-  __syncthreads();
-  // a token's slot, kSpan or more outside the span or the vocabulary
-  const auto slot_of = [&](long long id) { return (unsigned long long)id < (unsigned long long)V ? (uint32_t)((int)id - lo) : ~0u; };
-  if (h.history_length > 0) {
-    const int most = h.history_length;
-    const int n = h.lengths ? (int)max(0ll, min(h.lengths[row], (long long)most)) : most;
-    const long long prompt = h.prompt_lengths ? h.prompt_lengths[row] : 0;
-    const long long* tokens = h.history + (long long)row * most;
-    constexpr int kAtOnce = 8;             // loads in flight a thread
-    for (int first = tid; first < n; first += kAtOnce * kThreads) {
-      long long id[kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const long long i = (long long)first + j * kThreads;
-        id[j] = i < n ? tokens[i] : -1;
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const uint32_t at = slot_of(id[j]);
-        if (at >= (uint32_t)kSpan) continue;
-        if ((long long)first + j * kThreads >= prompt) {
-          atomicAdd(&words[at], 2u);
-        } else {
-          atomicOr(&words[at], 1u);
-        }
-      }
-    }
-  }
-  for (int b = tid; b < h.bias_count; b += kThreads) {
-    const uint32_t at = slot_of(h.bias_ids[(long long)row * h.bias_count + b]);
-    if (at >= (uint32_t)kSpan) continue;
-    atomicOr(&words[at], kBiased);
-    list.entry[atomicAdd(&list.count, 1)] = ((uint32_t)b << 16) | at;
-  }
-  __syncthreads();
-}
-
-// The eight bits of a row's `allowed` from logit e on (e > -8, < V).
-__device__ __forceinline__ uint32_t allowed_bits(const uint32_t* words, int e, int V) {
-  if (e < 0) return (words[0] << -e) & 0xFFu;
-  const int at = e >> 5, shift = e & 31;
-  uint32_t v = words[at] >> shift;
-  if (shift > 24 && 32 * (at + 1) < V) v |= words[at + 1] << (32 - shift);
-  return v & 0xFFu;
-}
-
-// Eight logits' bits: packed words in the 16-bit types.
 template <int kType>
-struct Group {
-  static constexpr bool kHalf = kType != SPLITK_DTYPE_F32;
-  static constexpr int kWords = kHalf ? 4 : 8, kSize = kHalf ? 2 : 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ uint32_t get(int j) const {
-    return !kHalf ? w[j % kWords] : j % 2 ? w[(j / 2) % kWords] >> 16 : w[(j / 2) % kWords] & 0xFFFFu;
+constexpr int kSize = kType == SPLITK_DTYPE_F32 ? 4 : 2;
+template <int kType>
+__device__ __forceinline__ uint32_t load_one(const void* p, long long at) {
+  return kType == SPLITK_DTYPE_F32 ? static_cast<const uint32_t*>(p)[at] : (uint32_t)static_cast<const uint16_t*>(p)[at];
+}
+template <int kType>
+__device__ __forceinline__ void store_one(void* p, long long at, uint32_t bits) {
+  if (kType == SPLITK_DTYPE_F32) {
+    static_cast<uint32_t*>(p)[at] = bits;
+  } else {
+    static_cast<uint16_t*>(p)[at] = (uint16_t)bits;
   }
-  __device__ __forceinline__ void set(int j, uint32_t bits) {
-    if (!kHalf) {
-      w[j % kWords] = bits;
-    } else {
-      uint32_t& v = w[(j / 2) % kWords];
-      v = j % 2 ? (v & 0xFFFFu) | (bits << 16) : (v & 0xFFFF0000u) | bits;
-    }
-  }
-  // those of `which`, at logit `at` of the tensor (16-byte aligned)
-  __device__ __forceinline__ void load(const void* p, long long at, uint32_t which) {
-    if (which == 0xFFu) {
-      const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * kSize);
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 v = from[i];
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if ((which >> j) & 1u) set(j, kHalf ? static_cast<const uint16_t*>(p)[at + j] : static_cast<const uint32_t*>(p)[at + j]);
-    }
-  }
-  __device__ __forceinline__ void store(void* p, long long at, uint32_t which) const {
-    if (which == 0xFFu) {
-      uint4* to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p) + at * kSize);
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (((which >> j) & 1u) == 0u) continue;
-      if (kHalf) {
-        static_cast<uint16_t*>(p)[at + j] = (uint16_t)get(j);
-      } else {
-        static_cast<uint32_t*>(p)[at + j] = get(j);
-      }
-    }
-  }
-};
+}
 
-// Rows of logits and out at the same place between 16-byte boundaries: kGroups
-// groups of eight logits a thread, from the boundary before the row's start on.
-template <int kType, int kThreads, int kGroups>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const AdjustParams p) {
-  constexpr int kSpan = kThreads * 8 * kGroups;
-  using G = Group<kType>;
-  extern __shared__ uint4 s_words[];
+// kEach bits of a row's `allowed` from logit e on, all of them the row's.
+template <int kEach>
+__device__ __forceinline__ uint32_t allowed_bits(const uint32_t* words, int e) {
+  constexpr uint32_t kAll = (1u << kEach) - 1u;
+  const int at = e >> 5, shift = e & 31;
+  if (e % 8 == 0) return reinterpret_cast<const uint8_t*>(words)[e / 8] & kAll;
+  uint32_t v = words[at] >> shift;
+  if (shift > 32 - kEach) v |= words[at + 1] << (32 - shift);
+  return v & kAll;
+}
+
+// 16 bytes of logits with those that have no bit in `keep` banned.
+template <int kType>
+__device__ __forceinline__ uint4 ban(uint4 v, uint32_t keep) {
+  constexpr uint32_t kInf = minus_infinity<kType>();
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (kType == SPLITK_DTYPE_F32) {
+      w[i] = (keep >> i) & 1u ? w[i] : kInf;
+    } else {
+      const uint32_t two = keep >> (2 * i), mask = ((two & 1u) | ((two & 2u) << 15)) * 0xFFFFu;
+      w[i] = (w[i] & mask) | (kInf * 0x10001u & ~mask);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 16 bytes from `shift` bytes (a logit's size times any number, below 16) behind
+// the start of `v` on, `u` being the next 16.
+__device__ __forceinline__ uint4 shifted(uint4 v, uint4 u, int shift) {
+  const uint32_t w[8] = {v.x, v.y, v.z, v.w, u.x, u.y, u.z, u.w};
+  const uint32_t bits = 8u * ((uint32_t)shift & 3u);
+  uint32_t o[4];
+  const auto from = [&](auto first) {
+    constexpr int k = decltype(first)::value;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[k + i], w[k + i + 1 < 8 ? k + i + 1 : 7], bits);
+  };
+  switch (shift >> 2) {                    // the same for all threads of a CTA
+    case 0: from(std::integral_constant<int, 0>{}); break;
+    case 1: from(std::integral_constant<int, 1>{}); break;
+    case 2: from(std::integral_constant<int, 2>{}); break;
+    default: from(std::integral_constant<int, 3>{}); break;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Threads resident an SM: 40 registers each for CTAs that are many and read short
+// histories, else 64.
+__host__ __device__ constexpr int threads_an_sm(int threads, int vecs) { return threads == 256 && vecs == 4 ? 1536 : 1024; }
+
+// kVecs times 16 bytes of a row of `out` a thread, from the 16-byte boundary before
+// the row's start on.  Where the row of logits lies otherwise between boundaries, a
+// vector is cut out of the two around it.  What a row's ends leave of a vector, or
+// would have read outside the row, goes a logit at a time.
+template <int kType, int kThreads, int kVecs>
+__global__ void __launch_bounds__(kThreads, threads_an_sm(kThreads, kVecs) / kThreads) adjust_kernel(const AdjustParams p) {
+  constexpr int kEach = 16 / kSize<kType>, kSpan = kThreads * kEach * kVecs;
+  static_assert(kSpan <= 1 << 16, "a slot has 16 bits");
+  extern __shared__ uint4 s_words[];                    // [kSpan] words, then the tokens met
   uint32_t* words = reinterpret_cast<uint32_t*>(s_words);
+  uint16_t* met = reinterpret_cast<uint16_t*>(words + kSpan);
   __shared__ BiasList list;
+  __shared__ int met_count;
   dev::griddep_launch_dependents();
   dev::griddep_wait();
   const splitk_adjust_t& h = p.how;
   const int row = (int)(blockIdx.x / (unsigned)p.spans), tid = (int)threadIdx.x;
-  const long long in = (long long)row * p.stride, to = (long long)row * p.out_stride;
-  const int past = (int)(((uintptr_t)p.logits + (uintptr_t)in * G::kSize) % 16) / G::kSize;   // the boundary
+  const uint8_t* logits = static_cast<const uint8_t*>(p.logits) + (long long)row * p.stride * kSize<kType>;
+  uint8_t* out = static_cast<uint8_t*>(p.out) + (long long)row * p.out_stride * kSize<kType>;
+  const int past = (int)((uintptr_t)out % 16) / kSize<kType>;
   const int lo = (int)(blockIdx.x % (unsigned)p.spans) * kSpan - past;
   const bool marked = h.history_length > 0 || h.bias_count > 0;
   const uint32_t* allowed =
       h.allowed ? reinterpret_cast<const uint32_t*>(h.allowed) + (long long)row * ((p.V + 31) / 32) : nullptr;
 
-  uint32_t live[kGroups], keep[kGroups];                // within the row; allowed
-  G x[kGroups];
+  // the first tokens of the history, without waiting for its length
+  constexpr int kTokens = threads_an_sm(kThreads, kVecs) > 1024 ? 4 : 8;        // a thread's loads at once
+  long long id[kTokens];
+  const auto load_tokens = [&](long long first, int end) {
+    const long long* tokens = h.history + (long long)row * h.history_length;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const int e = lo + (g * kThreads + tid) * 8;
-    live[g] = e >= p.V || e <= -8 ? 0u : (0xFFu << max(0, -e)) & (0xFFu >> max(0, e + 8 - p.V)) & 0xFFu;
-    keep[g] = live[g] == 0u ? 0u : allowed ? live[g] & allowed_bits(allowed, e, p.V) : live[g];
+    for (int j = 0; j < kTokens; ++j) {
+      const long long i = first + j * kThreads;
+      id[j] = i < end ? tokens[i] : -1;
+    }
+  };
+  const RowNumbers numbers(h, row);
+  const long long* bias_ids = h.bias_ids + (long long)row * h.bias_count;
+  const float* biases = h.bias_values + (long long)row * h.bias_count;
+  long long bias_id = tid < h.bias_count ? bias_ids[tid] : -1;
+  float bias = tid < h.bias_count ? biases[tid] : 0.0f;
+  if (kVecs < 4) load_tokens(tid, h.history_length);
+  if (marked) {
+#pragma unroll
+    for (int i = 0; i < kSpan / 4 / kThreads; ++i) s_words[i * kThreads + tid] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) list.count = 0, met_count = 0;
   }
+
+  // ---- the logits as they are
+  constexpr uint32_t kAll = (1u << kEach) - 1u;
+  // bytes between the boundary before a vector's logits and their start
+  const int shift = (int)(((uintptr_t)logits - (uintptr_t)past * kSize<kType>) % 16), margin = shift != 0 ? kEach : 0;
+  uint32_t keep[kVecs];                                 // of the vectors that are the row's with what is read around them
+  uint4 v[kVecs];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if (keep[g] != 0u && !p.in_place) x[g].load(p.logits, in + lo + (g * kThreads + tid) * 8, live[g]);
+  for (int i = 0; i < kVecs; ++i) {
+    const int e = lo + (i * kThreads + tid) * kEach;
+    keep[i] = e < margin || e + kEach + margin > p.V ? ~0u : allowed ? allowed_bits<kEach>(allowed, e) : kAll;
   }
-  const Changes changes(h, row);
-  if (marked) mark<kThreads, kSpan>(h, row, lo, p.V, words, list);
+  const uint8_t* from = logits + (long long)(lo + tid * kEach) * kSize<kType> - shift;
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    const int slot = (g * kThreads + tid) * 8;
-    const long long e = (long long)lo + slot;
-    uint32_t word[8] = {};
-    if (marked && keep[g] != 0u) {
-      const uint4 u = s_words[slot / 4], v = s_words[slot / 4 + 1];
-      word[0] = u.x, word[1] = u.y, word[2] = u.z, word[3] = u.w, word[4] = v.x, word[5] = v.y, word[6] = v.z, word[7] = v.w;
+  for (int i = 0; i < kVecs; ++i) {
+    if (keep[i] != 0u && keep[i] != ~0u && !(p.in_place && keep[i] == kAll)) {
+      v[i] = *reinterpret_cast<const uint4*>(from + i * kThreads * 16);
     }
-    const bool some = (word[0] | word[1] | word[2] | word[3] | word[4] | word[5] | word[6] | word[7]) != 0u;
-    if (p.in_place) {
-      if (!some && keep[g] == live[g]) continue;
-      if (keep[g] != 0u) x[g].load(p.logits, in + e, live[g]);
-    }
-    if (some) {
+  }
+  if (kVecs >= 4) load_tokens(tid, numbers.length);
+  uint8_t* into = out + (long long)(lo + tid * kEach) * kSize<kType>;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (word[j] != 0u) x[g].set(j, bits_of<kType>(changes.apply(value_of<kType>(x[g].get(j)), word[j], list, slot + j)));
+  for (int i = 0; i < kVecs; ++i) {
+    if (keep[i] == ~0u) {
+      const int e = lo + (i * kThreads + tid) * kEach;
+#pragma unroll 1
+      for (int j = max(e, 0); j < min(e + kEach, p.V); ++j) {
+        const bool kept = !allowed || ((allowed[j >> 5] >> (j & 31)) & 1u) != 0u;
+        if (!(kept && p.in_place)) store_one<kType>(out, j, kept ? load_one<kType>(logits, j) : minus_infinity<kType>());
       }
+      continue;
     }
-    if (keep[g] != live[g]) {
+    if (p.in_place && keep[i] == kAll) continue;
+    if (shift != 0 && keep[i] != 0u) {
+      v[i] = shifted(v[i], *reinterpret_cast<const uint4*>(from + i * kThreads * 16 + 16), shift);
+    }
+    if (keep[i] != kAll) v[i] = ban<kType>(v[i], keep[i]);
+    *reinterpret_cast<uint4*>(into + i * kThreads * 16) = v[i];
+  }
+  if (!marked) return;
+
+  // ---- the span's tokens counted
+  __syncthreads();
+  for (long long first = tid;;) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (((keep[g] >> j) & 1u) == 0u) x[g].set(j, minus_infinity<kType>());
-      }
+    for (int j = 0; j < kTokens; ++j) {
+      const uint32_t at = (uint32_t)id[j] - (uint32_t)lo;
+      const long long i = first + j * kThreads;
+      if ((unsigned long long)id[j] >= (unsigned long long)p.V || at >= (uint32_t)kSpan || i >= numbers.length) continue;
+      const uint32_t before = i >= numbers.prompt ? atomicAdd(&words[at], 2u) : atomicOr(&words[at], 1u);
+      if (before == 0u) met[atomicAdd(&met_count, 1)] = (uint16_t)at;
     }
-    if (live[g] != 0u) x[g].store(p.out, to + e, live[g]);
+    first += kTokens * kThreads;
+    if (first - tid >= numbers.length) break;
+    load_tokens(first, numbers.length);
+  }
+  for (int b = tid; b < h.bias_count; b += kThreads) {
+    if (b != tid) bias_id = bias_ids[b], bias = biases[b];
+    const uint32_t at = (uint32_t)bias_id - (uint32_t)lo;
+    if ((unsigned long long)bias_id >= (unsigned long long)p.V || at >= (uint32_t)kSpan) continue;
+    if ((atomicOr(&words[at], kBiased) & kBiased) != 0u) atomicOr(&words[at], kTwice);
+    const int i = atomicAdd(&list.count, 1);
+    list.entry[i] = ((uint32_t)b << 16) | at, list.value[i] = bias;
+  }
+  __syncthreads();
+
+  // ---- and changed, over what another thread has stored: those that were met and
+  // have no bias, and those that have
+  for (int i = tid; i < met_count + list.count; i += kThreads) {
+    const int b = i - met_count;
+    const uint32_t at = b < 0 ? met[i] : list.slot(b), word = words[at];
+    const int e = lo + (int)at;
+    const uint32_t bits = load_one<kType>(logits, e);
+    const uint32_t ok = allowed ? allowed[e >> 5] >> (e & 31) : 1u;
+    float sum = 0.0f;
+    if (b < 0) {
+      if ((word & kBiased) != 0u) continue;
+    } else if ((word & kTwice) == 0u) {
+      sum = list.value[b];
+    } else if (!bias_sum(list, b, &sum)) {
+      continue;
+    }
+    if ((ok & 1u) == 0u) continue;
+    float x = numbers.apply(value_of<kType>(bits), word);
+    if (b >= 0) x = __fadd_rn(x, sum);
+    store_one<kType>(out, e, bits_of<kType>(x));
   }
 }
 
-// Rows at different places: a thread's logits are kThreads apart, so that a warp's
-// accesses are consecutive.
-template <int kType, int kThreads, int kEach>
-__global__ void __launch_bounds__(kThreads) adjust_odd_kernel(const AdjustParams p) {
-  constexpr int kSpan = kThreads * kEach;
-  constexpr bool kHalf = kType != SPLITK_DTYPE_F32;
-  extern __shared__ uint4 s_words[];
-  uint32_t* words = reinterpret_cast<uint32_t*>(s_words);
-  __shared__ BiasList list;
-  dev::griddep_launch_dependents();
-  dev::griddep_wait();
-  const splitk_adjust_t& h = p.how;
-  const int row = (int)(blockIdx.x / (unsigned)p.spans), tid = (int)threadIdx.x;
-  const int lo = (int)(blockIdx.x % (unsigned)p.spans) * kSpan;
-  const long long in = (long long)row * p.stride + lo, to = (long long)row * p.out_stride + lo;
-  const bool marked = h.history_length > 0 || h.bias_count > 0;
-  const uint32_t* allowed =
-      h.allowed ? reinterpret_cast<const uint32_t*>(h.allowed) + (long long)row * ((p.V + 31) / 32) + lo / 32 : nullptr;
-  uint32_t keep = 0u, x[kEach];
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    const int e = j * kThreads + tid;
-    const bool k = lo + e < p.V && (!allowed || ((allowed[e / 32] >> (e % 32)) & 1u) != 0u);
-    keep |= (k ? 1u : 0u) << j;
-  }
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    const int e = j * kThreads + tid;
-    x[j] = minus_infinity<kType>();
-    if ((keep >> j) & 1u) x[j] = kHalf ? static_cast<const uint16_t*>(p.logits)[in + e] : static_cast<const uint32_t*>(p.logits)[in + e];
-  }
-  const Changes changes(h, row);
-  if (marked) mark<kThreads, kSpan>(h, row, lo, p.V, words, list);
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    const int e = j * kThreads + tid;
-    if (lo + e >= p.V) continue;
-    const uint32_t word = marked && ((keep >> j) & 1u) ? words[e] : 0u;
-    if (word != 0u) x[j] = bits_of<kType>(changes.apply(value_of<kType>(x[j]), word, list, (uint32_t)e));
-    if (kHalf) {
-      static_cast<uint16_t*>(p.out)[to + e] = (uint16_t)x[j];
-    } else {
-      static_cast<uint32_t*>(p.out)[to + e] = x[j];
-    }
-  }
-}
+// A kernel's shared memory: words of the span, and as many of its tokens as are met.
+template <int kType, int kThreads, int kVecs>
+constexpr int kSpanOf = kThreads * (16 / kSize<kType>) * kVecs;
+constexpr size_t smem_of(int span, int met) { return (size_t)span * 4 + (size_t)met * 2; }
 
-template <int kType, int kThreads, int kGroups>
-cudaError_t launch_adjust(AdjustParams& p, int M, bool even, cudaStream_t stream) {
-  constexpr int kSpan = kThreads * 8 * kGroups;
-  const int past = even ? 16 / Group<kType>::kSize - 1 : 0;           // at most, before a row's start
+template <int kType, int kThreads, int kVecs>
+cudaError_t launch_adjust(AdjustParams& p, int M, cudaStream_t stream) {
+  constexpr int kEach = 16 / kSize<kType>, kSpan = kSpanOf<kType, kThreads, kVecs>;
+  // (a row's start may be past a boundary: all of them alike, or by any number of logits)
+  const int past = p.out_stride % kEach == 0 ? (int)((uintptr_t)p.out % 16) / kSize<kType> : kEach - 1;
   p.spans = (p.V + past + kSpan - 1) / kSpan;
   const bool marked = p.how.history_length > 0 || p.how.bias_count > 0;
-  const size_t smem = marked ? (size_t)kSpan * 4 : 0;
-  const dim3 grid((unsigned)((long long)M * p.spans));
-  return even ? launch_chained(adjust_kernel<kType, kThreads, kGroups>, grid, dim3(kThreads), smem, 1, stream, p)
-              : launch_chained(adjust_odd_kernel<kType, kThreads, 8 * kGroups>, grid, dim3(kThreads), smem, 1, stream, p);
+  return launch_chained(adjust_kernel<kType, kThreads, kVecs>, dim3((unsigned)((long long)M * p.spans)), dim3(kThreads),
+                        marked ? smem_of(kSpan, std::min(kSpan, p.how.history_length)) : 0, 1, stream, p);
 }
 
+template <int kType, int kThreads, int kVecs>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(adjust_kernel<kType, kThreads, kVecs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)smem_of(kSpanOf<kType, kThreads, kVecs>, kSpanOf<kType, kThreads, kVecs>));
+}
+
+// Long spans read the history fewer times and have more loads in flight; short ones
+// fill the SMs and are the shortest chains of latencies.  Measured (us) with 256 x 1
+// vectors, 512 x 2, 256 x 4 and 512 x 4 a CTA: 1 x 131072 bf16, 1500 tokens 3.4, 3.5,
+// 4.8, 4.2; 64 x 32000 bf16, 1000 tokens 7.5, 5.1, 7.2, 6.4; 65 x 50001 f32, 300 tokens
+// 15.9, 13.3, 8.5, 12.2; 256 x 131072 bf16, 4096 tokens 113, 66, 60, 46, without 39, 29,
+// 22.3, 22.6; 256 x 50001 bf16, 1000 tokens 32, 23, 19.2, 18.2.
 template <int kType>
-cudaError_t choose_adjust(AdjustParams& p, int M, bool even, int num_sms, cudaStream_t stream) {
-  // long spans read the history fewer times; short ones fill the SMs
-  const long long all = (long long)M * p.V;
-  if (all <= (long long)num_sms * 4 * 2048) return launch_adjust<kType, 256, 1>(p, M, even, stream);
-  return launch_adjust<kType, 256, 4>(p, M, even, stream);
+cudaError_t choose_adjust(AdjustParams& p, int M, const DeviceSize& dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};                // a bit a device
+  static_assert(kMaxDevices <= 64, "");
+  const uint64_t bit = 1ull << dev.device;
+  if ((ready.load() & bit) == 0) {
+    cudaError_t e = allow_smem<kType, 256, 1>();
+    if (e == cudaSuccess) e = allow_smem<kType, 512, 2>();
+    if (e == cudaSuccess) e = allow_smem<kType, 256, 4>();
+    if (e == cudaSuccess) e = allow_smem<kType, 512, 4>();
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  constexpr int kEach = 16 / kSize<kType>;
+  const long long vectors = (long long)M * ((p.V + kEach - 1) / kEach);
+  if (vectors <= (long long)dev.num_sms * 1024) return launch_adjust<kType, 256, 1>(p, M, stream);
+  if (vectors <= (long long)dev.num_sms * 2048) return launch_adjust<kType, 512, 2>(p, M, stream);
+  return p.how.history_length > 512 ? launch_adjust<kType, 512, 4>(p, M, stream) : launch_adjust<kType, 256, 4>(p, M, stream);
 }
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1u)) == 0; }
@@ -355,7 +390,7 @@ SPLITK_API int splitk_adjust_logits(const void* logits, int type, long long stri
   const splitk_adjust_t& h = *how;
   if (type != SPLITK_DTYPE_BF16 && type != SPLITK_DTYPE_F32 && type != SPLITK_DTYPE_F16) return SPLITK_ERR_INVALID_ARGUMENT;
   if (M < 1 || V < 1 || V > (1 << 22) || stride < V || out_stride < V) return SPLITK_ERR_INVALID_SHAPE;
-  if (h.history_length < 0 || h.history_length > (1 << 29) || h.bias_count < 0 || h.bias_count > kMaxBias) {
+  if (h.history_length < 0 || h.history_length > kMaxHistory || h.bias_count < 0 || h.bias_count > kMaxBias) {
     return SPLITK_ERR_INVALID_ARGUMENT;
   }
   if ((h.history_length > 0 && !h.history) || (h.bias_count > 0 && (!h.bias_ids || !h.bias_values))) return SPLITK_ERR_NULL;
@@ -366,18 +401,16 @@ SPLITK_API int splitk_adjust_logits(const void* logits, int type, long long stri
       !aligned(h.bias_ids, 8) || !aligned(h.bias_values, 4) || !aligned(h.allowed, 4)) {
     return SPLITK_ERR_MISALIGNED;
   }
-  // a launch's CTAs, of at least 2048 logits
-  if ((long long)M * (V / 2048 + 2) > 0x7FFFFFFFll) return SPLITK_ERR_INVALID_SHAPE;
+  // a launch's CTAs, of at least 1024 logits
+  if ((long long)M * (V / 1024 + 2) > 0x7FFFFFFFll) return SPLITK_ERR_INVALID_SHAPE;
   DeviceSize dev;
   const int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
   AdjustParams p{logits, stride, out_stride, out, h, V, 1, out == logits && stride == out_stride};
-  // rows of both at the same place between 16-byte boundaries
-  const bool even = ((uintptr_t)logits - (uintptr_t)out) % 16 == 0 && (stride - out_stride) * (long long)size % 16 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == SPLITK_DTYPE_F32   ? choose_adjust<SPLITK_DTYPE_F32>(p, M, even, dev.num_sms, s)
-                        : type == SPLITK_DTYPE_F16 ? choose_adjust<SPLITK_DTYPE_F16>(p, M, even, dev.num_sms, s)
-                                                   : choose_adjust<SPLITK_DTYPE_BF16>(p, M, even, dev.num_sms, s);
+  const cudaError_t e = type == SPLITK_DTYPE_F32   ? choose_adjust<SPLITK_DTYPE_F32>(p, M, dev, s)
+                        : type == SPLITK_DTYPE_F16 ? choose_adjust<SPLITK_DTYPE_F16>(p, M, dev, s)
+                                                   : choose_adjust<SPLITK_DTYPE_BF16>(p, M, dev, s);
   return launched(e);
 }
 
