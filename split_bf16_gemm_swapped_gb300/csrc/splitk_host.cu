@@ -1270,19 +1270,6 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_output(CUtensorMap* map, void* ptr, bool f32, int N, int rows, int L, int box_n, int box_rows) {
-  auto fn = encode_fn();
-  const cuuint64_t size = f32 ? 4u : 2u;
-  if (!fn || (uintptr_t)ptr % 16 != 0 || (cuuint64_t)N * size % 16 != 0) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)rows, (cuuint64_t)L};
-  cuuint64_t strides[2] = {(cuuint64_t)N * size, (cuuint64_t)N * (cuuint64_t)rows * size};
-  cuuint32_t box[3] = {(cuuint32_t)box_n, (cuuint32_t)box_rows, 1u};
-  cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 unsigned injected() { return g_inject.load(); }

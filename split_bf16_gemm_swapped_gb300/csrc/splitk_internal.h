@@ -194,9 +194,6 @@ void add_fault_reader(int device, FaultReader read);
 // the bound on a kernel's waits and its injected failures.
 bool encode_codes(CUtensorMap* map, const void* ptr, int K, int rows, int L, int box_rows);
 unsigned long long wait_limit_ns();
-// A map of an output [L][rows][N] (bf16 or f32) written in boxes of box_n by
-// box_rows; false where its alignment or N does not allow one.
-bool encode_output(CUtensorMap* map, void* ptr, bool f32, int N, int rows, int L, int box_n, int box_rows);
 unsigned injected();
 
 // Defined in splitk_logprobs.cu.

@@ -40,6 +40,8 @@ namespace {
 
 // Warps: 0 copies of codes, 1 MMAs, 2 copies of scales into tensor memory, 3 set-up,
 // then those that bring scales and those that store the output.
+// (Four more output warps would leave 128 registers a thread, and what is spilled then
+// takes the issuing thread twice its time.)
 constexpr int kScale0 = 4, kScaleWarps = 4, kOut0 = kScale0 + kScaleWarps, kOutWarps = 4;
 constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
 constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
@@ -47,7 +49,6 @@ constexpr int kMxStages = 10;                        // at most
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
 constexpr uint32_t kMxBarBytes = 512;
-constexpr int kOutTokens = 32;                       // of a chunk that an output warp stores at once
 constexpr int kMaxSplit = 4;                         // pairs of a cluster
 constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
 
@@ -58,11 +59,6 @@ __host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAt
 __host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kCodesA + codes_b(tok) + scales_of(tok); }
 __host__ __device__ constexpr uint32_t mx_acc_cols(int tok) { return tok < 32 ? 32u : (uint32_t)tok; }
 __host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a stage
-
-// Chunks of 32 weight rows by kOutTokens tokens on their way out, two for each output
-// warp, in kernels for many tokens.
-__host__ __device__ constexpr bool out_boxes(int tok) { return tok >= 128; }
-__host__ __device__ constexpr uint32_t out_bytes(int tok) { return out_boxes(tok) ? kOutWarps * 2u * kOutTokens * 32u * 4u : 0u; }
 
 // kind::mxf4: E2M1 operands, both K-major, E8M0 scales for each 32, f32 accumulator;
 // the scales of a K = 64 step are the lower (id 0) or upper (id 2) half of a word.
@@ -110,24 +106,8 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int
       : "memory");
 }
 
-// A box of shared memory to global memory, in this thread's bulk group.
-__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
-               "r"(c1), "r"(c2), "r"(src)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// At most `kLeft` of this thread's stores have not read their shared memory yet, or
-// none is not in global memory.
-template <int kLeft>
-__device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
-}
-__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(addr), "r"(v) : "memory");
-}
+// A line of global memory to L2.
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
@@ -157,17 +137,15 @@ struct MxParams {
   int split, stages;
   int tile0, tile_end;      // the launch's tiles
   uint32_t tmem_cols;
-  bool c_boxes;             // C may be stored by TMA (c_map)
   int align;                // of the scales' rows: 16, 8, 4 or 1 bytes
   unsigned long long limit_ns;
   unsigned inject;
 };
 
-// K tiles of a batch of scales: 8 bytes of a row each; a sector where registers allow.
-__host__ __device__ constexpr int batch_of(int tok) { return tok >= 128 ? 2 : 4; }
+// K tiles of a batch of scales: 16 bytes of a row.
+constexpr int kBatch = 2;
 
 // The scale codes of a batch of K tiles: two words of four for each row and tile.
-template <int kBatch>
 struct ScaleRow {
   uint32_t w[2 * kBatch];
   // Codes [at, limit) of the row at `row`, 127 past the limit (its codes there are
@@ -227,26 +205,18 @@ __device__ __forceinline__ void store_mx(const MxParams& p, long long at, float 
   }
 }
 
-// A thread's weight row of `cols` consecutive tokens, `pitch` bytes apart from `to`
-// on.  (Sixteen stores without a branch between them: with a choice of type and a
-// check for each, a warp took 125 clocks a store, and 256 tokens 17 us.)
-template <bool kF32>
-__device__ __forceinline__ void store_tokens(uint8_t* to, long long pitch, const uint32_t (&v)[16], float bias, int cols) {
-  const auto one = [&](uint8_t* at, uint32_t bits) {
-    const float r = __uint_as_float(bits) + bias;
-    if (kF32) {
-      *reinterpret_cast<float*>(at) = r;
-    } else {
-      *reinterpret_cast<uint16_t*>(at) = (uint16_t)dev::pack_bf16x2(r, 0.0f);
-    }
-  };
-  if (cols == 16) {
+// A thread's weight row of kCols consecutive tokens, `pitch` bytes apart from `to` on, the
+// first `cols` of them.  (Stores without a branch between them: with a choice of type
+// and a check for each, a warp took 125 clocks a store, and 256 tokens 17 us.)
+template <int kCols, class F>
+__device__ __forceinline__ void store_tokens(uint8_t* to, long long pitch, int cols, F one) {
+  if (cols >= kCols) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e, to += pitch) one(to, v[e]);
+    for (int e = 0; e < kCols; ++e, to += pitch) one(to, e);
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e, to += pitch) {
-      if (e < cols) one(to, v[e]);
+    for (int e = 0; e < kCols; ++e, to += pitch) {
+      if (e < cols) one(to, e);
     }
   }
 }
@@ -270,28 +240,34 @@ struct MxTile {
 
 // What the scale warps work with.
 struct ScaleRing {
-  uint32_t slots, bar_scale_of_leader, bar_free, bar_turn;
+  uint32_t slots, bar_scale_of_leader, bar_free;
   int stages;
   Waiter waiter;
 };
 
-// One scale warp's batches of a tile; `batch` and `used` count the CTA's batches and
-// K tiles before it.  A lane has rows lane + 32 g of each group of 128: for each
-// word of K their four codes lie side by side in shared memory, one 16-byte store.
-// A batch's loads are under way while other warps' batches are stored, and while the
-// ring's slots become free.  Batches are stored in order: a warp ahead by two rounds
-// of the ring would take the phase before the last for the last.
+// One scale warp's part of a tile whose first K tile is the CTA's `used`-th, at ring
+// position `pos` (carried on over all of them).  Pairs of slots belong to the warps in
+// turn (a ring that goes round has an even number), so that a warp meets every phase
+// of its slots' barriers, and warps do not wait for one another: passing a turn bounded
+// tiles of 256 tokens at 0.4 us each.  A lane has rows lane + 32 g of each group of
+// 128: for each word of K their four codes lie side by side in shared memory, one
+// 16-byte store.  The loads of a pair of K tiles are under way while its slots become
+// free and while other warps store theirs.
 template <int kTok, int kAlign>
-__device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing& r, const MxTile& t, int batch, int used,
+__device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing& r, const MxTile& t, int used, RingPos& pos,
                                              int warp, int lane) {
   constexpr int kGroups = groups_b(kTok), kLive = kTok >= 128 ? 4 : (kTok + 31) / 32;     // 32s of tokens in a group
-  constexpr int kBatch = batch_of(kTok);
   const int blocks = p.K / kMxBlock, limit = min(blocks, (t.kt0 + t.k_tiles) * (kTileK / kMxBlock));
   const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
-  for (int first = 0; first < t.k_tiles; first += kBatch, ++batch) {
-    if (batch % kScaleWarps != warp) continue;
+  for (int first = 0; first < t.k_tiles;) {
+    const int here = pos.index % 2 == 0 && first + 1 < t.k_tiles ? 2 : 1;           // K tiles up to the pair's end
+    if (pos.index / 2 % kScaleWarps != warp) {
+      for (int i = 0; i < here; ++i) pos.advance(1, r.stages);
+      first += here;
+      continue;
+    }
     const int at = (t.kt0 + first) * (kTileK / kMxBlock);
-    ScaleRow<kBatch> a[4], b[kGroups][kLive];
+    ScaleRow a[4], b[kGroups][kLive];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int n = t.n0 + lane + 32 * g;
@@ -306,18 +282,12 @@ __device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing&
                                       p.b_scale, b_end);
       }
     }
-    if (batch > 0 && !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_turn + 8u * warp, (uint32_t)((batch - 1) / kScaleWarps) & 1u,
-                                                                    kRoleEpiDecode, first))) {
-      return false;
-    }
-    RingPos pos = RingPos::at(used + first, r.stages);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i, pos.advance(1, r.stages)) {
-      const int kt = first + i;
-      if (kt >= t.k_tiles) break;
+    for (int i = 0; i < kBatch; ++i) {
+      if (i >= here) break;
       const uint32_t s = (uint32_t)pos.index;
-      if (used + kt >= r.stages &&
-          !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_free + 8u * s, pos.phase ^ 1u, kRoleEpiDecode, kt))) return false;
+      if (used + first + i >= r.stages &&
+          !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_free + 8u * s, pos.phase ^ 1u, kRoleEpiDecode, first + i))) return false;
       const uint32_t dst = r.slots + s * scales_of(kTok) + 16u * lane;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
@@ -336,8 +306,9 @@ __device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing&
         dev::fence_release_shared_cluster();
         dev::mbar_arrive_remote_relaxed(r.bar_scale_of_leader + 8u * s);
       }
+      pos.advance(1, r.stages);
     }
-    if (lane == 0) dev::mbar_arrive(r.bar_turn + 8u * ((warp + 1) % kScaleWarps));
+    first += here;
   }
   return true;
 }
@@ -346,24 +317,21 @@ __device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing&
 // (its sums go where the ring was).
 template <int kTok>
 __global__ void __launch_bounds__(kMxThreads, 1)
-    mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
-               const __grid_constant__ CUtensorMap c_map, const MxParams p) {
+    mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const MxParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (dev::smem_u32(smem_raw) + (kAlignSlack - 1)) & ~(kAlignSlack - 1);
   const int stages = p.stages, split = p.split;
   const uint32_t s_a = base;
   const uint32_t s_b = s_a + (uint32_t)stages * kCodesA;
   const uint32_t s_s = s_b + (uint32_t)stages * codes_b(kTok);
-  const uint32_t s_out = s_s + (uint32_t)stages * scales_of(kTok);
-  const uint32_t s_bar = s_out + out_bytes(kTok);
+  const uint32_t s_bar = s_s + (uint32_t)stages * scales_of(kTok);
   const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes landed
   const uint32_t bar_scale = bar_full + 8u * kMxStages;     // [kMxStages] leader: both CTAs' scales are there
   const uint32_t bar_copied = bar_scale + 8u * kMxStages;   // [kMxStages] leader: and in tensor memory
   const uint32_t bar_free = bar_copied + 8u * kMxStages;    // [kMxStages] the MMAs have read all of it
   const uint32_t bar_acc = bar_free + 8u * kMxStages;       // a tile's accumulator is complete
   const uint32_t bar_read = bar_acc + 8u;                   // leader: both CTAs' output warps have read it
-  const uint32_t bar_turn = bar_read + 8u;                  // [kScaleWarps] the batch before the warp's next is stored
-  const uint32_t slot_tmem = bar_turn + 8u * kScaleWarps, slot_abort = slot_tmem + 4u;
+  const uint32_t slot_tmem = bar_read + 8u, slot_abort = slot_tmem + 4u;
 
   const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
   // cluster rank 2 r + half: CTA `half` of the pair that takes K slice r
@@ -380,7 +348,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
     dev::mbar_init(bar_acc, 1u);
     dev::mbar_init(bar_read, 2u * kOutWarps);
-    for (int i = 0; i < kScaleWarps; ++i) dev::mbar_init(bar_turn + 8u * i, 1u);
     dev::st_shared_u32(slot_abort, 0u);
     dev::fence_barrier_init();
   } else if (warp == 2) {
@@ -397,10 +364,19 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   // The next kernel may come once this CTA holds its tensor memory.
   dev::griddep_launch_dependents();
   const MxTile tile_first = MxTile::at<kTok>(p, tile0, rank, half);
-  // While the work ahead in the stream completes, the ring's first weight tiles come
-  // to L2 (which is where a kernel's writes would change them: nothing is read early).
+  // While the work ahead in the stream completes, the ring's first weight tiles and
+  // the first of their scales come to L2 (which is where a kernel's writes would change them: nothing is read early).
   if (warp == 0 && lane < min(stages, tile_first.k_tiles)) {
     dev::tma_prefetch_3d(&a_map, (tile_first.kt0 + lane) * (kTileK / 2), tile_first.n0, tile_first.l);
+  }
+  if (warp == kScale0) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int n = tile_first.n0 + lane + 32 * g;
+      if (n < p.N) {
+        prefetch_line(p.a_scale + ((long long)tile_first.l * p.N + n) * (p.K / kMxBlock) + tile_first.kt0 * (kTileK / kMxBlock));
+      }
+    }
   }
   dev::griddep_wait();
   const uint32_t tmem = dev::ld_shared_u32(slot_tmem);
@@ -442,7 +418,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         ok = turn == 0u || waiter.wait<true>(bar_read, (turn - 1u) & 1u, kRoleMmaAccFree, (int)turn);
         for (int kt = 0; ok && kt < t.k_tiles; ++kt, pos.advance(1, stages)) {
           const uint32_t s = (uint32_t)pos.index;
-          if (!waiter.wait<true>(bar_full + 8u * s, pos.phase, kRoleMma, kt) ||
+          if (!waiter.wait<false>(bar_full + 8u * s, pos.phase, kRoleMma, kt) ||
               !waiter.wait<false>(bar_copied + 8u * s, pos.phase, kRoleMma, kt)) {
             ok = false;
             break;
@@ -489,20 +465,20 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kScale0 && warp < kOut0) {
-    const ScaleRing ring{s_s, dev::mapa(bar_scale, leader), bar_free, bar_turn, stages, waiter};
-    int batch = 0, used = 0;
+    const ScaleRing ring{s_s, dev::mapa(bar_scale, leader), bar_free, stages, waiter};
+    RingPos pos{0, 0u};
+    int used = 0;
     bool ok = true;
     for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
       const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
-      // (each K tile is 8 bytes of a row)
-      const int align = p.align >= 16 && t.kt0 % 2 != 0 ? 8 : p.align, own = warp - kScale0;
+      // (each K tile is 8 bytes of a row, and a pair of slots starts with an even one)
+      const int align = p.align >= 16 && (t.kt0 | used) % 2 != 0 ? 8 : p.align, own = warp - kScale0;
       switch (align) {
-        case 16: ok = bring_scales<kTok, 16>(p, ring, t, batch, used, own, lane); break;
-        case 8: ok = bring_scales<kTok, 8>(p, ring, t, batch, used, own, lane); break;
-        case 4: ok = bring_scales<kTok, 4>(p, ring, t, batch, used, own, lane); break;
-        default: ok = bring_scales<kTok, 1>(p, ring, t, batch, used, own, lane); break;
+        case 16: ok = bring_scales<kTok, 16>(p, ring, t, used, pos, own, lane); break;
+        case 8: ok = bring_scales<kTok, 8>(p, ring, t, used, pos, own, lane); break;
+        case 4: ok = bring_scales<kTok, 4>(p, ring, t, used, pos, own, lane); break;
+        default: ok = bring_scales<kTok, 1>(p, ring, t, used, pos, own, lane); break;
       }
-      batch += (t.k_tiles + batch_of(kTok) - 1) / batch_of(kTok);
       used += t.k_tiles;
     }
   } else if (warp >= kOut0) {
@@ -510,70 +486,73 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int quad = warp - kOut0, row = quad * 32 + lane;
     const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t read_of_leader = dev::mapa(bar_read, leader);
-    const uint32_t s_mine = s_out + (uint32_t)quad * (out_bytes(kTok) / kOutWarps);
-    uint32_t turn = 0u, chunk = 0u;
+    uint32_t turn = 0u;
     for (int tile = tile0; tile < p.tile_end; tile += step, ++turn) {
       const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
       const int n = t.n0 + row, live = min(kTok, p.M - t.m0);
       const float bias = p.bias && n < p.N ? __uint_as_float((uint32_t)p.bias[(long long)t.l * p.N + n] << 16) : 0.0f;
       if (!__all_sync(0xFFFFFFFFu, waiter.wait<false>(bar_acc, turn & 1u, kRoleEpiMma, (int)turn))) break;
       dev::tc_fence_after();
-      if (out_boxes(kTok) && p.c_boxes && split == 1) {
-        const int n_box = t.n0 + quad * 32;
-        for (int g = 0; g * kOutTokens < live; ++g, ++chunk) {
-          uint32_t v[2][16];
-          dev::tmem_ld_x16(t_row + (uint32_t)(g * kOutTokens), v[0]);
-          dev::tmem_ld_x16(t_row + (uint32_t)(g * kOutTokens) + 16u, v[1]);
-          if (lane == 0) tma_store_wait_read<1>();           // the chunk before the last has left its place
-          dev::tmem_wait_ld();
+      const auto read = [&] {                                // the accumulator may be written again
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive_remote_relaxed(read_of_leader);
+      };
+      const int size = p.c_f32 ? 4 : 2;
+      uint8_t* to = static_cast<uint8_t*>(p.c) + (((long long)t.l * p.M + t.m0) * p.N + n) * size;
+      const long long pitch = (long long)p.N * size;
+      if (split > 1) {
+        for (int g = 0; g < live; g += 16) {
+          uint32_t v[16];
           __syncwarp();
-          const uint32_t to = s_mine + (chunk & 1u) * (kOutTokens * 32u * 4u);
-          if (p.c_f32) {
+          load_acc16(t_row + (uint32_t)g, 0u, false, v);
 #pragma unroll
-            for (int e = 0; e < kOutTokens; ++e) dev::st_shared_f32(to + 128u * e + 4u * lane, __uint_as_float(v[e / 16][e % 16]) + bias);
-          } else {
+          for (int e = 0; e < 16; ++e) dev::st_shared_u32(base + (uint32_t)((g + e) * kMmaM + row) * 4u, v[e]);
+        }
+        read();
+      } else if (p.c_f32) {
+        constexpr int kPart = kTok < 64 ? kTok : 64;
+#pragma unroll 1
+        for (int h = 0; h < kTok; h += kPart) {
+          uint32_t v[kPart / 16][16];
 #pragma unroll
-            for (int e = 0; e < kOutTokens; ++e) {
-              st_shared_u16(to + 64u * e + 2u * lane, dev::pack_bf16x2(__uint_as_float(v[e / 16][e % 16]) + bias, 0.0f));
+          for (int g = 0; g < kPart / 16; ++g) dev::tmem_ld_x16(t_row + (uint32_t)(h + 16 * g), v[g]);
+          dev::tmem_wait_ld();
+          if (h + kPart == kTok) read();
+          if (n < p.N) {
+            store_tokens<kPart>(to + h * pitch, pitch, live - h, [&](uint8_t* at, int e) {
+              *reinterpret_cast<float*>(at) = __uint_as_float(v[e / 16][e % 16]) + bias;
+            });
+          }
+          __syncwarp();
+        }
+      } else {
+        // up to half of it before any store, two tokens a register, so that the next
+        // tile's MMAs may start (16 tokens at a time held them up for 4.4 us)
+        constexpr int kPart = kTok < 128 ? kTok : 128;
+#pragma unroll 1
+        for (int h = 0; h < kTok; h += kPart) {
+          uint32_t v[kPart / 2];
+#pragma unroll
+          for (int g = 0; g < kPart / 16; ++g) {
+            uint32_t f[16];
+            dev::tmem_ld_x16(t_row + (uint32_t)(h + 16 * g), f);
+            dev::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[8 * g + e] = dev::pack_bf16x2(__uint_as_float(f[2 * e]) + bias, __uint_as_float(f[2 * e + 1]) + bias);
             }
           }
-          dev::fence_proxy_async_shared();
-          dev::tc_fence_before();
+          if (h + kPart == kTok) read();
+          if (n < p.N) {
+            store_tokens<kPart>(to + h * pitch, pitch, live - h, [&](uint8_t* at, int e) {
+              *reinterpret_cast<uint16_t*>(at) = (uint16_t)(e % 2 == 0 ? v[e / 2] & 0xFFFFu : v[e / 2] >> 16);
+            });
+          }
           __syncwarp();
-          if (lane == 0) {
-            if ((g + 1) * kOutTokens >= live) dev::mbar_arrive_remote_relaxed(read_of_leader);    // all of it is read
-            if (n_box < p.N) tma_store_3d(&c_map, to, n_box, t.m0 + g * kOutTokens, t.l);
-          }
-        }
-        continue;
-      }
-      for (int g = 0; g * 16 < live; ++g) {
-        uint32_t v[16];
-        __syncwarp();
-        load_acc16(t_row + 16u * g, 0u, false, v);
-        if ((g + 1) * 16 >= live) {                          // the accumulator may be written again
-          dev::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) dev::mbar_arrive_remote_relaxed(read_of_leader);
-        }
-        const int cols = min(16, live - g * 16);
-        if (split > 1) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (e < cols) dev::st_shared_u32(base + (uint32_t)((g * 16 + e) * kMmaM + row) * 4u, v[e]);
-          }
-        } else if (n < p.N) {
-          const int size = p.c_f32 ? 4 : 2;
-          uint8_t* to = static_cast<uint8_t*>(p.c) + (((long long)t.l * p.M + t.m0 + g * 16) * p.N + n) * size;
-          if (p.c_f32) {
-            store_tokens<true>(to, (long long)p.N * 4, v, bias, cols);
-          } else {
-            store_tokens<false>(to, (long long)p.N * 2, v, bias, cols);
-          }
         }
       }
     }
-    if (lane == 0 && chunk > 0u) tma_store_wait();
   }
   __syncwarp();
 
@@ -644,15 +623,17 @@ constexpr int kTokens[] = {16, 32, 64, 128, 256};
 // that fit one SM by shared memory, of whatever kernels, never wait for each
 // other's columns.
 size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& dev) {
-  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + out_bytes(tok) + kMxBarBytes;
+  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + kMxBarBytes;
   const size_t sums = split > 1 ? (size_t)kAlignSlack + (size_t)tok * kMmaM * 4 : 0;
   return std::max(std::max(ring, sums), std::min(dev.smem_per_sm * cols / 512, dev.smem_optin));
 }
 
-// The ring for CTAs of `k_tiles` K tiles (of all their tiles).
+// The ring for CTAs of `k_tiles` K tiles (of all their tiles).  (Rings of 4, 5 or 6 are
+// as fast for 256 tokens.)
 MxRing ring_of(int tokens, int split, long long k_tiles, const DeviceSize& dev) {
   const int most = tokens <= 64 ? 6 : kMxStages;
   for (int stages = (int)std::min<long long>(k_tiles, most); stages > 1; --stages) {
+    if (stages % 2 != 0 && stages < k_tiles) continue;  // one that goes round is even
     const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)stages * scale_cols(tokens));
     const size_t smem = mx_smem(tokens, stages, split, cols, dev);
     if (cols <= 512u && smem <= dev.smem_optin) return MxRing{stages, cols, smem};
@@ -758,20 +739,19 @@ inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 
 template <int kTok>
 cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, const MxPlan& plan, const DeviceSize& dev,
                        const MxDevice& d, cudaStream_t stream) {
-  CUtensorMap a_map, b_map, c_map = {};
+  CUtensorMap a_map, b_map;
   if (!encode_codes(&a_map, a, p.K / 2, p.N, p.L, kMmaM) || !encode_codes(&b_map, b, p.K / 2, p.M, p.L, kTok / 2)) {
     return cudaErrorInvalidValue;
   }
-  const bool boxes = out_boxes(kTok) && encode_output(&c_map, p.c, p.c_f32, p.N, p.M, p.L, 32, kOutTokens);
   const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + 2 * kMmaM - 1) / (2 * kMmaM)) * p.L;
   const int total = (p.K + kTileK - 1) / kTileK;
   const auto launch = [&](int first, long long end, int split, long long clusters) {
     const MxRing ring = ring_of(kTok, split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
     MxParams q = p;
     q.split = split, q.stages = ring.stages, q.tmem_cols = ring.tmem_cols;
-    q.tile0 = first, q.tile_end = (int)end, q.c_boxes = boxes;
+    q.tile0 = first, q.tile_end = (int)end;
     return launch_chained(mx4_kernel<kTok>, dim3((unsigned)(clusters * 2 * split)), dim3(kMxThreads), ring.smem,
-                          (unsigned)(2 * split), stream, a_map, b_map, c_map, q);
+                          (unsigned)(2 * split), stream, a_map, b_map, q);
   };
   if (plan.whole > 0) {
     const cudaError_t e = launch(0, plan.whole, 1, std::min(plan.whole, d.clusters[0]));
@@ -818,7 +798,7 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
                     : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4)   ? 4
                                                                                       : 1;
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
-                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, false, align,
+                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, align,
                    wait_limit_ns(), injected()};
   const uint8_t *a = static_cast<const uint8_t*>(a_q), *b = static_cast<const uint8_t*>(b_q);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
