@@ -6,17 +6,18 @@
 // CTA's tensor memory) and kTok tokens (its N side, half of them in each CTA's
 // shared memory).  TMA brings codes, 256 of K wide, from both operands into a ring of
 // shared memory (K-major, 128-byte swizzle); a tile's copies of both CTAs report to
-// the leader.  Scale warps bring the tiles' scales into shared memory in the order
-// that a copy into tensor memory wants: for 128 rows and four blocks of K, 512 bytes,
-// row r's four codes at 16 (r % 32) + 4 (r / 32).  In the leader one thread copies
-// them (tcgen05.cp, to all four lane quadrants of both CTAs) into columns of the
-// tile's own, another issues the tile's four MMAs of K = 64 for both.
+// the leader, where one warp issues the tile's four MMAs of K = 64 for both.
 //
-// Why pairs and two issuing threads: a tcgen05 instruction takes its thread ~46
-// clocks to issue whatever its size, and a tile of few tokens is four copies and four
-// MMAs (with one thread and one CTA a tile, 0.44 us; the copies' share was 0.1, the
-// MMAs' 0.09).  For many tokens a CTA alone would bring 48 KiB a tile for 256 tokens,
-// which takes 0.45 us from L2; a pair brings 32 for each.
+// The MMA reads scales from tensor memory: for 128 rows and four blocks of K, column g
+// of four holds in lane l, of each lane quadrant, the four codes of row 32 g + l.  Four
+// scale warps, a quadrant each, load rows' codes for a K tile each, exchange them
+// through shared memory and store all four tiles' into their quadrants.  (Copies by
+// tcgen05.cp keep the tensor pipe from MMAs for ~38 clocks each: six a tile of 256
+// tokens, 742 clocks with its MMAs instead of 512.)
+//
+// What bounds it: few tokens, the weights' arrival; many, the MMAs, whose K = 64 at 256
+// tokens takes a pair 128 clocks (9.6 PFLOP/s at 1.93 GHz; ~72 for up to 128 tokens).
+// A pair brings 32 KiB a tile of 256 tokens for each CTA, a CTA alone would bring 48.
 //
 // `split` pairs of a cluster may share one output tile, each taking a contiguous run
 // of K tiles; each CTA leaves its f32 sums in its own shared memory and then adds
@@ -38,16 +39,20 @@ namespace splitk {
 
 namespace {
 
-// Warps: 0 copies of codes, 1 MMAs, 2 copies of scales into tensor memory, 3 set-up,
-// then those that bring scales and those that store the output.
+// Warps: 0 copies of codes, 1 MMAs, 2 and 3 set-up, then those that bring scales and
+// those that store the output.
 // (Four more output warps would leave 128 registers a thread, and what is spilled then
 // takes the issuing thread twice its time.)
 constexpr int kScale0 = 4, kScaleWarps = 4, kOut0 = kScale0 + kScaleWarps, kOutWarps = 4;
 constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
 constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
-constexpr int kMxStages = 10;                        // at most
+constexpr int kMxStages = 8;                         // of the ring, at most
+// K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks, which
+// the MMAs of two tiles of 256 tokens cover (1024) and those of one do not.
+__host__ __device__ constexpr int sub_of(int tok) { return tok >= 128 ? 2 : 1; }
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
+constexpr int kGroup = kScaleWarps;                  // K tiles whose scales the scale warps exchange at once
 constexpr uint32_t kMxBarBytes = 512;
 constexpr int kMaxSplit = 4;                         // pairs of a cluster
 constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
@@ -56,9 +61,9 @@ constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
 __host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok / 2 * (kTileK / 2); }
 __host__ __device__ constexpr int groups_b(int tok) { return (tok + 127) / 128; }     // of 128 tokens
 __host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAtom * (1u + groups_b(tok)); }
-__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kCodesA + codes_b(tok) + scales_of(tok); }
+__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return sub_of(tok) * (kCodesA + codes_b(tok)); }
 __host__ __device__ constexpr uint32_t mx_acc_cols(int tok) { return tok < 32 ? 32u : (uint32_t)tok; }
-__host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a stage
+__host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a K tile
 
 // kind::mxf4: E2M1 operands, both K-major, E8M0 scales for each 32, f32 accumulator;
 // the scales of a K = 64 step are the lower (id 0) or upper (id 2) half of a word.
@@ -66,33 +71,32 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27) | (id << 29);
 }
 
+// The tensor cores' instructions of the one lane of a converged warp whose `leader` is 1:
+// operands that all lanes hold alike stay in uniform registers (with a branch to one
+// lane an MMA took it ~100 clocks to issue).
+
 // D[tmem] (+)= A B^T over the pair of CTAs.
 __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
-                                         uint32_t b_scale, uint32_t accumulate) {
+                                         uint32_t b_scale, uint32_t accumulate, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate), "r"(leader)
       : "memory");
 }
 
-// 32 rows of 16 bytes (unswizzled) of each CTA into four columns of its lane quadrants.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
-}
-
-// The arrival of what this thread has issued so far: on its CTA's barrier, or on the
-// same one of all CTAs of a mask.
-__device__ __forceinline__ void commit_here(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t cta_mask) {
+// The arrival of what it has issued so far on the same barrier of all CTAs of a mask.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t cta_mask, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .b16 m;\n\t"
+      "{\n\t.reg .pred q;\n\t"
+      ".reg .b16 m;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
       "cvt.u16.u32 m, %1;\n\t"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
-      "r"(cta_mask)
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          bar),
+      "r"(cta_mask), "r"(leader)
       : "memory");
 }
 
@@ -106,6 +110,13 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int
       : "memory");
 }
 
+// Eight consecutive TMEM columns of this thread's lane from registers.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // A line of global memory to L2.
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
@@ -115,16 +126,6 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncol
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// Shared-memory descriptor of such rows: no swizzle, eight rows (128 bytes) apart.
-__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(16u >> 4) << 16;
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
 }
 
 struct MxParams {
@@ -137,44 +138,36 @@ struct MxParams {
   int split, stages;
   int tile0, tile_end;      // the launch's tiles
   uint32_t tmem_cols;
-  int align;                // of the scales' rows: 16, 8, 4 or 1 bytes
+  int align;                // of the scales' rows: 8, 4 or 1 bytes
   unsigned long long limit_ns;
   unsigned inject;
 };
 
-// K tiles of a batch of scales: 16 bytes of a row.
-constexpr int kBatch = 2;
-
-// The scale codes of a batch of K tiles: two words of four for each row and tile.
+// The scale codes of one row and K tile: two words of four.
 struct ScaleRow {
-  uint32_t w[2 * kBatch];
+  uint32_t w[2];
   // Codes [at, limit) of the row at `row`, 127 past the limit (its codes there are
-  // zeros).  kAlign: what the addresses row + at are multiples of.  Words at odd
+  // zeros, or the row is none).  kAlign: what the addresses row + at are multiples of.  Words at odd
   // addresses come from the two aligned ones around them, where all their bytes are
   // within the array [first, end).
   template <int kAlign>
   __device__ __forceinline__ void load(const uint8_t* row, int at, int limit, const uint8_t* first, const uint8_t* end) {
     constexpr uint32_t kOnes = 0x7F7F7F7Fu;
 #pragma unroll
-    for (int i = 0; i < 2 * kBatch; ++i) w[i] = kOnes;
-    if constexpr (kAlign >= 4) {
-      constexpr int kWords = kAlign / 4;
+    for (int i = 0; i < 2; ++i) w[i] = kOnes;
+    if constexpr (kAlign == 8) {
+      if (at < limit) {                                // (the limit is a multiple of 8)
+        const uint2 v = *reinterpret_cast<const uint2*>(row + at);
+        w[0] = v.x, w[1] = v.y;
+      }
+    } else if constexpr (kAlign == 4) {
 #pragma unroll
-      for (int i = 0; i < 2 * kBatch; i += kWords) {
-        if (at + 4 * i >= limit) continue;             // (the limit is a multiple of kAlign, or ends the row)
-        if constexpr (kWords == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(row + at + 4 * i);
-          w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-        } else if constexpr (kWords == 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(row + at + 4 * i);
-          w[i] = v.x, w[i + 1] = v.y;
-        } else {
-          w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
-        }
+      for (int i = 0; i < 2; ++i) {
+        if (at + 4 * i < limit) w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2 * kBatch; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int n = limit - (at + 4 * i);
         if (n <= 0) continue;
         const uint8_t* p = row + at + 4 * i;
@@ -221,96 +214,120 @@ __device__ __forceinline__ void store_tokens(uint8_t* to, long long pitch, int c
   }
 }
 
-// One output tile of a pair: its place and K tiles.
+// One output tile of a pair: its place and its run of K in stages' shares.
 struct MxTile {
-  int m0, n0, l, k_tiles, kt0;
+  int m0, n0, l, steps, step0;
   template <int kTok>
   __device__ __forceinline__ static MxTile at(const MxParams& p, int tile, int rank, int half) {
     const int m_tiles = (p.M + kTok - 1) / kTok, n_tiles = (p.N + 2 * kMmaM - 1) / (2 * kMmaM);
-    const int total = (p.K + kTileK - 1) / kTileK, each = total / p.split, extra = total % p.split;
+    constexpr int kStepK = kTileK * sub_of(kTok);
+    const int total = (p.K + kStepK - 1) / kStepK, each = total / p.split, extra = total % p.split;
     MxTile t;
     t.m0 = (tile % m_tiles) * kTok;
     t.n0 = (2 * (tile / m_tiles % n_tiles) + half) * kMmaM;
     t.l = tile / m_tiles / n_tiles;
-    t.k_tiles = each + (rank < extra ? 1 : 0);
-    t.kt0 = rank * each + (rank < extra ? rank : extra);
+    t.steps = each + (rank < extra ? 1 : 0);
+    t.step0 = rank * each + (rank < extra ? rank : extra);
     return t;
   }
 };
 
 // What the scale warps work with.
 struct ScaleRing {
-  uint32_t slots, bar_scale_of_leader, bar_free;
+  uint32_t exchange;        // two buffers of kGroup tiles in shared memory
+  uint32_t tmem;            // the first stage's columns, of the warp's lane quadrant
+  uint32_t bar_full_of_leader, bar_done;
   int stages;
   Waiter waiter;
 };
 
-// One scale warp's part of a tile whose first K tile is the CTA's `used`-th, at ring
-// position `pos` (carried on over all of them).  Pairs of slots belong to the warps in
-// turn (a ring that goes round has an even number), so that a warp meets every phase
-// of its slots' barriers, and warps do not wait for one another: passing a turn bounded
-// tiles of 256 tokens at 0.4 us each.  A lane has rows lane + 32 g of each group of
-// 128: for each word of K their four codes lie side by side in shared memory, one
-// 16-byte store.  The loads of a pair of K tiles are under way while its slots become
-// free and while other warps store theirs.
+// One scale warp: the CTA's K tiles, of all its output tiles, in groups of kGroup.  The
+// loads of its tile of the next group are under way while it stores this one's.  Two
+// buffers let one barrier of the warps a group do.
 template <int kTok, int kAlign>
-__device__ __forceinline__ bool bring_scales(const MxParams& p, const ScaleRing& r, const MxTile& t, int used, RingPos& pos,
+__device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing& r, int tile0, int step, int rank, int half,
                                              int warp, int lane) {
   constexpr int kGroups = groups_b(kTok), kLive = kTok >= 128 ? 4 : (kTok + 31) / 32;     // 32s of tokens in a group
-  const int blocks = p.K / kMxBlock, limit = min(blocks, (t.kt0 + t.k_tiles) * (kTileK / kMxBlock));
+  constexpr int kSub = sub_of(kTok);
+  const int blocks = p.K / kMxBlock;
   const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
-  for (int first = 0; first < t.k_tiles;) {
-    const int here = pos.index % 2 == 0 && first + 1 < t.k_tiles ? 2 : 1;           // K tiles up to the pair's end
-    if (pos.index / 2 % kScaleWarps != warp) {
-      for (int i = 0; i < here; ++i) pos.advance(1, r.stages);
-      first += here;
-      continue;
+  MxTile t = MxTile::at<kTok>(p, tile0, rank, half);
+  int tile = tile0, kt = warp;                          // where its next tile is
+  ScaleRow a[4], b[kGroups][kLive];
+  const auto load = [&] {
+    while (kt >= t.steps * kSub && tile < p.tile_end) {
+      kt -= t.steps * kSub, tile += step;
+      if (tile < p.tile_end) t = MxTile::at<kTok>(p, tile, rank, half);
     }
-    const int at = (t.kt0 + first) * (kTileK / kMxBlock);
-    ScaleRow a[4], b[kGroups][kLive];
+    if (tile >= p.tile_end) return;
+    const int at = (t.step0 * kSub + kt) * (kTileK / kMxBlock);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int n = t.n0 + lane + 32 * g;
-      a[g].template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? limit : 0, p.a_scale, a_end);
+      a[g].template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? blocks : 0, p.a_scale, a_end);
     }
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
 #pragma unroll
       for (int g = 0; g < kLive; ++g) {
         const int o = 128 * q + lane + 32 * g, m = t.m0 + o;
-        b[q][g].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? limit : 0,
+        b[q][g].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? blocks : 0,
                                       p.b_scale, b_end);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (i >= here) break;
-      const uint32_t s = (uint32_t)pos.index;
-      if (used + first + i >= r.stages &&
-          !__all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_free + 8u * s, pos.phase ^ 1u, kRoleEpiDecode, first + i))) return false;
-      const uint32_t dst = r.slots + s * scales_of(kTok) + 16u * lane;
+    kt += kGroup;
+  };
+  const int all = t.steps * kSub * ((p.tile_end - tile0 + step - 1) / step);
+  load();
+  RingPos pos{0, 0u};
+  uint32_t buffer = 0u;
+  bool ok = true;                                       // a warp whose wait failed still meets the others' barriers
+  for (int first = 0; first < all; first += kGroup, buffer ^= 1u) {
+    const uint32_t group = r.exchange + buffer * (kGroup * scales_of(kTok)) + 16u * lane;
+    if (first + warp < all) {
+      const uint32_t dst = group + (uint32_t)warp * scales_of(kTok);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const int j = 2 * i + w;
-        dev::st_shared_v4(dst + w * kScaleAtom, a[0].w[j], a[1].w[j], a[2].w[j], a[3].w[j]);
+        dev::st_shared_v4(dst + w * kScaleAtom, a[0].w[w], a[1].w[w], a[2].w[w], a[3].w[w]);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-          dev::st_shared_v4(dst + (2u + w * kGroups + q) * kScaleAtom, b[q][0].w[j], kLive > 1 ? b[q][1 % kLive].w[j] : 0u,
-                            kLive > 2 ? b[q][2 % kLive].w[j] : 0u, kLive > 3 ? b[q][3 % kLive].w[j] : 0u);
+          dev::st_shared_v4(dst + (2u + w * kGroups + q) * kScaleAtom, b[q][0].w[w], kLive > 1 ? b[q][1 % kLive].w[w] : 0u,
+                            kLive > 2 ? b[q][2 % kLive].w[w] : 0u, kLive > 3 ? b[q][3 % kLive].w[w] : 0u);
         }
       }
-      dev::fence_proxy_async_shared();
-      __syncwarp();
-      // (released at cluster scope, where the leader's copying thread acquires it)
-      if (lane == 0 && (p.inject & kInjectSkipPublish) == 0) {
-        dev::fence_release_shared_cluster();
-        dev::mbar_arrive_remote_relaxed(r.bar_scale_of_leader + 8u * s);
-      }
-      pos.advance(1, r.stages);
     }
-    first += here;
+    load();
+    dev::named_bar_sync(1, 32 * kScaleWarps);
+#pragma unroll 1
+    for (int i = 0; ok && i < kGroup && first + i < all; ++i) {
+      uint32_t v[16], u[8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        dev::ld_shared_v4(group + (uint32_t)i * scales_of(kTok) + c * kScaleAtom, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      }
+      if (kGroups > 1) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          dev::ld_shared_v4(group + (uint32_t)i * scales_of(kTok) + (4 + c) * kScaleAtom, u[4 * c], u[4 * c + 1], u[4 * c + 2],
+                            u[4 * c + 3]);
+        }
+      }
+      const int sub = kSub == 1 ? 0 : i % kSub;          // (groups are whole stages)
+      if (sub == 0 && first + i >= r.stages * kSub) {     // the stage's MMAs before
+        ok = __all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_done + 8u * pos.index, pos.phase ^ 1u, kRoleEpiDecode, first + i));
+        if (!ok) break;
+      }
+      dev::tc_fence_after();
+      const uint32_t to = r.tmem + (uint32_t)(pos.index * kSub + sub) * scale_cols(kTok);
+      dev::tmem_st_x16(to, v);
+      if (kGroups > 1) tmem_st_x8(to + 16u, u);
+      dev::tmem_wait_st();
+      dev::tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && (p.inject & kInjectSkipPublish) == 0) dev::mbar_arrive_remote_relaxed(r.bar_full_of_leader + 8u * pos.index);
+      if (sub + 1 == kSub) pos.advance(1, r.stages);
+    }
   }
-  return true;
 }
 
 // A cluster takes tiles gridDim.x / cluster size apart; with split > 1 one alone
@@ -320,16 +337,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const MxParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (dev::smem_u32(smem_raw) + (kAlignSlack - 1)) & ~(kAlignSlack - 1);
+  constexpr int kSub = sub_of(kTok);
   const int stages = p.stages, split = p.split;
   const uint32_t s_a = base;
-  const uint32_t s_b = s_a + (uint32_t)stages * kCodesA;
-  const uint32_t s_s = s_b + (uint32_t)stages * codes_b(kTok);
-  const uint32_t s_bar = s_s + (uint32_t)stages * scales_of(kTok);
-  const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes landed
-  const uint32_t bar_scale = bar_full + 8u * kMxStages;     // [kMxStages] leader: both CTAs' scales are there
-  const uint32_t bar_copied = bar_scale + 8u * kMxStages;   // [kMxStages] leader: and in tensor memory
-  const uint32_t bar_free = bar_copied + 8u * kMxStages;    // [kMxStages] the MMAs have read all of it
-  const uint32_t bar_acc = bar_free + 8u * kMxStages;       // a tile's accumulator is complete
+  const uint32_t s_b = s_a + (uint32_t)stages * kSub * kCodesA;
+  const uint32_t s_s = s_b + (uint32_t)stages * kSub * codes_b(kTok);
+  const uint32_t s_bar = s_s + 2u * kGroup * scales_of(kTok);
+  const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes and scales are there
+  const uint32_t bar_done = bar_full + 8u * kMxStages;      // [kMxStages] the MMAs have read them
+  const uint32_t bar_acc = bar_done + 8u * kMxStages;       // a tile's accumulator is complete
   const uint32_t bar_read = bar_acc + 8u;                   // leader: both CTAs' output warps have read it
   const uint32_t slot_tmem = bar_read + 8u, slot_abort = slot_tmem + 4u;
 
@@ -341,10 +357,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   if (warp == 3 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
-      dev::mbar_init(bar_full + 8u * s, 1u);
-      dev::mbar_init(bar_scale + 8u * s, 2u);
-      dev::mbar_init(bar_copied + 8u * s, 1u);
-      dev::mbar_init(bar_free + 8u * s, 1u);
+      dev::mbar_init(bar_full + 8u * s, 1u + 2u * kScaleWarps * kSub);
+      dev::mbar_init(bar_done + 8u * s, 1u);
     }
     dev::mbar_init(bar_acc, 1u);
     dev::mbar_init(bar_read, 2u * kOutWarps);
@@ -366,15 +380,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const MxTile tile_first = MxTile::at<kTok>(p, tile0, rank, half);
   // While the work ahead in the stream completes, the ring's first weight tiles and
   // the first of their scales come to L2 (which is where a kernel's writes would change them: nothing is read early).
-  if (warp == 0 && lane < min(stages, tile_first.k_tiles)) {
-    dev::tma_prefetch_3d(&a_map, (tile_first.kt0 + lane) * (kTileK / 2), tile_first.n0, tile_first.l);
+  if (warp == 0 && lane < min(stages, tile_first.steps) * kSub) {
+    dev::tma_prefetch_3d(&a_map, (tile_first.step0 * kSub + lane) * (kTileK / 2), tile_first.n0, tile_first.l);
   }
   if (warp == kScale0) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int n = tile_first.n0 + lane + 32 * g;
       if (n < p.N) {
-        prefetch_line(p.a_scale + ((long long)tile_first.l * p.N + n) * (p.K / kMxBlock) + tile_first.kt0 * (kTileK / kMxBlock));
+        prefetch_line(p.a_scale + ((long long)tile_first.l * p.N + n) * (p.K / kMxBlock) +
+                      tile_first.step0 * kSub * (kTileK / kMxBlock));
       }
     }
   }
@@ -391,95 +406,76 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       bool ok = true;
       for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
         const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
-        for (int kt = 0; kt < t.k_tiles; ++kt, pos.advance(1, stages)) {
-          const uint32_t s = (uint32_t)pos.index;
-          if (issued >= stages && !waiter.wait<false>(bar_free + 8u * s, pos.phase ^ 1u, kRoleWeightTma, kt)) {
+        for (int i = 0; i < t.steps; ++i, pos.advance(1, stages)) {
+          const uint32_t s = (uint32_t)pos.index, bar = full_of_leader + 8u * s;
+          if (issued >= stages && !waiter.wait<false>(bar_done + 8u * s, pos.phase ^ 1u, kRoleWeightTma, i)) {
             ok = false;
             break;
           }
-          if (half == 0) dev::mbar_arrive_expect_tx(bar_full + 8u * s, 2u * (kCodesA + codes_b(kTok)));
-          tma_load_pair(s_a + s * kCodesA, &a_map, (t.kt0 + kt) * (kTileK / 2), t.n0, t.l, full_of_leader + 8u * s, policy_a);
-          tma_load_pair(s_b + s * codes_b(kTok), &b_map, (t.kt0 + kt) * (kTileK / 2), t.m0 + half * (kTok / 2), t.l,
-                        full_of_leader + 8u * s, keep);
+          if (half == 0) dev::mbar_arrive_expect_tx(bar_full + 8u * s, 2u * stage_bytes(kTok));
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) {
+            const int k = ((t.step0 + i) * kSub + j) * (kTileK / 2);
+            tma_load_pair(s_a + (s * kSub + j) * kCodesA, &a_map, k, t.n0, t.l, bar, policy_a);
+            tma_load_pair(s_b + (s * kSub + j) * codes_b(kTok), &b_map, k, t.m0 + half * (kTok / 2), t.l, bar, keep);
+          }
           ++issued;
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (half == 0 && lane == 0) {
+    // (the whole warp of the leader CTA walks the tiles)
+    if (half == 0) {
       RingPos pos{0, 0u};
-      const uint32_t both = 3u << (2 * rank);
+      const uint32_t both = 3u << (2 * rank), one = lane == 0 ? 1u : 0u;
       const uint64_t a_desc = dev::smem_desc_sw128(s_a), b_desc = dev::smem_desc_sw128(s_b);
+      const uint32_t acc = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const auto met = [&](bool done) { return __all_sync(0xFFFFFFFFu, done) != 0; };
+      const auto landed = [&](int i) { return met(waiter.wait<true>(bar_full + 8u * pos.index, pos.phase, kRoleMma, i)); };
       uint32_t turn = 0u;
       bool ok = true;
       for (int tile = tile0; ok && tile < p.tile_end; tile += step, ++turn) {
         const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
-        ok = turn == 0u || waiter.wait<true>(bar_read, (turn - 1u) & 1u, kRoleMmaAccFree, (int)turn);
-        for (int kt = 0; ok && kt < t.k_tiles; ++kt, pos.advance(1, stages)) {
-          const uint32_t s = (uint32_t)pos.index;
-          if (!waiter.wait<false>(bar_full + 8u * s, pos.phase, kRoleMma, kt) ||
-              !waiter.wait<false>(bar_copied + 8u * s, pos.phase, kRoleMma, kt)) {
-            ok = false;
-            break;
-          }
+        ok = landed(0) && (turn == 0u || met(waiter.wait<true>(bar_read, (turn - 1u) & 1u, kRoleMmaAccFree, (int)turn)));
+        for (int i = 0; ok && i < t.steps; ++i) {
           dev::tc_fence_after();
-          const uint32_t t_a = tmem + mx_acc_cols(kTok) + s * scale_cols(kTok), t_b = t_a + 8u;
-          const uint64_t a_d = dev::smem_desc_advance(a_desc, s * kCodesA), b_d = dev::smem_desc_advance(b_desc, s * codes_b(kTok));
+          const uint32_t s = (uint32_t)pos.index;
+          const uint32_t t_s = acc + mx_acc_cols(kTok) + s * (kSub * scale_cols(kTok));
+          const uint64_t a_d = dev::smem_desc_advance(a_desc, s * (kSub * kCodesA));
+          const uint64_t b_d = dev::smem_desc_advance(b_desc, s * (kSub * codes_b(kTok)));
+          pos.advance(1, stages);
+          // (64s of K that there are)
+          const int chunks = min(4 * kSub, (p.K - (t.step0 + i) * (kSub * kTileK) + 63) / 64);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_mxf4(tmem, dev::smem_desc_advance(a_d, 32u * j), dev::smem_desc_advance(b_d, 32u * j),
-                     j % 2 == 0 ? idesc_mxf4(2 * kMmaM, kTok, 0u) : idesc_mxf4(2 * kMmaM, kTok, 2u), t_a + 4u * (j / 2),
-                     t_b + 4u * groups_b(kTok) * (j / 2), (kt != 0 || j != 0) ? 1u : 0u);
+          for (int j = 0; j < 4 * kSub; ++j) {
+            const uint32_t sub = j / 4, t_a = t_s + sub * scale_cols(kTok) + 4u * (j % 4 / 2);
+            const uint32_t t_b = t_s + sub * scale_cols(kTok) + 8u + 4u * groups_b(kTok) * (j % 4 / 2);
+            if (j < chunks) {
+              mma_mxf4(acc, dev::smem_desc_advance(a_d, sub * kCodesA + 32u * (j % 4)),
+                       dev::smem_desc_advance(b_d, sub * codes_b(kTok) + 32u * (j % 4)),
+                       j % 2 == 0 ? idesc_mxf4(2 * kMmaM, kTok, 0u) : idesc_mxf4(2 * kMmaM, kTok, 2u), t_a, t_b,
+                       (i != 0 || j != 0) ? 1u : 0u, one);
+            }
+            // the next stage is waited for while these are under way
+            if (j == 4 * kSub - 3 && i + 1 < t.steps) ok = landed(i + 1);
           }
-          commit_pair(bar_free + 8u * s, both);
+          commit_pair(bar_done + 8u * s, both, one);
         }
-        commit_pair(bar_acc, both);
+        commit_pair(bar_acc, both, one);
       }
       // after a failed wait, MMAs in flight land before the pair gives up its memory
       if (!ok) drain_wait(bar_acc, (turn - 1u) & 1u, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    if (half == 0 && lane == 0) {
-      RingPos pos{0, 0u};
-      const uint64_t s_desc = smem_desc_rows16(s_s);
-      bool ok = true;
-      for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
-        const int k_tiles = MxTile::at<kTok>(p, tile, rank, half).k_tiles;
-        for (int kt = 0; kt < k_tiles; ++kt, pos.advance(1, stages)) {
-          const uint32_t s = (uint32_t)pos.index;
-          if (!waiter.wait<true>(bar_scale + 8u * s, pos.phase, kRoleMma, kt)) {
-            ok = false;
-            break;
-          }
-          dev::tc_fence_after();
-          const uint32_t t_a = tmem + mx_acc_cols(kTok) + s * scale_cols(kTok);
-#pragma unroll
-          for (int i = 0; i < 2 * (1 + groups_b(kTok)); ++i) {
-            tmem_cp_scales(t_a + 4u * i, dev::smem_desc_advance(s_desc, s * scales_of(kTok) + kScaleAtom * i));
-          }
-          commit_here(bar_copied + 8u * s);
-        }
-      }
-    }
-    __syncwarp();
   } else if (warp >= kScale0 && warp < kOut0) {
-    const ScaleRing ring{s_s, dev::mapa(bar_scale, leader), bar_free, stages, waiter};
-    RingPos pos{0, 0u};
-    int used = 0;
-    bool ok = true;
-    for (int tile = tile0; ok && tile < p.tile_end; tile += step) {
-      const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
-      // (each K tile is 8 bytes of a row, and a pair of slots starts with an even one)
-      const int align = p.align >= 16 && (t.kt0 | used) % 2 != 0 ? 8 : p.align, own = warp - kScale0;
-      switch (align) {
-        case 16: ok = bring_scales<kTok, 16>(p, ring, t, used, pos, own, lane); break;
-        case 8: ok = bring_scales<kTok, 8>(p, ring, t, used, pos, own, lane); break;
-        case 4: ok = bring_scales<kTok, 4>(p, ring, t, used, pos, own, lane); break;
-        default: ok = bring_scales<kTok, 1>(p, ring, t, used, pos, own, lane); break;
-      }
-      used += t.k_tiles;
+    const int own = warp - kScale0;                         // and its lane quadrant
+    const ScaleRing ring{s_s, tmem + ((uint32_t)(32 * own) << 16) + mx_acc_cols(kTok), dev::mapa(bar_full, leader), bar_done, stages,
+                         waiter};
+    switch (p.align) {
+      case 8: bring_scales<kTok, 8>(p, ring, tile0, step, rank, half, own, lane); break;
+      case 4: bring_scales<kTok, 4>(p, ring, tile0, step, rank, half, own, lane); break;
+      default: bring_scales<kTok, 1>(p, ring, tile0, step, rank, half, own, lane); break;
     }
   } else if (warp >= kOut0) {
     // ---- output: warp kOut0 + w has TMEM lane quadrant w, thread = weight row
@@ -623,23 +619,19 @@ constexpr int kTokens[] = {16, 32, 64, 128, 256};
 // that fit one SM by shared memory, of whatever kernels, never wait for each
 // other's columns.
 size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& dev) {
-  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + kMxBarBytes;
+  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + 2 * kGroup * (size_t)scales_of(tok) + kMxBarBytes;
   const size_t sums = split > 1 ? (size_t)kAlignSlack + (size_t)tok * kMmaM * 4 : 0;
   return std::max(std::max(ring, sums), std::min(dev.smem_per_sm * cols / 512, dev.smem_optin));
 }
 
-// The ring for CTAs of `k_tiles` K tiles (of all their tiles).  (Rings of 4, 5 or 6 are
-// as fast for 256 tokens.)
-MxRing ring_of(int tokens, int split, long long k_tiles, const DeviceSize& dev) {
-  const int most = tokens <= 64 ? 6 : kMxStages;
-  for (int stages = (int)std::min<long long>(k_tiles, most); stages > 1; --stages) {
-    if (stages % 2 != 0 && stages < k_tiles) continue;  // one that goes round is even
-    const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)stages * scale_cols(tokens));
+// The ring for CTAs of `steps` stages' shares of K (of all their tiles).
+MxRing ring_of(int tokens, int split, long long steps, const DeviceSize& dev) {
+  int stages = (int)std::min<long long>(steps, tokens <= 64 ? 6 : kMxStages);
+  for (;; --stages) {
+    const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)(stages * sub_of(tokens)) * scale_cols(tokens));
     const size_t smem = mx_smem(tokens, stages, split, cols, dev);
-    if (cols <= 512u && smem <= dev.smem_optin) return MxRing{stages, cols, smem};
+    if (stages == 1 || (cols <= 512u && smem <= dev.smem_optin)) return MxRing{stages, cols, smem};
   }
-  const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + scale_cols(tokens));
-  return MxRing{1, cols, mx_smem(tokens, 1, split, cols, dev)};
 }
 
 void* kernel_of(int tokens) {
@@ -705,7 +697,7 @@ int prepare_mx4(const DeviceSize& dev, MxDevice* out) {
 double launch_us(long long tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
   const int fit = d.clusters[split - 1];
   if (tiles == 0) return 0.0;
-  if (fit <= 0 || split > k_tiles) return 1e30;
+  if (fit <= 0 || split > (k_tiles + sub_of(tokens) - 1) / sub_of(tokens)) return 1e30;
   const double rounds = (double)((tiles + fit - 1) / fit);
   const double step = tokens == 256 ? 0.43 : tokens == 128 ? 0.38 : 0.36;
   const double each = step * ((k_tiles + split - 1) / split);
@@ -744,7 +736,7 @@ cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, co
     return cudaErrorInvalidValue;
   }
   const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + 2 * kMmaM - 1) / (2 * kMmaM)) * p.L;
-  const int total = (p.K + kTileK - 1) / kTileK;
+  const int total = (p.K + kTileK * sub_of(kTok) - 1) / (kTileK * sub_of(kTok));
   const auto launch = [&](int first, long long end, int split, long long clusters) {
     const MxRing ring = ring_of(kTok, split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
     MxParams q = p;
@@ -793,10 +785,9 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
     return SPLITK_ERR_INVALID_SHAPE;
   }
   const int blocks = K / kMxBlock;
-  const int align = blocks % 16 == 0 && aligned(a_scale, 16) && aligned(b_scale, 16) ? 16
-                    : blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
-                    : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4)   ? 4
-                                                                                      : 1;
+  const int align = blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
+                    : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4) ? 4
+                                                                                    : 1;
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
                    static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, align,
                    wait_limit_ns(), injected()};
