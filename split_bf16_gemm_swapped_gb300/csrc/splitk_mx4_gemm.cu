@@ -10,8 +10,9 @@
 //
 // The MMA reads scales from tensor memory: for 128 rows and four blocks of K, column g
 // of four holds in lane l, of each lane quadrant, the four codes of row 32 g + l.  Four
-// scale warps, a quadrant each, load rows' codes for a K tile each, exchange them
-// through shared memory and store all four tiles' into their quadrants.  (Copies by
+// scale warps, a quadrant each, load 32s of rows, a sector of each (four K tiles: a
+// load costs the L1 cache a look-up a row, however short), exchange them through
+// shared memory and store all of them into their quadrants.  (Copies by
 // tcgen05.cp keep the tensor pipe from MMAs for ~38 clocks each: six a tile of 256
 // tokens, 742 clocks with its MMAs instead of 512.)
 //
@@ -52,7 +53,7 @@ constexpr int kMxStages = 8;                         // of the ring, at most
 __host__ __device__ constexpr int sub_of(int tok) { return tok >= 128 ? 2 : 1; }
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
-constexpr int kGroup = kScaleWarps;                  // K tiles whose scales the scale warps exchange at once
+constexpr int kGroup = 4;                            // K tiles whose scales the scale warps exchange at once
 constexpr uint32_t kMxBarBytes = 512;
 constexpr int kMaxSplit = 4;                         // pairs of a cluster
 constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
@@ -110,13 +111,6 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int
       : "memory");
 }
 
-// Eight consecutive TMEM columns of this thread's lane from registers.
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // A line of global memory to L2.
 __device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 
@@ -138,36 +132,46 @@ struct MxParams {
   int split, stages;
   int tile0, tile_end;      // the launch's tiles
   uint32_t tmem_cols;
-  int align;                // of the scales' rows: 8, 4 or 1 bytes
+  int align;                // of the scales' rows: 32, 8, 4 or 1 bytes
   unsigned long long limit_ns;
   unsigned inject;
 };
 
-// The scale codes of one row and K tile: two words of four.
+// The scale codes of one row and a group of K tiles: two words of four for each.
 struct ScaleRow {
-  uint32_t w[2];
+  uint32_t w[2 * kGroup];
   // Codes [at, limit) of the row at `row`, 127 past the limit (its codes there are
-  // zeros, or the row is none).  kAlign: what the addresses row + at are multiples of.  Words at odd
-  // addresses come from the two aligned ones around them, where all their bytes are
-  // within the array [first, end).
+  // zeros, or the row is none).  kAlign: what the addresses row + at are multiples of
+  // (and the limit, but where it ends the row).  Words at odd addresses come from the
+  // two aligned ones around them, where all their bytes are within the array [first,
+  // end).
   template <int kAlign>
   __device__ __forceinline__ void load(const uint8_t* row, int at, int limit, const uint8_t* first, const uint8_t* end) {
     constexpr uint32_t kOnes = 0x7F7F7F7Fu;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = kOnes;
-    if constexpr (kAlign == 8) {
-      if (at < limit) {                                // (the limit is a multiple of 8)
-        const uint2 v = *reinterpret_cast<const uint2*>(row + at);
-        w[0] = v.x, w[1] = v.y;
+    for (int i = 0; i < 2 * kGroup; ++i) w[i] = kOnes;
+    if constexpr (kAlign == 32) {
+      if (at < limit) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(row + at)
+                     : "memory");
+      }
+    } else if constexpr (kAlign == 8) {
+#pragma unroll
+      for (int i = 0; i < 2 * kGroup; i += 2) {
+        if (at + 4 * i >= limit) continue;
+        const uint2 v = *reinterpret_cast<const uint2*>(row + at + 4 * i);
+        w[i] = v.x, w[i + 1] = v.y;
       }
     } else if constexpr (kAlign == 4) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2 * kGroup; ++i) {
         if (at + 4 * i < limit) w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2 * kGroup; ++i) {
         const int n = limit - (at + 4 * i);
         if (n <= 0) continue;
         const uint8_t* p = row + at + 4 * i;
@@ -241,92 +245,89 @@ struct ScaleRing {
   Waiter waiter;
 };
 
-// One scale warp: the CTA's K tiles, of all its output tiles, in groups of kGroup.  The
-// loads of its tile of the next group are under way while it stores this one's.  Two
-// buffers let one barrier of the warps a group do.
+// One scale warp: the CTA's K tiles, of one output tile after another, in groups of
+// kGroup.  Its rows' loads of the next group are under way while it stores this one's.
+// Two buffers let one barrier of the warps a group do.
 template <int kTok, int kAlign>
 __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing& r, int tile0, int step, int rank, int half,
                                              int warp, int lane) {
-  constexpr int kGroups = groups_b(kTok), kLive = kTok >= 128 ? 4 : (kTok + 31) / 32;     // 32s of tokens in a group
-  constexpr int kSub = sub_of(kTok);
+  constexpr int kGroups = groups_b(kTok), kLive = (kTok + 31) / 32;        // 128s and 32s of tokens
+  constexpr int kOwn = (kLive + kScaleWarps - 1) / kScaleWarps;            // of which a warp loads at most
+  constexpr int kSub = sub_of(kTok), kStages = kGroup / kSub;              // whole stages a group
+  constexpr int kVecs = 2 * kSub * (1 + kGroups);                          // 16 bytes of a lane, of a stage
   const int blocks = p.K / kMxBlock;
   const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
   MxTile t = MxTile::at<kTok>(p, tile0, rank, half);
-  int tile = tile0, kt = warp;                          // where its next tile is
-  ScaleRow a[4], b[kGroups][kLive];
+  int tile = tile0, kt = 0;                             // where the group to load starts
+  const int k_tiles = t.steps * kSub, groups = (k_tiles + kGroup - 1) / kGroup * ((p.tile_end - tile0 + step - 1) / step);
+  ScaleRow a, b[kOwn];
   const auto load = [&] {
-    while (kt >= t.steps * kSub && tile < p.tile_end) {
-      kt -= t.steps * kSub, tile += step;
-      if (tile < p.tile_end) t = MxTile::at<kTok>(p, tile, rank, half);
-    }
     if (tile >= p.tile_end) return;
     const int at = (t.step0 * kSub + kt) * (kTileK / kMxBlock);
+    const int n = t.n0 + lane + 32 * warp;
+    a.template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? blocks : 0, p.a_scale, a_end);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int n = t.n0 + lane + 32 * g;
-      a[g].template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? blocks : 0, p.a_scale, a_end);
-    }
-#pragma unroll
-    for (int q = 0; q < kGroups; ++q) {
-#pragma unroll
-      for (int g = 0; g < kLive; ++g) {
-        const int o = 128 * q + lane + 32 * g, m = t.m0 + o;
-        b[q][g].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? blocks : 0,
-                                      p.b_scale, b_end);
-      }
+    for (int q = 0; q < kOwn; ++q) {
+      const int o = 32 * (warp + kScaleWarps * q) + lane, m = t.m0 + o;
+      b[q].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? blocks : 0, p.b_scale,
+                                 b_end);
     }
     kt += kGroup;
+    if (kt >= k_tiles) {
+      kt = 0, tile += step;
+      if (tile < p.tile_end) t = MxTile::at<kTok>(p, tile, rank, half);
+    }
   };
-  const int all = t.steps * kSub * ((p.tile_end - tile0 + step - 1) / step);
   load();
   RingPos pos{0, 0u};
-  uint32_t buffer = 0u;
+  int used = 0, left = k_tiles;                         // stages before; K tiles of the output tile not stored yet
   bool ok = true;                                       // a warp whose wait failed still meets the others' barriers
-  for (int first = 0; first < all; first += kGroup, buffer ^= 1u) {
-    const uint32_t group = r.exchange + buffer * (kGroup * scales_of(kTok)) + 16u * lane;
-    if (first + warp < all) {
-      const uint32_t dst = group + (uint32_t)warp * scales_of(kTok);
+  uint32_t buffer = r.exchange;
+  for (int group = 0; group < groups; ++group) {
+    // word w of a K tile: 512 bytes of A's rows, then of B's each 128
+    const uint32_t mine = buffer + 16u * lane + 4u * warp;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        dev::st_shared_v4(dst + w * kScaleAtom, a[0].w[w], a[1].w[w], a[2].w[w], a[3].w[w]);
+    for (int j = 0; j < 2 * kGroup; ++j) {
+      const uint32_t at = mine + (j / 2) * scales_of(kTok) + (j % 2) * kScaleAtom;
+      dev::st_shared_u32(at, a.w[j]);
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) {
-          dev::st_shared_v4(dst + (2u + w * kGroups + q) * kScaleAtom, b[q][0].w[w], kLive > 1 ? b[q][1 % kLive].w[w] : 0u,
-                            kLive > 2 ? b[q][2 % kLive].w[w] : 0u, kLive > 3 ? b[q][3 % kLive].w[w] : 0u);
+      for (int q = 0; q < kOwn; ++q) {
+        if (kLive >= kScaleWarps || warp < kLive) {
+          dev::st_shared_u32(at + (2u + (j % 2) * (kGroups - 1u) + q) * kScaleAtom, b[q].w[j]);
         }
       }
     }
     load();
     dev::named_bar_sync(1, 32 * kScaleWarps);
 #pragma unroll 1
-    for (int i = 0; ok && i < kGroup && first + i < all; ++i) {
-      uint32_t v[16], u[8];
+    for (int i = 0; ok && i < kStages && i * kSub < left; ++i, ++used) {
+      uint32_t v[kVecs][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        dev::ld_shared_v4(group + (uint32_t)i * scales_of(kTok) + c * kScaleAtom, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      for (int c = 0; c < kVecs; ++c) {
+        dev::ld_shared_v4(buffer + 16u * lane + (uint32_t)i * (kSub * scales_of(kTok)) + c * kScaleAtom, v[c][0], v[c][1], v[c][2],
+                          v[c][3]);
       }
-      if (kGroups > 1) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          dev::ld_shared_v4(group + (uint32_t)i * scales_of(kTok) + (4 + c) * kScaleAtom, u[4 * c], u[4 * c + 1], u[4 * c + 2],
-                            u[4 * c + 3]);
-        }
-      }
-      const int sub = kSub == 1 ? 0 : i % kSub;          // (groups are whole stages)
-      if (sub == 0 && first + i >= r.stages * kSub) {     // the stage's MMAs before
-        ok = __all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_done + 8u * pos.index, pos.phase ^ 1u, kRoleEpiDecode, first + i));
+      if (used >= r.stages) {                           // the stage's MMAs before
+        ok = __all_sync(0xFFFFFFFFu, r.waiter.wait<false>(r.bar_done + 8u * pos.index, pos.phase ^ 1u, kRoleEpiDecode, used));
         if (!ok) break;
       }
       dev::tc_fence_after();
-      const uint32_t to = r.tmem + (uint32_t)(pos.index * kSub + sub) * scale_cols(kTok);
-      dev::tmem_st_x16(to, v);
-      if (kGroups > 1) tmem_st_x8(to + 16u, u);
+      const uint32_t to = r.tmem + (uint32_t)pos.index * (kSub * scale_cols(kTok));
+#pragma unroll
+      for (int c = 0; c < kVecs; c += 4) {
+        uint32_t x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = v[(c + e / 4) % kVecs][e % 4];
+        dev::tmem_st_x16(to + 4u * c, x);
+      }
       dev::tmem_wait_st();
       dev::tc_fence_before();
       __syncwarp();
       if (lane == 0 && (p.inject & kInjectSkipPublish) == 0) dev::mbar_arrive_remote_relaxed(r.bar_full_of_leader + 8u * pos.index);
-      if (sub + 1 == kSub) pos.advance(1, r.stages);
+      pos.advance(1, r.stages);
     }
+    left = left > kGroup ? left - kGroup : k_tiles;
+    buffer = r.exchange + (r.exchange + kGroup * scales_of(kTok) - buffer);
   }
 }
 
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   if (warp == 3 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
-      dev::mbar_init(bar_full + 8u * s, 1u + 2u * kScaleWarps * kSub);
+      dev::mbar_init(bar_full + 8u * s, 1u + 2u * kScaleWarps);
       dev::mbar_init(bar_done + 8u * s, 1u);
     }
     dev::mbar_init(bar_acc, 1u);
@@ -472,7 +473,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int own = warp - kScale0;                         // and its lane quadrant
     const ScaleRing ring{s_s, tmem + ((uint32_t)(32 * own) << 16) + mx_acc_cols(kTok), dev::mapa(bar_full, leader), bar_done, stages,
                          waiter};
-    switch (p.align) {
+    // (a K tile is 8 bytes of a row, a group of them 32)
+    switch (p.align == 32 && tile_first.step0 * kSub % kGroup != 0 ? 8 : p.align) {
+      case 32: bring_scales<kTok, 32>(p, ring, tile0, step, rank, half, own, lane); break;
       case 8: bring_scales<kTok, 8>(p, ring, tile0, step, rank, half, own, lane); break;
       case 4: bring_scales<kTok, 4>(p, ring, tile0, step, rank, half, own, lane); break;
       default: bring_scales<kTok, 1>(p, ring, tile0, step, rank, half, own, lane); break;
@@ -785,7 +788,8 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
     return SPLITK_ERR_INVALID_SHAPE;
   }
   const int blocks = K / kMxBlock;
-  const int align = blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
+  const int align = blocks % 32 == 0 && aligned(a_scale, 32) && aligned(b_scale, 32) ? 32
+                    : blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
                     : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4) ? 4
                                                                                     : 1;
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
