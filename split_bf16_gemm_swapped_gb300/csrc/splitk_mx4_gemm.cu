@@ -628,8 +628,11 @@ size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& 
 }
 
 // The ring for CTAs of `steps` stages' shares of K (of all their tiles).
-MxRing ring_of(int tokens, int split, long long steps, const DeviceSize& dev) {
-  int stages = (int)std::min<long long>(steps, tokens <= 64 ? 6 : kMxStages);
+// For few tokens 8 stages, or 6 where nearly all pairs work (bytes in flight beyond some
+// 16 MB no longer help: 64x7168x16384 on 56 pairs 16.1 us with 6 and 15.6 with 8,
+// 1x7168x2048 on 28 4.9 and 4.8, but 1x18432x7168 on 72 14.3 and 14.8).
+MxRing ring_of(int tokens, int split, long long pairs, long long steps, const DeviceSize& dev) {
+  int stages = (int)std::min<long long>(steps, tokens <= 64 && pairs * 5 > dev.num_sms * 2 ? 6 : kMxStages);
   for (;; --stages) {
     const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)(stages * sub_of(tokens)) * scale_cols(tokens));
     const size_t smem = mx_smem(tokens, stages, split, cols, dev);
@@ -696,15 +699,25 @@ int prepare_mx4(const DeviceSize& dev, MxDevice* out) {
   return SPLITK_OK;
 }
 
-// What a launch of `tiles` tiles costs, in microseconds.
+// What a launch of `tiles` tiles costs, in microseconds: a pair's time for a K tile where
+// nothing but its own work bounds it, no less than the pairs at work take to read theirs
+// (6.2 bytes a picosecond: what these kernels reach on codes and scales from memory),
+// and what comes before, between and after the tiles (for a tile in shares, their sums
+// too: with its tokens). Measured, with the choice it
+// decides (us): 1000x7168x16384 by 128 tokens 49.8, by 256 54.6; 2048x18432x7168
+// 108.5 and 94.3; 2048x7168x2048 17.9 and 16.8; 1x7168x2048 on one pair a tile 4.8, on
+// two 5.3; 16x4096x7168 10.0, 7.6, on three 7.5; 64x7168x16384 20.6 and 15.6;
+// 1x500x16384 18.4, 11.1, 8.8, on four 7.1; 64x18432x7168 14.7 and 21.8 (two rounds).
 double launch_us(long long tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
   const int fit = d.clusters[split - 1];
   if (tiles == 0) return 0.0;
   if (fit <= 0 || split > (k_tiles + sub_of(tokens) - 1) / sub_of(tokens)) return 1e30;
   const double rounds = (double)((tiles + fit - 1) / fit);
-  const double step = tokens == 256 ? 0.43 : tokens == 128 ? 0.38 : 0.36;
+  const double pairs = (double)(std::min<long long>(tiles, fit) * split);
+  const double step = std::max(tokens == 256 ? 0.39 : tokens == 128 ? 0.23 : 0.24,
+                               tokens == 256 ? 0.0 : pairs * (2 * kMmaM * kTileK * 17 / 32) / 6.2e6);
   const double each = step * ((k_tiles + split - 1) / split);
-  return rounds * each + (split > 1 ? rounds * 4.5 : 4.0 + (rounds - 1) * 0.5) + (split > 1 ? 0.3 : 0.0);
+  return rounds * each + (split > 1 ? rounds * (3.0 + 0.02 * (pairs + tokens)) : 3.2 + (rounds - 1) * 0.5);
 }
 
 MxPlan plan_mx4(int M, int N, int K, int L, const MxDevice& d) {
@@ -741,7 +754,7 @@ cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, co
   const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + 2 * kMmaM - 1) / (2 * kMmaM)) * p.L;
   const int total = (p.K + kTileK * sub_of(kTok) - 1) / (kTileK * sub_of(kTok));
   const auto launch = [&](int first, long long end, int split, long long clusters) {
-    const MxRing ring = ring_of(kTok, split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
+    const MxRing ring = ring_of(kTok, split, clusters * split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
     MxParams q = p;
     q.split = split, q.stages = ring.stages, q.tmem_cols = ring.tmem_cols;
     q.tile0 = first, q.tile_end = (int)end;
