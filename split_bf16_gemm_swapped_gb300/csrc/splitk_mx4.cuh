@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t mx_scale_code(float top) {
 }
 
 // What multiplies a value of a block to give its quotient by the scale: exact (a
-// power of two with exponent field 254 - code, 2 .. 253), 0 for a block without
-// codes (whose values are not used).
+// power of two with exponent field 254 - code, 2 .. 253).  For a block without codes
+// the quotients are of no use.
 __device__ __forceinline__ float mx_inverse_scale(uint32_t code) { return __uint_as_float((254u - code) << 23); }
 
 // The scale that a code stands for: 2^(code - 127), subnormal for 0, NaN for 255.

@@ -49,6 +49,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return kKind == kF16 ? pack_f16x2(lo, hi) : dev::pack_bf16x2(lo, hi);
 }
 
+// Both halves' larger ones.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Eight consecutive elements, in 16-byte words or (`vec` false) one by one.
 template <int kKind>
 struct Eight {
@@ -77,6 +84,23 @@ struct Eight {
     for (int j = 0; j < kVec; ++j) {
       v[j] = kKind == kF32 ? __uint_as_float(w[j % kWords]) : half_value<kKind>(j % 2 ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu);
     }
+  }
+  // The largest magnitude of a block (four lanes' vectors), from the bits: without
+  // their signs the values are ordered as whole numbers, NaN above infinity.
+  __device__ __forceinline__ float block_top() const {
+    uint32_t top = 0u;
+    if (kKind == kF32) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) top = max(top, w[i] & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      return __uint_as_float(top);
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) top = max_u16x2(top, w[i] & 0x7FFF7FFFu);
+    top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    return half_value<kKind>(max(top & 0xFFFFu, top >> 16));
   }
   __device__ __forceinline__ void set(const float (&v)[kVec]) {
 #pragma unroll
@@ -108,20 +132,25 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// The codes of a thread's eight values, four lanes to a block: all lanes of the
-// warp call it.  `code` is the block's scale code.
-__device__ __forceinline__ uint32_t block_codes(const float (&n)[kVec], uint32_t& code) {
-  float top = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) top = max_nan(top, fabsf(n[j]));
-  top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-  top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+// The codes of eight values of a block whose largest magnitude is `top`, and its
+// scale code.
+__device__ __forceinline__ uint32_t codes_of(const float (&n)[kVec], float top, uint32_t& code) {
   code = mx_scale_code(top);
   const float inverse = mx_inverse_scale(code);
   float q[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) q[j] = n[j] * inverse;
   return code == kMxNaN ? 0u : dev::e2m1x8(q);
+}
+
+// The same for four lanes to a block: all lanes of the warp call it.
+__device__ __forceinline__ uint32_t block_codes(const float (&n)[kVec], uint32_t& code) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) top = max_nan(top, fabsf(n[j]));
+  top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  return codes_of(n, top, code);
 }
 
 // ---------------------------------------------------------------- quantise
@@ -131,7 +160,7 @@ struct QuantizeParams {
   uint8_t* codes;           // [rows][width / 2]
   uint8_t* scale;           // [rows][width / 32]
   long long rows, width;
-  long long chunks;         // of a row, `step` vectors of kEach threads
+  uint32_t chunks;          // of a row, `step` vectors of kEach threads
   bool vec;
 };
 
@@ -143,10 +172,10 @@ template <int kKind>
 __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const QuantizeParams p) {
   dev::griddep_launch_dependents();
   dev::griddep_wait();
-  const long long group = (long long)blockIdx.x / p.chunks, chunk = (long long)blockIdx.x % p.chunks;
-  const long long row = group * blockDim.y + threadIdx.y;
-  const long long first = (chunk * kEach * blockDim.x + threadIdx.x) * kVec;
-  Eight<kKind> e[kEach];
+  const uint32_t group = p.chunks == gridDim.x ? 0u : blockIdx.x / p.chunks, chunk = blockIdx.x - group * p.chunks;
+  const long long row = (long long)group * blockDim.y + threadIdx.y;
+  const long long first = ((long long)chunk * (kEach * blockDim.x) + threadIdx.x) * kVec;
+  Eight<kKind> e[kEach] = {};
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const long long at = first + (long long)i * blockDim.x * kVec;
@@ -156,11 +185,12 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const QuantizePar
   for (int i = 0; i < kEach; ++i) {
     const long long at = first + (long long)i * blockDim.x * kVec;
     const bool in = row < p.rows && at < p.width;      // the same in a block's four lanes
-    float v[kVec] = {};
-    if (in) e[i].values(v);
-    uint32_t code;
-    const uint32_t q = block_codes(v, code);
+    const float top = e[i].block_top();
     if (!in) continue;
+    float v[kVec];
+    e[i].values(v);
+    uint32_t code;
+    const uint32_t q = codes_of(v, top, code);
     const long long to = row * p.width + at;
     *reinterpret_cast<uint32_t*>(p.codes + to / 2) = q;
     if (threadIdx.x % 4 == 0) p.scale[to / kMxBlock] = (uint8_t)code;
@@ -435,7 +465,7 @@ SPLITK_API int splitk_quantize_mx4(const void* x, int x_type, long long x_stride
   int rc = check_shape(M, K);
   if (rc != SPLITK_OK || x_stride < K) return SPLITK_ERR_INVALID_SHAPE;
   if (!aligned(x, type_size(x_type)) || !aligned(codes, 16)) return SPLITK_ERR_MISALIGNED;
-  QuantizeParams p{x, x_stride, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scale), M, K, 1, false};
+  QuantizeParams p{x, x_stride, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scale), M, K, 1u, false};
   p.vec = aligned(x, 16) && x_stride * (long long)type_size(x_type) % 16 == 0;
   if (x_stride == K) p.rows = 1, p.width = (long long)M * K, p.x_stride = p.width;     // one row of all
   // rows of fewer vectors than a CTA's threads share it
@@ -443,9 +473,10 @@ SPLITK_API int splitk_quantize_mx4(const void* x, int x_type, long long x_stride
   unsigned wide = 32;
   while (wide < kRowThreads && (long long)wide * kEach < vecs) wide *= 2;
   const dim3 block(wide, kRowThreads / wide);
-  p.chunks = (vecs + (long long)kEach * wide - 1) / ((long long)kEach * wide);
-  const long long ctas = (p.rows + block.y - 1) / block.y * p.chunks;
+  const long long chunks = (vecs + (long long)kEach * wide - 1) / ((long long)kEach * wide);
+  const long long ctas = (p.rows + block.y - 1) / block.y * chunks;
   if (ctas > 0x7FFFFFFFll) return SPLITK_ERR_INVALID_SHAPE;
+  p.chunks = (uint32_t)chunks;
   DeviceSize dev;
   rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
