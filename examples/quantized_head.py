@@ -1,9 +1,11 @@
-"""The end of a decode step with 8-bit weights and activations: the last
-projection's output joins the residual stream and is normed to codes, the
-vocabulary head multiplies them with its codes, and the logits become the next
-token of each sequence, its log probability and its alternatives.
+"""The end of a decode step with 8-bit, or microscaled 4-bit, weights and
+activations: the last projection's output joins the residual stream and is normed
+to codes, the vocabulary head multiplies them with its codes, and the logits become
+the next token of each sequence, its log probability and its alternatives.  In 4 bits
+each step also adds its token to the sequence's history, whose tokens the next step's
+logits are adjusted for.
 
-    python examples/quantized_head.py [--tokens 4] [--width 7168] [--vocabulary 32000] [--steps 20]
+    python examples/quantized_head.py [--format i8|mx4] [--tokens 4] [--width 7168] [--vocabulary 32000] [--steps 20]
 
 Random weights; the same step in bf16 (``splitk_gemm_bf16``) runs beside it for
 comparison.
@@ -42,8 +44,34 @@ class QuantizedHead:
         return ids[:, 0], logprobs[:, 0], entropy, ids, logprobs
 
 
+class MicroscaledHead(QuantizedHead):
+    """The same with 4-bit codes and a scale for 32 of them, and a penalty for each time
+    that a token was chosen before."""
+
+    def __init__(self, norm: torch.Tensor, head: torch.Tensor, eps: float = 1e-6, rows: int = 1, most: int = 256,
+                 penalty: float = 0.5):
+        self.norm, self.eps = norm, eps
+        self.codes, self.scales = sk.splitk_quantize_mx4(head)
+        self.history = torch.full((rows, most), -1, dtype=torch.int64, device=head.device)
+        self.lengths = torch.zeros(rows, dtype=torch.int64, device=head.device)
+        self.penalty = torch.full((rows,), penalty, device=head.device)
+
+    def logits(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        codes, scale, _ = sk.splitk_rmsnorm_mx4(x, self.norm, residual, eps=self.eps, residual_out=residual)
+        logits = sk.splitk_gemm_mx4(self.codes, self.scales, codes, scale, out_dtype=torch.float32)
+        return sk.splitk_adjust_logits(logits, history=self.history, lengths=self.lengths, frequency=self.penalty, out=logits)
+
+    def step(self, x: torch.Tensor, residual: torch.Tensor, alternatives: int):
+        answer = super().step(x, residual, alternatives)
+        at = self.lengths.clamp_max(self.history.shape[1] - 1)
+        self.history.scatter_(1, at[:, None], answer[0][:, None])
+        self.lengths += 1
+        return answer
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    ap.add_argument("--format", choices=("i8", "mx4"), default="i8")
     ap.add_argument("--tokens", type=int, default=4)
     ap.add_argument("--width", type=int, default=7168)
     ap.add_argument("--vocabulary", type=int, default=32000)
@@ -65,7 +93,7 @@ def main() -> None:
     wide = sk.splitk_gemm_bf16(head, n)
     _, wide_entropy, wide_ids, wide_logprobs = sk.splitk_logprobs(wide, top_k=a.alternatives)
 
-    quantized = QuantizedHead(norm, head)
+    quantized = QuantizedHead(norm, head) if a.format == "i8" else MicroscaledHead(norm, head, rows=a.tokens)
     kept = residual.clone()
     token, logprob, entropy, ids, logprobs = quantized.step(x, kept, a.alternatives)
     # the bf16 step's first choice, as the quantized logits see it
