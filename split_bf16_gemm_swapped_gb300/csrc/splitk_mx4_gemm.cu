@@ -49,7 +49,9 @@ constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
 constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
 constexpr int kMxStages = 8;                         // of the ring, at most
 // K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks, which
-// the MMAs of two tiles of 256 tokens cover (1024) and those of one do not.
+// the MMAs of two tiles of 256 tokens cover (1024) and those of one do not.  Each tile's
+// place is free for the next copies by itself (with whole stages, the copies came too late:
+// 2048x18432x7168 93 us, so 90; 1000x7168x16384 54, 51).
 __host__ __device__ constexpr int sub_of(int tok) { return tok >= 128 ? 2 : 1; }
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
@@ -346,7 +348,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const uint32_t s_bar = s_s + 2u * kGroup * scales_of(kTok);
   const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes and scales are there
   const uint32_t bar_done = bar_full + 8u * kMxStages;      // [kMxStages] the MMAs have read them
-  const uint32_t bar_acc = bar_done + 8u * kMxStages;       // a tile's accumulator is complete
+  const uint32_t bar_half = bar_done + 8u * kMxStages;      // [kMxStages] those of the first of two K tiles have read it
+  const uint32_t bar_acc = bar_half + 8u * kMxStages;       // a tile's accumulator is complete
   const uint32_t bar_read = bar_acc + 8u;                   // leader: both CTAs' output warps have read it
   const uint32_t slot_tmem = bar_read + 8u, slot_abort = slot_tmem + 4u;
 
@@ -360,6 +363,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     for (int s = 0; s < stages; ++s) {
       dev::mbar_init(bar_full + 8u * s, 1u + 2u * kScaleWarps);
       dev::mbar_init(bar_done + 8u * s, 1u);
+      dev::mbar_init(bar_half + 8u * s, 1u);
     }
     dev::mbar_init(bar_acc, 1u);
     dev::mbar_init(bar_read, 2u * kOutWarps);
@@ -409,18 +413,20 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const MxTile t = MxTile::at<kTok>(p, tile, rank, half);
         for (int i = 0; i < t.steps; ++i, pos.advance(1, stages)) {
           const uint32_t s = (uint32_t)pos.index, bar = full_of_leader + 8u * s;
-          if (issued >= stages && !waiter.wait<false>(bar_done + 8u * s, pos.phase ^ 1u, kRoleWeightTma, i)) {
-            ok = false;
-            break;
-          }
-          if (half == 0) dev::mbar_arrive_expect_tx(bar_full + 8u * s, 2u * stage_bytes(kTok));
+          const bool again = issued >= stages;
 #pragma unroll
           for (int j = 0; j < kSub; ++j) {
+            if (again) ok = ok && waiter.wait<false>((j + 1 < kSub ? bar_half : bar_done) + 8u * s, pos.phase ^ 1u, kRoleWeightTma, i);
+            if (!ok) break;
+            if (j == 0) {
+              ++issued;
+              if (half == 0) dev::mbar_arrive_expect_tx(bar_full + 8u * s, 2u * stage_bytes(kTok));
+            }
             const int k = ((t.step0 + i) * kSub + j) * (kTileK / 2);
             tma_load_pair(s_a + (s * kSub + j) * kCodesA, &a_map, k, t.n0, t.l, bar, policy_a);
             tma_load_pair(s_b + (s * kSub + j) * codes_b(kTok), &b_map, k, t.m0 + half * (kTok / 2), t.l, bar, keep);
           }
-          ++issued;
+          if (!ok) break;
         }
       }
     }
@@ -458,6 +464,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                        j % 2 == 0 ? idesc_mxf4(2 * kMmaM, kTok, 0u) : idesc_mxf4(2 * kMmaM, kTok, 2u), t_a, t_b,
                        (i != 0 || j != 0) ? 1u : 0u, one);
             }
+            if (kSub == 2 && j == 3) commit_pair(bar_half + 8u * s, both, one);
             // the next stage is waited for while these are under way
             if (j == 4 * kSub - 3 && i + 1 < t.steps) ok = landed(i + 1);
           }

@@ -88,19 +88,14 @@ struct Eight {
   // The largest magnitude of a block (four lanes' vectors), from the bits: without
   // their signs the values are ordered as whole numbers, NaN above infinity.
   __device__ __forceinline__ float block_top() const {
+    constexpr uint32_t kMagnitude = kKind == kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    const auto larger = [](uint32_t a, uint32_t b) { return kKind == kF32 ? max(a, b) : max_u16x2(a, b); };
     uint32_t top = 0u;
-    if (kKind == kF32) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) top = max(top, w[i] & 0x7FFFFFFFu);
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      return __uint_as_float(top);
-    }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) top = max_u16x2(top, w[i] & 0x7FFF7FFFu);
-    top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    return half_value<kKind>(max(top & 0xFFFFu, top >> 16));
+    for (int i = 0; i < kWords; ++i) top = larger(top, w[i] & kMagnitude);
+    top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = larger(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    return kKind == kF32 ? __uint_as_float(top) : half_value<kKind>(max(top & 0xFFFFu, top >> 16));
   }
   __device__ __forceinline__ void set(const float (&v)[kVec]) {
 #pragma unroll
