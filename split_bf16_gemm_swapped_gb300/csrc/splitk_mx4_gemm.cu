@@ -465,10 +465,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                        (i != 0 || j != 0) ? 1u : 0u, one);
             }
             if (kSub == 2 && j == 3) commit_pair(bar_half + 8u * s, both, one);
-            // the next stage is waited for while these are under way
-            if (j == 4 * kSub - 3 && i + 1 < t.steps) ok = landed(i + 1);
           }
           commit_pair(bar_done + 8u * s, both, one);
+          // (the next stage is waited for while these are under way)
+          if (i + 1 < t.steps) ok = landed(i + 1);
         }
         commit_pair(bar_acc, both, one);
       }
