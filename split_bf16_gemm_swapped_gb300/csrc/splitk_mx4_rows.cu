@@ -61,7 +61,8 @@ template <int kKind>
 struct Eight {
   static constexpr int kWords = kKind == kF32 ? 8 : 4;
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const void* p, long long at, bool vec) {
+  template <class Place>
+  __device__ __forceinline__ void load(const void* p, Place at, bool vec) {
     if (vec) {
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * size_of(kKind));
 #pragma unroll
@@ -169,26 +170,29 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kernel(const QuantizePar
   dev::griddep_wait();
   const uint32_t group = p.chunks == gridDim.x ? 0u : blockIdx.x / p.chunks, chunk = blockIdx.x - group * p.chunks;
   const long long row = (long long)group * blockDim.y + threadIdx.y;
-  const long long first = ((long long)chunk * (kEach * blockDim.x) + threadIdx.x) * kVec;
+  const long long first = (long long)chunk * (kEach * blockDim.x * kVec);
+  // from the CTA's part of the row on, 32 bits hold a place
+  const int left = row < p.rows ? (int)min(p.width - first, (long long)(kEach * kRowThreads * kVec)) : 0;
+  const int step = (int)blockDim.x * kVec, at = (int)threadIdx.x * kVec;
+  const uint8_t* from = static_cast<const uint8_t*>(p.x) + (row * p.x_stride + first) * size_of(kKind);
+  uint8_t* codes = p.codes + (row * p.width + first) / 2;
+  uint8_t* scale = p.scale + (row * p.width + first) / kMxBlock;
   Eight<kKind> e[kEach] = {};
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const long long at = first + (long long)i * blockDim.x * kVec;
-    if (row < p.rows && at < p.width) e[i].load(p.x, row * p.x_stride + at, p.vec);
+    if (at + i * step < left) e[i].load(from, at + i * step, p.vec);
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const long long at = first + (long long)i * blockDim.x * kVec;
-    const bool in = row < p.rows && at < p.width;      // the same in a block's four lanes
+    const int place = at + i * step;
     const float top = e[i].block_top();
-    if (!in) continue;
+    if (place >= left) continue;                       // (the same in a block's four lanes)
     float v[kVec];
     e[i].values(v);
     uint32_t code;
     const uint32_t q = codes_of(v, top, code);
-    const long long to = row * p.width + at;
-    *reinterpret_cast<uint32_t*>(p.codes + to / 2) = q;
-    if (threadIdx.x % 4 == 0) p.scale[to / kMxBlock] = (uint8_t)code;
+    *reinterpret_cast<uint32_t*>(codes + (uint32_t)place / 2u) = q;
+    if (threadIdx.x % 4 == 0) scale[(uint32_t)place / (uint32_t)kMxBlock] = (uint8_t)code;
   }
 }
 
