@@ -16,7 +16,9 @@
 // history that lie in the span in shared memory (whole numbers: any order gives the
 // same) and list the tokens that they meet; then they go over the listed tokens one by
 // one.  Memory is the bound: each logit is read and written once, the history read
-// once for each span, from L2.  (Looking at every logit's count on its way took 224
+// once for each span, from L2: 256 x 131072 bf16 logits take 22.6 us (5.9 TB/s), 46 with
+// histories of 4096, 64 biases and masks (a span's three dependent phases, with two CTAs
+// an SM beside each other); one row of 131072 3.3 us.  (Looking at every logit's count on its way took 224
 // instructions for eight of each of a warp's lanes, since some lane always has a
 // counted one: 256 x 131072 logits with histories of 4096 tokens 51-86 us.)
 

@@ -12,13 +12,19 @@
 // of four holds in lane l, of each lane quadrant, the four codes of row 32 g + l.  Four
 // scale warps, a quadrant each, load 32s of rows, a sector of each (four K tiles: a
 // load costs the L1 cache a look-up a row, however short), exchange them through
-// shared memory and store all of them into their quadrants.  (Copies by
+// shared memory and store all of them into their quadrants (2048 x 18432 x 7168 110 us with
+// a word of one K tile a lane, 94 with sectors).  (Copies by
 // tcgen05.cp keep the tensor pipe from MMAs for ~38 clocks each: six a tile of 256
 // tokens, 742 clocks with its MMAs instead of 512.)
 //
-// What bounds it: few tokens, the weights' arrival; many, the MMAs, whose K = 64 at 256
-// tokens takes a pair 128 clocks (9.6 PFLOP/s at 1.93 GHz; ~72 for up to 128 tokens).
-// A pair brings 32 KiB a tile of 256 tokens for each CTA, a CTA alone would bring 48.
+// What bounds it: few tokens, the weights' arrival (1 x 18432 x 7168 14.3 us, 64 tokens
+// 14.7: 4.9 TB/s, of which 3 us before the first MMA and after the last); one token and
+// short weights, latency (1 x 7168 x 2048 4.8 us); many tokens, the copies' way from L2.
+// An MMA's K = 64 at 256 tokens takes a pair 128 clocks (9.6 PFLOP/s at 1.93 GHz; ~72 for
+// up to 128 tokens), but each CTA takes 32 KiB of codes a K tile of 512 clocks, 64
+// bytes a clock, which its way from L2 just holds: 2048 x 18432 x 7168 takes 91 us (5.9
+// PFLOP/s), 77 with no output stored, 71 with half the copies left out and 57 by the
+// MMAs' count; 1000 x 7168 x 16384 51 us.  (A CTA alone would bring 48 KiB a tile.)
 //
 // `split` pairs of a cluster may share one output tile, each taking a contiguous run
 // of K tiles; each CTA leaves its f32 sums in its own shared memory and then adds
