@@ -650,7 +650,7 @@ typedef struct splitk_adjust_t {
  * unless the above changes them; a row that allows nothing is -inf throughout.
  *   logits  bf16, f16 or f32 (type), rows `stride` elements apart (stride >= V)
  *   out     of the same type, rows out_stride apart; may be `logits` itself, at the
- *           same stride
+ *           same stride (else SPLITK_ERR_INVALID_ARGUMENT)
  */
 SPLITK_API int splitk_adjust_logits(const void *logits, int type, long long stride,
                                     const splitk_adjust_t *how, void *out, long long out_stride,

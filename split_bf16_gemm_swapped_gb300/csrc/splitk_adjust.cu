@@ -403,12 +403,13 @@ SPLITK_API int splitk_adjust_logits(const void* logits, int type, long long stri
       !aligned(h.bias_ids, 8) || !aligned(h.bias_values, 4) || !aligned(h.allowed, 4)) {
     return SPLITK_ERR_MISALIGNED;
   }
+  if (out == logits && M > 1 && stride != out_stride) return SPLITK_ERR_INVALID_ARGUMENT;    // rows over other rows
   // a launch's CTAs, of at least 1024 logits
   if ((long long)M * (V / 1024 + 2) > 0x7FFFFFFFll) return SPLITK_ERR_INVALID_SHAPE;
   DeviceSize dev;
   const int rc = require_device(&dev);
   if (rc != SPLITK_OK) return rc;
-  AdjustParams p{logits, stride, out_stride, out, h, V, 1, out == logits && stride == out_stride};
+  AdjustParams p{logits, stride, out_stride, out, h, V, 1, out == logits};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = type == SPLITK_DTYPE_F32   ? choose_adjust<SPLITK_DTYPE_F32>(p, M, dev, s)
                         : type == SPLITK_DTYPE_F16 ? choose_adjust<SPLITK_DTYPE_F16>(p, M, dev, s)

@@ -140,61 +140,71 @@ struct MxParams {
   int split, stages;
   int tile0, tile_end;      // the launch's tiles
   uint32_t tmem_cols;
-  int align;                // of the scales' rows: 32, 8, 4 or 1 bytes
+  bool sectors;             // the scales' rows are whole sectors of 32 bytes
   unsigned long long limit_ns;
   unsigned inject;
 };
 
-// The scale codes of one row and a group of K tiles: two words of four for each.
-struct ScaleRow {
-  uint32_t w[2 * kGroup];
-  // Codes [at, limit) of the row at `row`, 127 past the limit (its codes there are
-  // zeros, or the row is none).  kAlign: what the addresses row + at are multiples of
-  // (and the limit, but where it ends the row).  Words at odd addresses come from the
-  // two aligned ones around them, where all their bytes are within the array [first,
-  // end).
-  template <int kAlign>
-  __device__ __forceinline__ void load(const uint8_t* row, int at, int limit, const uint8_t* first, const uint8_t* end) {
-    constexpr uint32_t kOnes = 0x7F7F7F7Fu;
+// 16 bytes of an array [first, end), zeros outside it (out of line: an array's ends).
+__device__ __noinline__ uint4 edge_bytes(const uint8_t* p, const uint8_t* first, const uint8_t* end) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 2 * kGroup; ++i) w[i] = kOnes;
-    if constexpr (kAlign == 32) {
-      if (at < limit) {
+  for (int j = 0; j < 16; ++j) {
+    if (p + j >= first && p + j < end) w[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The scale codes of one row and a group of K tiles, 32 bytes.  kSector: they are a
+// sector of memory.  Else they lie somewhere in up to three times 16 bytes, and are cut
+// out when they are used, as they may still be on their way before.  (Word by word, two
+// loads each: 1300 x 6000 x 4448 73 us.)
+template <bool kSector>
+struct ScaleRow {
+  uint32_t x[kSector ? 8 : 12];
+  uint32_t shift;           // bytes before the row's first
+  int live;                 // bytes that are the row's
+  // Codes [at, limit) of the row at `row` of the array [first, end); limit 0: no row.
+  __device__ __forceinline__ void load(const uint8_t* row, int at, int limit, const uint8_t* first, const uint8_t* end) {
+    live = limit - at;
+    if constexpr (kSector) {
+      if (live > 0) {
         asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
                      : "l"(row + at)
                      : "memory");
       }
-    } else if constexpr (kAlign == 8) {
-#pragma unroll
-      for (int i = 0; i < 2 * kGroup; i += 2) {
-        if (at + 4 * i >= limit) continue;
-        const uint2 v = *reinterpret_cast<const uint2*>(row + at + 4 * i);
-        w[i] = v.x, w[i + 1] = v.y;
-      }
-    } else if constexpr (kAlign == 4) {
-#pragma unroll
-      for (int i = 0; i < 2 * kGroup; ++i) {
-        if (at + 4 * i < limit) w[i] = *reinterpret_cast<const uint32_t*>(row + at + 4 * i);
-      }
     } else {
+      shift = (uint32_t)(uintptr_t)(row + at) & 15u;
+      const uint8_t* low = row + at - shift;
 #pragma unroll
-      for (int i = 0; i < 2 * kGroup; ++i) {
-        const int n = limit - (at + 4 * i);
-        if (n <= 0) continue;
-        const uint8_t* p = row + at + 4 * i;
-        const uint8_t* low = reinterpret_cast<const uint8_t*>((uintptr_t)p & ~(uintptr_t)3);
-        uint32_t v = 0u;
-        if (low >= first && low + 8 <= end) {
-          const uint32_t* two = reinterpret_cast<const uint32_t*>(low);
-          v = __funnelshift_r(two[0], two[1], 8u * (uint32_t)(p - low));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j < n) v |= (uint32_t)p[j] << (8 * j);
-          }
+      for (int c = 0; c < 3; ++c) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const uint8_t* p = low + 16 * c;
+        if (live > 0 && 16 * c < (int)shift + min(live, 32)) {
+          v = p >= first && p + 16 <= end ? *reinterpret_cast<const uint4*>(p) : edge_bytes(p, first, end);
         }
-        const uint32_t kept = n >= 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+        x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
+      }
+    }
+  }
+  // The codes, 127 past the limit (the row's codes there are zeros, or it is none).
+  __device__ __forceinline__ void words(uint32_t (&w)[2 * kGroup]) const {
+    constexpr uint32_t kOnes = 0x7F7F7F7Fu;
+    if constexpr (kSector) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = live > 0 ? x[i] : kOnes;
+    } else {
+      uint32_t y[10], z[9];
+#pragma unroll
+      for (int i = 0; i < 10; ++i) y[i] = (shift & 8u) != 0u ? x[i + 2] : x[i];
+#pragma unroll
+      for (int i = 0; i < 9; ++i) z[i] = (shift & 4u) != 0u ? y[i + 1] : y[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v = __funnelshift_r(z[i], z[i + 1], 8u * (shift & 3u));
+        const int n = live - 4 * i;
+        const uint32_t kept = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
         w[i] = (v & kept) | (kOnes & ~kept);
       }
     }
@@ -256,7 +266,7 @@ struct ScaleRing {
 // One scale warp: the CTA's K tiles, of one output tile after another, in groups of
 // kGroup.  Its rows' loads of the next group are under way while it stores this one's.
 // Two buffers let one barrier of the warps a group do.
-template <int kTok, int kAlign>
+template <int kTok, bool kSector>
 __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing& r, int tile0, int step, int rank, int half,
                                              int warp, int lane) {
   constexpr int kGroups = groups_b(kTok), kLive = (kTok + 31) / 32;        // 128s and 32s of tokens
@@ -267,18 +277,18 @@ __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing&
   const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
   MxTile t = MxTile::at<kTok>(p, tile0, rank, half);
   int tile = tile0, kt = 0;                             // where the group to load starts
-  const int k_tiles = t.steps * kSub, groups = (k_tiles + kGroup - 1) / kGroup * ((p.tile_end - tile0 + step - 1) / step);
-  ScaleRow a, b[kOwn];
+  // (groups start at multiples of their size: a share of K may begin within its first)
+  const int skip = t.step0 * kSub % kGroup, k_tiles = skip + t.steps * kSub, groups = (k_tiles + kGroup - 1) / kGroup * ((p.tile_end - tile0 + step - 1) / step);
+  ScaleRow<kSector> a, b[kOwn];
   const auto load = [&] {
     if (tile >= p.tile_end) return;
-    const int at = (t.step0 * kSub + kt) * (kTileK / kMxBlock);
+    const int at = (t.step0 * kSub - skip + kt) * (kTileK / kMxBlock);
     const int n = t.n0 + lane + 32 * warp;
-    a.template load<kAlign>(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? blocks : 0, p.a_scale, a_end);
+    a.load(p.a_scale + ((long long)t.l * p.N + n) * blocks, at, n < p.N ? blocks : 0, p.a_scale, a_end);
 #pragma unroll
     for (int q = 0; q < kOwn; ++q) {
       const int o = 32 * (warp + kScaleWarps * q) + lane, m = t.m0 + o;
-      b[q].template load<kAlign>(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? blocks : 0, p.b_scale,
-                                 b_end);
+      b[q].load(p.b_scale + ((long long)t.l * p.M + m) * blocks, at, o < kTok && m < p.M ? blocks : 0, p.b_scale, b_end);
     }
     kt += kGroup;
     if (kt >= k_tiles) {
@@ -294,21 +304,23 @@ __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing&
   for (int group = 0; group < groups; ++group) {
     // word w of a K tile: 512 bytes of A's rows, then of B's each 128
     const uint32_t mine = buffer + 16u * lane + 4u * warp;
+    uint32_t w[2 * kGroup];
+    a.words(w);
 #pragma unroll
-    for (int j = 0; j < 2 * kGroup; ++j) {
-      const uint32_t at = mine + (j / 2) * scales_of(kTok) + (j % 2) * kScaleAtom;
-      dev::st_shared_u32(at, a.w[j]);
+    for (int j = 0; j < 2 * kGroup; ++j) dev::st_shared_u32(mine + (j / 2) * scales_of(kTok) + (j % 2) * kScaleAtom, w[j]);
 #pragma unroll
-      for (int q = 0; q < kOwn; ++q) {
-        if (kLive >= kScaleWarps || warp < kLive) {
-          dev::st_shared_u32(at + (2u + (j % 2) * (kGroups - 1u) + q) * kScaleAtom, b[q].w[j]);
-        }
+    for (int q = 0; q < kOwn; ++q) {
+      if (kLive < kScaleWarps && warp >= kLive) continue;
+      b[q].words(w);
+#pragma unroll
+      for (int j = 0; j < 2 * kGroup; ++j) {
+        dev::st_shared_u32(mine + (j / 2) * scales_of(kTok) + (2u + (j % 2) * kGroups + q) * kScaleAtom, w[j]);
       }
     }
     load();
     dev::named_bar_sync(1, 32 * kScaleWarps);
 #pragma unroll 1
-    for (int i = 0; ok && i < kStages && i * kSub < left; ++i, ++used) {
+    for (int i = left == k_tiles ? skip / kSub : 0; ok && i < kStages && i * kSub < left; ++i, ++used) {
       uint32_t v[kVecs][4];
 #pragma unroll
       for (int c = 0; c < kVecs; ++c) {
@@ -486,12 +498,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int own = warp - kScale0;                         // and its lane quadrant
     const ScaleRing ring{s_s, tmem + ((uint32_t)(32 * own) << 16) + mx_acc_cols(kTok), dev::mapa(bar_full, leader), bar_done, stages,
                          waiter};
-    // (a K tile is 8 bytes of a row, a group of them 32)
-    switch (p.align == 32 && tile_first.step0 * kSub % kGroup != 0 ? 8 : p.align) {
-      case 32: bring_scales<kTok, 32>(p, ring, tile0, step, rank, half, own, lane); break;
-      case 8: bring_scales<kTok, 8>(p, ring, tile0, step, rank, half, own, lane); break;
-      case 4: bring_scales<kTok, 4>(p, ring, tile0, step, rank, half, own, lane); break;
-      default: bring_scales<kTok, 1>(p, ring, tile0, step, rank, half, own, lane); break;
+    // (a K tile is 8 bytes of a row, a group of them a sector where rows are whole ones)
+    if (p.sectors) {
+      bring_scales<kTok, true>(p, ring, tile0, step, rank, half, own, lane);
+    } else {
+      bring_scales<kTok, false>(p, ring, tile0, step, rank, half, own, lane);
     }
   } else if (warp >= kOut0) {
     // ---- output: warp kOut0 + w has TMEM lane quadrant w, thread = weight row
@@ -714,21 +725,24 @@ int prepare_mx4(const DeviceSize& dev, MxDevice* out) {
 
 // What a launch of `tiles` tiles costs, in microseconds: a pair's time for a K tile where
 // nothing but its own work bounds it, no less than the pairs at work take to read theirs
-// (6.2 bytes a picosecond: what these kernels reach on codes and scales from memory),
+// (6.2 bytes a picosecond: what these kernels reach on codes and scales from memory; the
+// `m_tiles` tiles of the same weights read them once),
 // and what comes before, between and after the tiles (for a tile in shares, their sums
 // too: with its tokens). Measured, with the choice it
 // decides (us): 1000x7168x16384 by 128 tokens 49.8, by 256 54.6; 2048x18432x7168
 // 108.5 and 94.3; 2048x7168x2048 17.9 and 16.8; 1x7168x2048 on one pair a tile 4.8, on
 // two 5.3; 16x4096x7168 10.0, 7.6, on three 7.5; 64x7168x16384 20.6 and 15.6;
-// 1x500x16384 18.4, 11.1, 8.8, on four 7.1; 64x18432x7168 14.7 and 21.8 (two rounds).
-double launch_us(long long tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
+// 1x500x16384 18.4, 11.1, 8.8, on four 7.1; 64x18432x7168 14.7 and 21.8 (two rounds);
+// 300x10300x8192 by 128 tokens 21.9, by 256 27.7; 520x7168x4096 14.0 and 17.8;
+// 16x20480x16384 in two rounds 44.8, its last 4 tiles on four pairs each 36.9.
+double launch_us(long long tiles, int m_tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
   const int fit = d.clusters[split - 1];
   if (tiles == 0) return 0.0;
   if (fit <= 0 || split > (k_tiles + sub_of(tokens) - 1) / sub_of(tokens)) return 1e30;
   const double rounds = (double)((tiles + fit - 1) / fit);
   const double pairs = (double)(std::min<long long>(tiles, fit) * split);
   const double step = std::max(tokens == 256 ? 0.39 : tokens == 128 ? 0.23 : 0.24,
-                               tokens == 256 ? 0.0 : pairs * (2 * kMmaM * kTileK * 17 / 32) / 6.2e6);
+                               tokens == 256 ? 0.0 : pairs / m_tiles * (2 * kMmaM * kTileK * 17 / 32) / 6.2e6);
   const double each = step * ((k_tiles + split - 1) / split);
   return rounds * each + (split > 1 ? rounds * (3.0 + 0.02 * (pairs + tokens)) : 3.2 + (rounds - 1) * 0.5);
 }
@@ -740,13 +754,14 @@ MxPlan plan_mx4(int M, int N, int K, int L, const MxDevice& d) {
   for (int tokens : kTokens) {
     if (tokens < 128 && tokens < M) continue;          // the smallest that holds M, or 128 or 256
     if (tokens > 16 && tokens / 2 >= M) continue;
-    const long long tiles = (long long)((M + tokens - 1) / tokens) * ((N + 2 * kMmaM - 1) / (2 * kMmaM)) * L;
-    const double all = launch_us(tiles, tokens, k_tiles, 1, d);
+    const int m_tiles = (M + tokens - 1) / tokens;
+    const long long tiles = (long long)m_tiles * ((N + 2 * kMmaM - 1) / (2 * kMmaM)) * L;
+    const double all = launch_us(tiles, m_tiles, tokens, k_tiles, 1, d);
     if (all < least) least = all, best = MxPlan{tokens, (int)tiles, 1};
     const long long rounds = d.clusters[0] > 0 ? tiles / d.clusters[0] : 0;
     for (int split = 2; split <= kMaxSplit; ++split) {
       for (long long whole : {0ll, rounds * d.clusters[0]}) {
-        const double us = launch_us(whole, tokens, k_tiles, 1, d) + launch_us(tiles - whole, tokens, k_tiles, split, d) -
+        const double us = launch_us(whole, m_tiles, tokens, k_tiles, 1, d) + launch_us(tiles - whole, m_tiles, tokens, k_tiles, split, d) -
                           (whole > 0 ? 2.0 : 0.0);
         if (us < least) least = us, best = MxPlan{tokens, (int)whole, split};
       }
@@ -814,12 +829,9 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
     return SPLITK_ERR_INVALID_SHAPE;
   }
   const int blocks = K / kMxBlock;
-  const int align = blocks % 32 == 0 && aligned(a_scale, 32) && aligned(b_scale, 32) ? 32
-                    : blocks % 8 == 0 && aligned(a_scale, 8) && aligned(b_scale, 8)   ? 8
-                    : blocks % 4 == 0 && aligned(a_scale, 4) && aligned(b_scale, 4) ? 4
-                                                                                    : 1;
+  const bool sectors = blocks % 32 == 0 && aligned(a_scale, 32) && aligned(b_scale, 32);
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
-                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, align,
+                   static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, sectors,
                    wait_limit_ns(), injected()};
   const uint8_t *a = static_cast<const uint8_t*>(a_q), *b = static_cast<const uint8_t*>(b_q);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -386,6 +386,24 @@ def test_product_of_a_vocabulary_head(M, N, K):
     assert sk.splitk_get_status() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 20480, 4096), (40, 19600, 8192), (100, 20000, 4128), (300, 10300, 8192), (520, 7000, 4096),
+                                   (1, 300, (1 << 20) + 32), (200, 500, 1 << 18)])
+def test_product_of_a_round_of_tiles_and_a_few_and_of_long_rows(M, N, K):
+    """A few tiles more than there are pairs of SMs run on several pairs each, after the
+    others or alone; rows of many K tiles."""
+    g = gen(M + K)
+    a, sa = sk.splitk_quantize_mx4(randn((N, K), g))
+    b, sb = sk.splitk_quantize_mx4(randn((M, K), g))
+    bias = randn((N,), g)
+    c = sk.splitk_gemm_mx4(a, sa, b, sb, bias=bias, out_dtype=F32)
+    av, bv = (sk.splitk_dequantize_mx4(q, s, out_dtype=F32).double() for q, s in ((a, sa), (b, sb)))
+    ref = bv @ av.T + bias.double()
+    # exact products; at least 16 of them are added at a time, each time off by 2 u at most
+    bound = 2 * 2.0 ** -24 * (K / 16 + 16) * (bv.abs() @ av.abs().T) + 2.0 ** -24 * ref.abs()
+    assert ((c.double() - ref).abs() <= bound).all()
+    assert sk.splitk_get_status() == 0
+
+
 @pytest.mark.parametrize("M", [1, 4, 128])
 def test_rows_before_a_wide_down_projection(M):
     """Widths of 53248: norm to codes, then the product with K as long."""

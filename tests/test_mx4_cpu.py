@@ -102,6 +102,7 @@ def test_adjust_refusals():
     for kw in (dict(kind=3), dict(kind=-1), dict(history=P, history_length=-1), dict(history=P, history_length=(1 << 30) + 1),
                dict(bias_count=1025, bias_ids=P, bias_values=P), dict(bias_count=-1)):
         assert adjust(**kw) == ARG, kw
+    assert adjust(x=P, out=P, stride=100, out_stride=101) == ARG          # in place, rows over other rows
     some = dict(history=P, history_length=4, bias_ids=P, bias_values=P, bias_count=2)
     for kw in (dict(x=P + 1), dict(x=P + 2, kind=1), dict(out=P + 1), dict(allowed=P + 2), dict(some, history=P + 4),
                dict(some, lengths=P + 4), dict(some, prompt_lengths=P + 4), dict(some, repetition=P + 2),
