@@ -53,12 +53,13 @@ namespace {
 constexpr int kScale0 = 4, kScaleWarps = 4, kOut0 = kScale0 + kScaleWarps, kOutWarps = 4;
 constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
 constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
-constexpr int kMxStages = 8;                         // of the ring, at most
-// K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks, which
-// the MMAs of two tiles of 256 tokens cover (1024) and those of one do not.  Each tile's
+constexpr int kMxStages = 4;                         // of the ring, at most
+// K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks and its
+// scales a scale warp ~400, the MMAs of one tile 288 to 512 (1x500x16384 7.3 us with one,
+// 6.7 with two; 16x4096x7168 7.5, 7.4; 7x2080x256 3.7, 3.8).  Each tile's
 // place is free for the next copies by itself (with whole stages, the copies came too late:
 // 2048x18432x7168 93 us, so 90; 1000x7168x16384 54, 51).
-__host__ __device__ constexpr int sub_of(int tok) { return tok >= 128 ? 2 : 1; }
+constexpr int kSub = 2;
 constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
 constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
 constexpr int kGroup = 4;                            // K tiles whose scales the scale warps exchange at once
@@ -70,7 +71,7 @@ constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
 __host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok / 2 * (kTileK / 2); }
 __host__ __device__ constexpr int groups_b(int tok) { return (tok + 127) / 128; }     // of 128 tokens
 __host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAtom * (1u + groups_b(tok)); }
-__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return sub_of(tok) * (kCodesA + codes_b(tok)); }
+__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kSub * (kCodesA + codes_b(tok)); }
 __host__ __device__ constexpr uint32_t mx_acc_cols(int tok) { return tok < 32 ? 32u : (uint32_t)tok; }
 __host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a K tile
 
@@ -145,16 +146,6 @@ struct MxParams {
   unsigned inject;
 };
 
-// 16 bytes of an array [first, end), zeros outside it (out of line: an array's ends).
-__device__ __noinline__ uint4 edge_bytes(const uint8_t* p, const uint8_t* first, const uint8_t* end) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (p + j >= first && p + j < end) w[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // The scale codes of one row and a group of K tiles, 32 bytes.  kSector: they are a
 // sector of memory.  Else they lie somewhere in up to three times 16 bytes, and are cut
 // out when they are used, as they may still be on their way before.  (Word by word, two
@@ -177,14 +168,22 @@ struct ScaleRow {
     } else {
       shift = (uint32_t)(uintptr_t)(row + at) & 15u;
       const uint8_t* low = row + at - shift;
+      const int bytes = live > 0 ? (int)shift + min(live, 32) : 0;       // from `low` on, to the last one wanted
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        const uint8_t* p = low + 16 * c;
-        if (live > 0 && 16 * c < (int)shift + min(live, 32)) {
-          v = p >= first && p + 16 <= end ? *reinterpret_cast<const uint4*>(p) : edge_bytes(p, first, end);
+      for (int i = 0; i < 12; ++i) x[i] = 0u;
+      if (low >= first && low + ((bytes + 15) & ~15) <= end) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (16 * c >= bytes) continue;
+          const uint4 v = reinterpret_cast<const uint4*>(low)[c];
+          x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
         }
-        x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
+      } else {                                               // an end of the array: byte by byte
+        shift = 0u;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < live) x[j / 4] |= (uint32_t)row[at + j] << (8 * (j % 4));
+        }
       }
     }
   }
@@ -242,7 +241,7 @@ struct MxTile {
   template <int kTok>
   __device__ __forceinline__ static MxTile at(const MxParams& p, int tile, int rank, int half) {
     const int m_tiles = (p.M + kTok - 1) / kTok, n_tiles = (p.N + 2 * kMmaM - 1) / (2 * kMmaM);
-    constexpr int kStepK = kTileK * sub_of(kTok);
+    constexpr int kStepK = kTileK * kSub;
     const int total = (p.K + kStepK - 1) / kStepK, each = total / p.split, extra = total % p.split;
     MxTile t;
     t.m0 = (tile % m_tiles) * kTok;
@@ -271,14 +270,15 @@ __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing&
                                              int warp, int lane) {
   constexpr int kGroups = groups_b(kTok), kLive = (kTok + 31) / 32;        // 128s and 32s of tokens
   constexpr int kOwn = (kLive + kScaleWarps - 1) / kScaleWarps;            // of which a warp loads at most
-  constexpr int kSub = sub_of(kTok), kStages = kGroup / kSub;              // whole stages a group
+  constexpr int kStages = kGroup / kSub;              // whole stages a group
   constexpr int kVecs = 2 * kSub * (1 + kGroups);                          // 16 bytes of a lane, of a stage
   const int blocks = p.K / kMxBlock;
   const uint8_t *a_end = p.a_scale + (long long)p.L * p.N * blocks, *b_end = p.b_scale + (long long)p.L * p.M * blocks;
   MxTile t = MxTile::at<kTok>(p, tile0, rank, half);
   int tile = tile0, kt = 0;                             // where the group to load starts
   // (groups start at multiples of their size: a share of K may begin within its first)
-  const int skip = t.step0 * kSub % kGroup, k_tiles = skip + t.steps * kSub, groups = (k_tiles + kGroup - 1) / kGroup * ((p.tile_end - tile0 + step - 1) / step);
+  const int skip = t.step0 * kSub % kGroup, k_tiles = skip + t.steps * kSub;
+  const int groups = (k_tiles + kGroup - 1) / kGroup * ((p.tile_end - tile0 + step - 1) / step);
   ScaleRow<kSector> a, b[kOwn];
   const auto load = [&] {
     if (tile >= p.tile_end) return;
@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const MxParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (dev::smem_u32(smem_raw) + (kAlignSlack - 1)) & ~(kAlignSlack - 1);
-  constexpr int kSub = sub_of(kTok);
   const int stages = p.stages, split = p.split;
   const uint32_t s_a = base;
   const uint32_t s_b = s_a + (uint32_t)stages * kSub * kCodesA;
@@ -434,7 +433,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           const bool again = issued >= stages;
 #pragma unroll
           for (int j = 0; j < kSub; ++j) {
-            if (again) ok = ok && waiter.wait<false>((j + 1 < kSub ? bar_half : bar_done) + 8u * s, pos.phase ^ 1u, kRoleWeightTma, i);
+            if (again) {
+              ok = ok && waiter.wait<false>((j == 0 ? bar_half : bar_done) + 8u * s, pos.phase ^ 1u, kRoleWeightTma, i);
+            }
             if (!ok) break;
             if (j == 0) {
               ++issued;
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                        j % 2 == 0 ? idesc_mxf4(2 * kMmaM, kTok, 0u) : idesc_mxf4(2 * kMmaM, kTok, 2u), t_a, t_b,
                        (i != 0 || j != 0) ? 1u : 0u, one);
             }
-            if (kSub == 2 && j == 3) commit_pair(bar_half + 8u * s, both, one);
+            if (j == 3) commit_pair(bar_half + 8u * s, both, one);
           }
           commit_pair(bar_done + 8u * s, both, one);
           // (the next stage is waited for while these are under way)
@@ -652,13 +653,13 @@ size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& 
 }
 
 // The ring for CTAs of `steps` stages' shares of K (of all their tiles).
-// For few tokens 8 stages, or 6 where nearly all pairs work (bytes in flight beyond some
-// 16 MB no longer help: 64x7168x16384 on 56 pairs 16.1 us with 6 and 15.6 with 8,
+// For few tokens 4 stages, or 3 where nearly all pairs work (bytes in flight beyond some
+// 16 MB no longer help: 64x7168x16384 on 56 pairs 16.1 us with 3 and 15.6 with 4,
 // 1x7168x2048 on 28 4.9 and 4.8, but 1x18432x7168 on 72 14.3 and 14.8).
 MxRing ring_of(int tokens, int split, long long pairs, long long steps, const DeviceSize& dev) {
-  int stages = (int)std::min<long long>(steps, tokens <= 64 && pairs * 5 > dev.num_sms * 2 ? 6 : kMxStages);
+  int stages = (int)std::min<long long>(steps, tokens <= 64 && pairs * 5 > dev.num_sms * 2 ? 3 : kMxStages);
   for (;; --stages) {
-    const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)(stages * sub_of(tokens)) * scale_cols(tokens));
+    const uint32_t cols = pow2_at_least(mx_acc_cols(tokens) + (uint32_t)(stages * kSub) * scale_cols(tokens));
     const size_t smem = mx_smem(tokens, stages, split, cols, dev);
     if (stages == 1 || (cols <= 512u && smem <= dev.smem_optin)) return MxRing{stages, cols, smem};
   }
@@ -729,25 +730,27 @@ int prepare_mx4(const DeviceSize& dev, MxDevice* out) {
 // `m_tiles` tiles of the same weights read them once),
 // and what comes before, between and after the tiles (for a tile in shares, their sums
 // too: with its tokens). Measured, with the choice it
-// decides (us): 1000x7168x16384 by 128 tokens 49.8, by 256 54.6; 2048x18432x7168
-// 108.5 and 94.3; 2048x7168x2048 17.9 and 16.8; 1x7168x2048 on one pair a tile 4.8, on
+// decides (us): 1000x7168x16384 by 128 tokens 52.9, by 256 47.8; 2048x18432x7168
+// 108.5 and 88.7; 2048x7168x2048 17.9 and 16.8; 1x7168x2048 on one pair a tile 4.8, on
 // two 5.3; 16x4096x7168 10.0, 7.6, on three 7.5; 64x7168x16384 20.6 and 15.6;
 // 1x500x16384 18.4, 11.1, 8.8, on four 7.1; 64x18432x7168 14.7 and 21.8 (two rounds);
 // 300x10300x8192 by 128 tokens 21.9, by 256 27.7; 520x7168x4096 14.0 and 17.8;
 // 16x20480x16384 in two rounds 44.8, its last 4 tiles on four pairs each 36.9.
-double launch_us(long long tiles, int m_tiles, int tokens, int k_tiles, int split, const MxDevice& d) {
+double launch_us(long long tiles, int m_tiles, int tokens, int k_tiles, int split, bool sectors, const MxDevice& d) {
   const int fit = d.clusters[split - 1];
   if (tiles == 0) return 0.0;
-  if (fit <= 0 || split > (k_tiles + sub_of(tokens) - 1) / sub_of(tokens)) return 1e30;
-  const double rounds = (double)((tiles + fit - 1) / fit);
-  const double pairs = (double)(std::min<long long>(tiles, fit) * split);
-  const double step = std::max(tokens == 256 ? 0.39 : tokens == 128 ? 0.23 : 0.24,
-                               tokens == 256 ? 0.0 : pairs / m_tiles * (2 * kMmaM * kTileK * 17 / 32) / 6.2e6);
-  const double each = step * ((k_tiles + split - 1) / split);
-  return rounds * each + (split > 1 ? rounds * (3.0 + 0.02 * (pairs + tokens)) : 3.2 + (rounds - 1) * 0.5);
+  if (fit <= 0 || split > (k_tiles + kSub - 1) / kSub) return 1e30;
+  // (scales that are no sectors: 0.13 to 0.18 more)
+  const double own = (tokens == 256 ? 0.345 : tokens == 128 ? 0.25 : 0.22) + (sectors ? 0.0 : 0.16);
+  const auto round = [&](long long n) {
+    const double pairs = (double)(n * split);
+    const double arrival = tokens == 256 ? 0.0 : pairs / m_tiles * (2 * kMmaM * kTileK * 17 / 32) / 6.2e6;
+    return std::max(own, arrival) * ((k_tiles + split - 1) / split) + (split > 1 ? 2.7 + 0.02 * (pairs + tokens) : 0.5);
+  };
+  return (double)(tiles / fit) * round(fit) + (tiles % fit > 0 ? round(tiles % fit) : 0.0) + (split > 1 ? 0.0 : 2.3 + 0.01 * tokens);
 }
 
-MxPlan plan_mx4(int M, int N, int K, int L, const MxDevice& d) {
+MxPlan plan_mx4(int M, int N, int K, int L, bool sectors, const MxDevice& d) {
   const int k_tiles = (K + kTileK - 1) / kTileK;
   MxPlan best{};
   double least = 1e30;
@@ -756,14 +759,15 @@ MxPlan plan_mx4(int M, int N, int K, int L, const MxDevice& d) {
     if (tokens > 16 && tokens / 2 >= M) continue;
     const int m_tiles = (M + tokens - 1) / tokens;
     const long long tiles = (long long)m_tiles * ((N + 2 * kMmaM - 1) / (2 * kMmaM)) * L;
-    const double all = launch_us(tiles, m_tiles, tokens, k_tiles, 1, d);
+    const double all = launch_us(tiles, m_tiles, tokens, k_tiles, 1, sectors, d);
     if (all < least) least = all, best = MxPlan{tokens, (int)tiles, 1};
     const long long rounds = d.clusters[0] > 0 ? tiles / d.clusters[0] : 0;
     for (int split = 2; split <= kMaxSplit; ++split) {
       for (long long whole : {0ll, rounds * d.clusters[0]}) {
-        const double us = launch_us(whole, m_tiles, tokens, k_tiles, 1, d) + launch_us(tiles - whole, m_tiles, tokens, k_tiles, split, d) -
-                          (whole > 0 ? 2.0 : 0.0);
-        if (us < least) least = us, best = MxPlan{tokens, (int)whole, split};
+        // (what is split has to be worth more than the estimate's errors of short K)
+        const double us = launch_us(whole, m_tiles, tokens, k_tiles, 1, sectors, d) +
+                          launch_us(tiles - whole, m_tiles, tokens, k_tiles, split, sectors, d);
+        if (us + 0.27 < least) least = us, best = MxPlan{tokens, (int)whole, split};
       }
     }
   }
@@ -780,9 +784,10 @@ cudaError_t launch_mx4(const uint8_t* a, const uint8_t* b, const MxParams& p, co
     return cudaErrorInvalidValue;
   }
   const long long tiles = (long long)((p.M + kTok - 1) / kTok) * ((p.N + 2 * kMmaM - 1) / (2 * kMmaM)) * p.L;
-  const int total = (p.K + kTileK * sub_of(kTok) - 1) / (kTileK * sub_of(kTok));
+  const int total = (p.K + kTileK * kSub - 1) / (kTileK * kSub);
   const auto launch = [&](int first, long long end, int split, long long clusters) {
-    const MxRing ring = ring_of(kTok, split, clusters * split, (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters), dev);
+    const long long steps = (long long)((total + split - 1) / split) * ((end - first + clusters - 1) / clusters);
+    const MxRing ring = ring_of(kTok, split, clusters * split, steps, dev);
     MxParams q = p;
     q.split = split, q.stages = ring.stages, q.tmem_cols = ring.tmem_cols;
     q.tile0 = first, q.tile_end = (int)end;
@@ -822,14 +827,14 @@ SPLITK_API int splitk_gemm_mx4(const void* a_q, const void* a_scale, const void*
   MxDevice d;
   rc = prepare_mx4(dev, &d);
   if (rc != SPLITK_OK) return rc;
-  const MxPlan plan = plan_mx4(M, N, K, L, d);
+  const int blocks = K / kMxBlock;
+  const bool sectors = blocks % 32 == 0 && aligned(a_scale, 32) && aligned(b_scale, 32);
+  const MxPlan plan = plan_mx4(M, N, K, L, sectors, d);
   if (plan.tokens == 0) return SPLITK_ERR_NO_FIT;      // no CTA pair of it fits the device
   // (a CTA counts the K tiles of all its tiles)
   if (((long long)plan.whole / std::max(d.clusters[0], 1) + 1) * ((K + kTileK - 1) / kTileK) > (1ll << 30)) {
     return SPLITK_ERR_INVALID_SHAPE;
   }
-  const int blocks = K / kMxBlock;
-  const bool sectors = blocks % 32 == 0 && aligned(a_scale, 32) && aligned(b_scale, 32);
   const MxParams p{static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
                    static_cast<const uint16_t*>(bias), c, c_type == SPLITK_DTYPE_F32, M, N, K, L, 1, 1, 0, 0, 0u, sectors,
                    wait_limit_ns(), injected()};
