@@ -17,14 +17,14 @@
 // tcgen05.cp keep the tensor pipe from MMAs for ~38 clocks each: six a tile of 256
 // tokens, 742 clocks with its MMAs instead of 512.)
 //
-// What bounds it: few tokens, the weights' arrival (1 x 18432 x 7168 14.3 us, 64 tokens
-// 14.7: 4.9 TB/s, of which 3 us before the first MMA and after the last); one token and
-// short weights, latency (1 x 7168 x 2048 4.8 us); many tokens, the copies' way from L2.
+// What bounds it: few tokens, the weights' arrival (1 x 18432 x 7168 14.1 us, 64 tokens
+// 14.4: 5.0 TB/s, of which 3 us before the first MMA and after the last); one token and
+// short weights, latency (1 x 7168 x 2048 4.75 us); many tokens, the copies' way from L2.
 // An MMA's K = 64 at 256 tokens takes a pair 128 clocks (9.6 PFLOP/s at 1.93 GHz; ~72 for
 // up to 128 tokens), but each CTA takes 32 KiB of codes a K tile of 512 clocks, 64
-// bytes a clock, which its way from L2 just holds: 2048 x 18432 x 7168 takes 91 us (5.9
-// PFLOP/s), 77 with no output stored, 71 with half the copies left out and 57 by the
-// MMAs' count; 1000 x 7168 x 16384 51 us.  (A CTA alone would bring 48 KiB a tile.)
+// bytes a clock, which its way from L2 just holds: 2048 x 18432 x 7168 takes 89.5 us (6.0
+// PFLOP/s), 77 with no output stored, 71 without scales' loads and half the copies, too,
+// and 57 by the MMAs' count; 1000 x 7168 x 16384 50.5 us.  (A CTA alone would bring 48 KiB a tile.)
 //
 // `split` pairs of a cluster may share one output tile, each taking a contiguous run
 // of K tiles; each CTA leaves its f32 sums in its own shared memory and then adds
