@@ -76,30 +76,44 @@ __device__ __forceinline__ constexpr uint32_t minus_infinity() {
 constexpr uint32_t kBiased = 0x80000000u, kTwice = 0x40000000u;
 constexpr int kMaxHistory = 1 << 28;       // counts stay below
 
-// A row's biases that lie in the span: slot and place in the row's list, in any order.
+// A row's biases: the slot of each in the span, or kOutside, and its value, by place in
+// the row's list; and the places of those that lie in the span, in any order.
+constexpr uint32_t kOutside = 0xFFFFu;
 struct BiasList {
-  int count;
-  uint32_t entry[kMaxBias];                // place << 16 | slot
-  float value[kMaxBias];
-  __device__ __forceinline__ int place(int i) const { return (int)(entry[i] >> 16); }
-  __device__ __forceinline__ uint32_t slot(int i) const { return entry[i] & 0xFFFFu; }
+  int count;                               // that lie in the span
+  uint16_t place[kMaxBias];
+  alignas(16) uint16_t slot[kMaxBias];     // to a multiple of eight
+  alignas(16) float value[kMaxBias];       // of those that lie in the span
 };
 
-// The sum of a slot's biases in the list's order, for its first one alone (entry
-// `first`): false for the others.
-__device__ __noinline__ bool bias_sum(const BiasList& list, int first, float* sum) {
-  const uint32_t slot = list.slot(first);
-  float total = list.value[first];
-  for (int last = list.place(first);;) {
-    int next = -1;                         // the entry of the place after `last`
-    for (int i = 0; i < list.count; ++i) {
-      if (list.slot(i) != slot) continue;
-      if (list.place(i) < list.place(first)) return false;
-      if (list.place(i) > last && (next < 0 || list.place(i) < list.place(next))) next = i;
+// The sum of a slot's biases in the list's order, for its first one alone (at `place`):
+// false for the others.  One pass over the list's `n` slots, eight a load: whether any of
+// two is the one looked for is whether their difference has a zero half.  The eight
+// values are there before the first is needed, and nothing branches between additions.
+// (1 x 131072 bf16, 1024 biases of one token 29 us, of 512 tokens twice 39, of
+// different ones 4.3; with a pass of the list for each addition 98600 and 427.)
+__device__ __noinline__ bool bias_sum(const BiasList& list, int n, int place, float* sum) {
+  const uint32_t slot = list.slot[place], both = slot * 0x10001u;
+  const uint4* eights = reinterpret_cast<const uint4*>(list.slot);
+  float total = list.value[place];
+#pragma unroll 2
+  for (int first = 0; first < n; first += 8) {
+    const uint4 q = eights[first / 8];
+    const uint32_t w[4] = {q.x ^ both, q.y ^ both, q.z ^ both, q.w ^ both};
+    uint32_t zero = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zero |= (w[i] - 0x00010001u) & ~w[i] & 0x80008000u;
+    if (zero == 0u) continue;
+    if (first + 8 <= place) return false;
+    const float4 lo = *reinterpret_cast<const float4*>(list.value + first), hi = *reinterpret_cast<const float4*>(list.value + first + 4);
+    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool hit = (w[i / 2] & (i % 2 ? 0xFFFF0000u : 0xFFFFu)) == 0u;
+      if (hit && first + i < place) return false;
+      const float next = __fadd_rn(total, v[i]);
+      total = hit && first + i > place ? next : total;
     }
-    if (next < 0) break;
-    total = __fadd_rn(total, list.value[next]);
-    last = list.place(next);
   }
   *sum = total;
   return true;
@@ -199,7 +213,7 @@ __host__ __device__ constexpr int threads_an_sm(int threads, int vecs) { return 
 template <int kType, int kThreads, int kVecs>
 __global__ void __launch_bounds__(kThreads, threads_an_sm(kThreads, kVecs) / kThreads) adjust_kernel(const AdjustParams p) {
   constexpr int kEach = 16 / kSize<kType>, kSpan = kThreads * kEach * kVecs;
-  static_assert(kSpan <= 1 << 16, "a slot has 16 bits");
+  static_assert(kSpan <= kOutside, "a slot has 16 bits");
   extern __shared__ uint4 s_words[];                    // [kSpan] words, then the tokens met
   uint32_t* words = reinterpret_cast<uint32_t*>(s_words);
   uint16_t* met = reinterpret_cast<uint16_t*>(words + kSpan);
@@ -295,21 +309,22 @@ __global__ void __launch_bounds__(kThreads, threads_an_sm(kThreads, kVecs) / kTh
     if (first - tid >= numbers.length) break;
     load_tokens(first, numbers.length);
   }
-  for (int b = tid; b < h.bias_count; b += kThreads) {
-    if (b != tid) bias_id = bias_ids[b], bias = biases[b];
+  for (int b = tid; b < ((h.bias_count + 7) & ~7); b += kThreads) {
+    if (b != tid) bias_id = b < h.bias_count ? bias_ids[b] : -1, bias = b < h.bias_count ? biases[b] : 0.0f;
     const uint32_t at = (uint32_t)bias_id - (uint32_t)lo;
-    if ((unsigned long long)bias_id >= (unsigned long long)p.V || at >= (uint32_t)kSpan) continue;
+    const bool in = (unsigned long long)bias_id < (unsigned long long)p.V && at < (uint32_t)kSpan;
+    list.slot[b] = (uint16_t)(in ? at : kOutside);
+    if (!in) continue;
     if ((atomicOr(&words[at], kBiased) & kBiased) != 0u) atomicOr(&words[at], kTwice);
-    const int i = atomicAdd(&list.count, 1);
-    list.entry[i] = ((uint32_t)b << 16) | at, list.value[i] = bias;
+    list.place[atomicAdd(&list.count, 1)] = (uint16_t)b, list.value[b] = bias;
   }
   __syncthreads();
 
   // ---- and changed, over what another thread has stored: those that were met and
   // have no bias, and those that have
   for (int i = tid; i < met_count + list.count; i += kThreads) {
-    const int b = i - met_count;
-    const uint32_t at = b < 0 ? met[i] : list.slot(b), word = words[at];
+    const int b = i < met_count ? -1 : list.place[i - met_count];
+    const uint32_t at = b < 0 ? met[i] : list.slot[b], word = words[at];
     const int e = lo + (int)at;
     const uint32_t bits = load_one<kType>(logits, e);
     const uint32_t ok = allowed ? allowed[e >> 5] >> (e & 31) : 1u;
@@ -318,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, threads_an_sm(kThreads, kVecs) / kTh
       if ((word & kBiased) != 0u) continue;
     } else if ((word & kTwice) == 0u) {
       sum = list.value[b];
-    } else if (!bias_sum(list, b, &sum)) {
+    } else if (!bias_sum(list, h.bias_count, b, &sum)) {
       continue;
     }
     if ((ok & 1u) == 0u) continue;

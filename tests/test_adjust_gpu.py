@@ -233,6 +233,50 @@ def test_bias_counts(B):
     check(logits(3, 500, g, F32), **parts(3, 500, g, B=B))
 
 
+def repeated(how, M, V, B, g):
+    """bias_ids of one token, of tokens that are there twice (beside each other and half
+    the list apart), of some and a padding of zeros, and of different ones."""
+    rows = {"one": torch.full((B,), min(5, V - 1)), "twice": torch.arange(B) // 2, "apart": torch.arange(B) % (B // 2),
+            "padded": torch.cat([torch.arange(1, 21), torch.zeros(B - 20, dtype=torch.long)]), "different": torch.arange(B)}
+    return (rows[how] % V).to(DEV).expand(M, B).contiguous()
+
+
+@pytest.mark.parametrize("how", ["one", "twice", "apart", "padded"])
+@pytest.mark.parametrize("dtype,M,V", [(F32, 2, 700), (BF16, 3, 9001), (F16, 2, 40000)])
+@pytest.mark.parametrize("B", [300, 1023, 1024])
+def test_biases_of_the_same_tokens(how, dtype, M, V, B):
+    """The sum in the list's order, whatever of it one token takes."""
+    g = gen(B)
+    values = torch.randn(M, B, device=DEV, generator=g) * torch.where(torch.rand(M, B, device=DEV, generator=g) < 0.2, 1e4, 1.0)
+    check(logits(M, V, g, dtype), bias_ids=repeated(how, M, V, B, g), bias_values=values, **parts(M, V, g, H=40, allow=0.9))
+
+
+@pytest.mark.parametrize("how", ["one", "twice", "apart", "padded"])
+@pytest.mark.parametrize("M,V", [(1, 131072), (64, 32000)])
+def test_biases_of_the_same_tokens_take_no_longer(how, M, V):
+    """A list is gone over once for each of its tokens, by as many threads: 1024 steps, a
+    few microseconds, beside a list of different tokens (a pass for each entry of one
+    token took a thousand times as long)."""
+    g, B = gen(1), 1024
+    x, v = logits(M, V, g, BF16), torch.randn(M, B, device=DEV, generator=g)
+    out = torch.empty_like(x)
+
+    def time(ids):
+        best = float("inf")
+        for _ in range(5):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(4):
+                sk.splitk_adjust_logits(x, bias_ids=ids, bias_values=v, out=out)
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(end) / 4)
+        return best
+
+    other, same_tokens = time(repeated("different", M, V, B, g)), time(repeated(how, M, V, B, g))
+    assert same_tokens <= 10 * other + 0.02, (same_tokens, other)
+
+
 def test_more_biases_than_it_takes_are_refused():
     with pytest.raises(sk.SplitKError, match="INVALID_ARGUMENT"):
         sk.splitk_adjust_logits(torch.zeros(1, 50, device=DEV), bias_ids=torch.zeros(1, 1025, dtype=torch.long, device=DEV),
