@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "splitk_device.cuh"
+#include "splitk_internal.h"
 
 namespace splitk {
 
@@ -54,6 +55,38 @@ __device__ __forceinline__ float mx_inverse_scale(uint32_t code) { return __uint
 // The scale that a code stands for: 2^(code - 127), subnormal for 0, NaN for 255.
 __device__ __forceinline__ float mx_scale(uint32_t code) {
   return __uint_as_float(code == 0 ? 0x00400000u : code == kMxNaN ? 0x7FC00000u : code << 23);
+}
+
+// ---------------------------------------------------------------- the product's shared memory
+constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
+constexpr int kMxStages = 4;                         // of the ring, at most
+// K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks and its
+// scales a scale warp ~400, the MMAs of one tile 288 to 512 (1x500x16384 7.3 us with one,
+// 6.7 with two; 16x4096x7168 7.5, 7.4; 7x2080x256 3.7, 3.8).  Each tile's
+// place is free for the next copies by itself (with whole stages, the copies came too late:
+// 2048x18432x7168 93 us, so 90; 1000x7168x16384 54, 51).
+constexpr int kSub = 2;
+constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
+constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
+constexpr int kGroup = 4;                            // K tiles whose scales the scale warps exchange at once
+constexpr uint32_t kMxBarBytes = 512;
+
+// (of the half of the tokens that a CTA brings)
+__host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok / 2 * (kTileK / 2); }
+__host__ __device__ constexpr int groups_b(int tok) { return (tok + 127) / 128; }     // of 128 tokens
+__host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAtom * (1u + groups_b(tok)); }
+__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kSub * (kCodesA + codes_b(tok)); }
+
+// A CTA's shared memory: codes of A, codes of B, scales, barriers.  A share of split K
+// leaves its sums from the start on (tokens of 128 f32), over what its MMAs have read, while
+// others still wait on the barriers: they lie behind the longer of both.  (256 tokens'
+// sums pass a ring of one stage, 128 KiB and 88.)
+__host__ __device__ constexpr uint32_t mx_ring_bytes(int tok, int stages) {
+  return (uint32_t)stages * stage_bytes(tok) + 2u * kGroup * scales_of(tok);
+}
+__host__ __device__ constexpr uint32_t mx_sum_bytes(int tok, int split) { return split > 1 ? (uint32_t)tok * kMmaM * 4u : 0u; }
+__host__ __device__ constexpr uint32_t mx_bars_at(int tok, int stages, int split) {
+  return mx_ring_bytes(tok, stages) > mx_sum_bytes(tok, split) ? mx_ring_bytes(tok, stages) : mx_sum_bytes(tok, split);
 }
 
 }  // namespace splitk

@@ -52,26 +52,9 @@ namespace {
 // takes the issuing thread twice its time.)
 constexpr int kScale0 = 4, kScaleWarps = 4, kOut0 = kScale0 + kScaleWarps, kOutWarps = 4;
 constexpr int kMxThreads = 32 * (kOut0 + kOutWarps);
-constexpr int kTileK = 256;                          // codes of a K tile: 128 bytes
-constexpr int kMxStages = 4;                         // of the ring, at most
-// K tiles of a stage: a stage's wait and commit take the issuing warp ~230 clocks and its
-// scales a scale warp ~400, the MMAs of one tile 288 to 512 (1x500x16384 7.3 us with one,
-// 6.7 with two; 16x4096x7168 7.5, 7.4; 7x2080x256 3.7, 3.8).  Each tile's
-// place is free for the next copies by itself (with whole stages, the copies came too late:
-// 2048x18432x7168 93 us, so 90; 1000x7168x16384 54, 51).
-constexpr int kSub = 2;
-constexpr uint32_t kCodesA = kMmaM * (kTileK / 2);   // 16 KiB
-constexpr uint32_t kScaleAtom = 512;                 // 128 rows x 4 scales
-constexpr int kGroup = 4;                            // K tiles whose scales the scale warps exchange at once
-constexpr uint32_t kMxBarBytes = 512;
 constexpr int kMaxSplit = 4;                         // pairs of a cluster
 constexpr unsigned long long kDrainNs = 10000000ull; // 10 ms
 
-// (of the half of the tokens that a CTA brings)
-__host__ __device__ constexpr uint32_t codes_b(int tok) { return (uint32_t)tok / 2 * (kTileK / 2); }
-__host__ __device__ constexpr int groups_b(int tok) { return (tok + 127) / 128; }     // of 128 tokens
-__host__ __device__ constexpr uint32_t scales_of(int tok) { return 2u * kScaleAtom * (1u + groups_b(tok)); }
-__host__ __device__ constexpr uint32_t stage_bytes(int tok) { return kSub * (kCodesA + codes_b(tok)); }
 __host__ __device__ constexpr uint32_t mx_acc_cols(int tok) { return tok < 32 ? 32u : (uint32_t)tok; }
 __host__ __device__ constexpr uint32_t scale_cols(int tok) { return 8u * (1u + groups_b(tok)); }   // of a K tile
 
@@ -352,7 +335,7 @@ __device__ __forceinline__ void bring_scales(const MxParams& p, const ScaleRing&
 }
 
 // A cluster takes tiles gridDim.x / cluster size apart; with split > 1 one alone
-// (its sums go where the ring was).
+// (its sums go where the ring was, below the barriers).
 template <int kTok>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mx4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const MxParams p) {
@@ -362,7 +345,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const uint32_t s_a = base;
   const uint32_t s_b = s_a + (uint32_t)stages * kSub * kCodesA;
   const uint32_t s_s = s_b + (uint32_t)stages * kSub * codes_b(kTok);
-  const uint32_t s_bar = s_s + 2u * kGroup * scales_of(kTok);
+  const uint32_t s_bar = base + mx_bars_at(kTok, stages, split);
   const uint32_t bar_full = s_bar;                          // [kMxStages] leader: both CTAs' codes and scales are there
   const uint32_t bar_done = bar_full + 8u * kMxStages;      // [kMxStages] the MMAs have read them
   const uint32_t bar_half = bar_done + 8u * kMxStages;      // [kMxStages] those of the first of two K tiles have read it
@@ -647,9 +630,8 @@ constexpr int kTokens[] = {16, 32, 64, 128, 256};
 // that fit one SM by shared memory, of whatever kernels, never wait for each
 // other's columns.
 size_t mx_smem(int tok, int stages, int split, uint32_t cols, const DeviceSize& dev) {
-  const size_t ring = (size_t)kAlignSlack + (size_t)stages * stage_bytes(tok) + 2 * kGroup * (size_t)scales_of(tok) + kMxBarBytes;
-  const size_t sums = split > 1 ? (size_t)kAlignSlack + (size_t)tok * kMmaM * 4 : 0;
-  return std::max(std::max(ring, sums), std::min(dev.smem_per_sm * cols / 512, dev.smem_optin));
+  const size_t own = (size_t)kAlignSlack + mx_bars_at(tok, stages, split) + kMxBarBytes;
+  return std::max(own, std::min(dev.smem_per_sm * cols / 512, dev.smem_optin));
 }
 
 // The ring for CTAs of `steps` stages' shares of K (of all their tiles).

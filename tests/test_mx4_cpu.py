@@ -181,3 +181,39 @@ def test_the_binding_refuses_tensors_that_are_not_on_a_gpu():
             call()
     with pytest.raises(ValueError, match="device"):
         sk.splitk_gemm_mx4(meta(64, 32, dtype=U8), meta(64, 2, dtype=U8), codes, scale)
+
+
+# ---------------------------------------------------------------- the product's shared memory
+LAYOUT = r"""
+#include <stdio.h>
+#include "splitk_mx4.cuh"
+int main() {
+  for (int tokens : {16, 32, 64, 128, 256}) {
+    for (int stages = 1; stages <= splitk::kMxStages; ++stages) {
+      for (int split = 1; split <= 4; ++split) {
+        printf("%d %d %d %u %u\n", tokens, stages, split, splitk::mx_ring_bytes(tokens, stages),
+               splitk::mx_bars_at(tokens, stages, split));
+      }
+    }
+  }
+}
+"""
+
+
+def test_a_shares_sums_end_before_the_barriers(tmp_path):
+    """Sums of a tile's shares lie over the ring, and the barriers behind both, whatever
+    tile, depth and split are chosen: 128 weight rows of f32 a token."""
+    import subprocess
+    (tmp_path / "layout.cu").write_text(LAYOUT)
+    exe = tmp_path / "layout"
+    res = subprocess.run([_build._nvcc(), *_build.ARCH_FLAGS, "-std=c++17", "-I", str(_build.INCLUDE), "-I", str(_build.CSRC),
+                          str(tmp_path / "layout.cu"), "-o", str(exe)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-3000:]
+    rows = [tuple(map(int, line.split())) for line in subprocess.run([exe], capture_output=True, text=True).stdout.splitlines()]
+    assert len(rows) == 5 * 4 * 4
+    for tokens, stages, split, ring, bars in rows:
+        # a stage: two K tiles of 128 bytes of 128 weight rows and half of the tokens
+        assert ring >= stages * 2 * 128 * (128 + tokens // 2)
+        assert bars >= ring and bars % 8 == 0, (tokens, stages, split)
+        if split > 1:
+            assert bars >= tokens * 128 * 4, (tokens, stages, split, bars)
