@@ -253,10 +253,11 @@ struct NormParams {
 
 // A sum of squares as a whole number of 2^-shift.
 struct FixedSum {
-  int units;                // at most 2^31, of 32 addends below 2^26
-  int shift;
-  bool bad;                 // an addend was NaN or infinite
+  uint32_t units;           // at most 2^31
+  float rest;               // of a unit: what a join of sums cut off below one
+  int shift;                // kBadShift: an addend was NaN or infinite
 };
+constexpr int kBadShift = -1024, kNoShift = 1024;       // (finite sums: -102 .. 151)
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -269,32 +270,50 @@ __device__ __forceinline__ float scaled(float v, int e) { return v * power_of_tw
 // took twice as long as its memory).
 __device__ __forceinline__ FixedSum warp_sum(float v) {
   const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));        // (NaN of either sign is above all)
-  FixedSum s;
-  s.bad = top >= 0x7F800000u;
-  s.shift = 25 - ((int)max(top >> 23, 1u) - 127);
-  s.units = __reduce_add_sync(0xFFFFFFFFu, s.bad ? 0 : __float2int_rn(scaled(v, s.shift)));
-  return s;
+  const bool bad = top >= 0x7F800000u;
+  const int shift = 25 - ((int)max(top >> 23, 1u) - 127);
+  const int units = __reduce_add_sync(0xFFFFFFFFu, bad ? 0 : __float2int_rn(scaled(v, shift)));
+  return {(uint32_t)units, 0.0f, bad ? kBadShift : shift};
+}
+
+// The sum of up to 32 warps' sums, one a lane (kNoShift in the others): in units of 32
+// of the coarsest, and 27 bits below them, so nothing is cut off of a sum whose own unit
+// is 2^-22 of the coarsest or more.  (With each warp's 31 bits passed on as an f32 value, 24
+// rows in a hundred of 1024 f32 values had another mean, now 6.)
+__device__ __forceinline__ FixedSum join_sums(uint32_t units, int shift) {
+  const int coarsest = __reduce_min_sync(0xFFFFFFFFu, shift);
+  const unsigned long long w = ((unsigned long long)units << 32) >> min(shift - coarsest + 5, 63);
+  const uint32_t whole = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)(w >> 32));
+  const uint32_t rest = __reduce_add_sync(0xFFFFFFFFu, (uint32_t)w >> 5);
+  return {whole, (float)rest * 0x1p-27f, coarsest == kBadShift ? kBadShift : coarsest - 5};
 }
 
 // 1 / sqrt(mean + eps) of the row, in every thread of it, from the threads' own sums
-// of 8 to 32 squares (f32, whose errors average out over the row).  The mean is the
-// exact one rounded to f32 for all but a few rows in a hundred, so codes do not
-// depend on the order of additions.  A row is one warp (blockDim.x = 32) or the whole
-// CTA, which takes turns between two buffers.  NaN for a row whose sum passes f32.
+// of 8 to 32 squares, which are f32 and the one thing that rounds on the way: the mean
+// does not depend on the order of additions.  By a model of this arithmetic, rows of
+// normal values whose mean is not the exact one rounded to f32, but its neighbour, are 2 in
+// a hundred at 7168 with an f32 residual, 4 to 6 at 1024 and 2048, and 10 to 25 with values
+// of bf16 (28 to 43 above 16384, a thread's 32 squares).  A row is one warp
+// (blockDim.x = 32) or the whole CTA, which takes turns between two buffers.  NaN for a row
+// whose sum passes f32.
 __device__ __forceinline__ float row_factor(const NormParams& p, float own, int turn) {
   FixedSum s = warp_sum(own);
   if (blockDim.x != 32) {
-    __shared__ float s_sum[2][32];
+    __shared__ int2 s_sum[2][32];
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, warps = (int)blockDim.x >> 5;
-    if (lane == 0) s_sum[turn][warp] = s.bad ? __uint_as_float(0x7FC00000u) : scaled((float)s.units, -s.shift);
+    if (lane == 0) s_sum[turn][warp] = make_int2((int)s.units, s.shift);
     __syncthreads();
-    s = warp_sum(lane < warps ? s_sum[turn][lane] : 0.0f);
+    const int2 one = lane < warps ? s_sum[turn][lane] : make_int2(0, kNoShift);
+    s = join_sums((uint32_t)one.x, one.y);
   }
+  const bool bad = s.shift == kBadShift;
+  const int shift = bad ? 0 : s.shift;
   // units 2^-shift / width, as the f32 quotient and what it leaves
-  const float hi = __int2float_rz(s.units), lo = (float)(s.units - (int)hi), inverse = p.mean_of, width = (float)p.width;
+  const float hi = __uint2float_rz(s.units), lo = (float)(s.units - (uint32_t)hi) + s.rest;
+  const float inverse = p.mean_of, width = (float)p.width;
   const float q = hi * inverse, mean = q + (fmaf(-q, width, hi) + lo) * inverse;
-  const float factor = 1.0f / sqrtf(scaled(mean, -s.shift) + p.eps);
-  const bool past = s.bad || !(scaled(hi, -s.shift) <= 3.4028234e38f);
+  const float factor = 1.0f / sqrtf(scaled(mean, -shift) + p.eps);
+  const bool past = bad || !(scaled(hi, -shift) <= 3.4028234e38f);
   return past ? __uint_as_float(0x7FC00000u) : factor;
 }
 

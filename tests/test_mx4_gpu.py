@@ -313,6 +313,46 @@ def test_norm_is_the_elementary_operations_to_the_bit():
     assert off <= 2, off
 
 
+@pytest.mark.parametrize("D,residual", [(64, None), (64, BF16), (1024, None), (1024, F32), (7168, None), (7168, BF16)])
+def test_norm_of_other_rows_is_the_elementary_operations_to_the_bit(D, residual):
+    """As above.  A thread's sums move the mean to a neighbour in up to one row of four
+    here; the factor then moves by at most one in 2^23, which takes a value of a row
+    over a border of codes once in some 10^7: of 2048 rows less than one, on average."""
+    g = gen(D)
+    x, w = randn((2048, D), g, BF16), (1 + randn((D,), g, F32, 0.1)).to(BF16)
+    r = None if residual is None else randn((2048, D), g, residual, 4.0)
+    codes, scale, _ = sk.splitk_rmsnorm_mx4(x, w, r)
+    sync()
+    y = x.float() if r is None else x.float() + r.float()
+    n = y * w.float() * (1 / torch.sqrt(y.double().square().mean(1, keepdim=True).float() + 1e-6))
+    want, want_scale = quantised(n.double())
+    off = ((unpack(codes) != want).any(1) | (scale.long() != want_scale).any(1)).sum().item()
+    assert off <= 2, off
+
+
+@pytest.mark.parametrize("M", [1, 700])
+@pytest.mark.parametrize("D", [64, 512, 544, 1024, 2048, 4992, 7168, 20480])
+def test_norm_joins_its_threads_sums_without_a_loss(M, D):
+    """Whole numbers whose squares a thread sums exactly (32 of at most 723^2 are below
+    2^24), so that the mean is the exact one, rounded once; and weights that bring every
+    value of the row to a border between two codes, where another mean shows."""
+    g = gen(D)
+    grid = torch.tensor(GRID, dtype=F64, device=DEV)
+    middle = (grid[1:] + grid[:-1]) / 2
+    for _ in range(30):
+        y = torch.randint(1, 724, (D,), device=DEV, generator=g) * (2 * torch.randint(0, 2, (D,), device=DEV, generator=g) - 1)
+        x = torch.randint(-200, 201, (D,), device=DEV, generator=g).to(BF16)
+        r = (y - x.long()).float()
+        factor = 1 / torch.sqrt(y.double().square().mean().float() + 1e-6)
+        goal = middle[torch.randint(0, 7, (D,), device=DEV, generator=g)]
+        goal[::32] = 5.0                                               # every block's scale is 1
+        w = (goal / (y.double() * factor.double())).float()
+        codes, scale, _ = sk.splitk_rmsnorm_mx4(x.expand(M, D).contiguous(), w, r.expand(M, D).contiguous())
+        sync()
+        want, want_scale = quantised((y.float() * w * factor).double())
+        assert (scale.long() == want_scale).all() and (unpack(codes) == want).all()
+
+
 # ---------------------------------------------------------------- product
 def random_codes(shape, g, low=120, high=134):
     """Codes, and scale codes of a few binades."""
