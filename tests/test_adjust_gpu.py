@@ -312,6 +312,31 @@ def test_workload_sizes(M, V, dtype):
     assert torch.equal(out[free], x[free])
 
 
+@pytest.mark.parametrize("V", [50003, 50048])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("H", [0, 300, 600])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_large_batches(dtype, H, pad, V):
+    """Batches of more than 2048 vectors an SM, which the longest spans take: every type,
+    short and long histories, and logits whose rows lie otherwise between 16-byte
+    boundaries than the outputs'."""
+    each = 16 // dtype.itemsize
+    M = 2048 * torch.cuda.get_device_properties(0).multi_processor_count // (V // each) + 2
+    g = gen(V + H + pad)
+    x, how = logits(M, V, g, dtype, pad), parts(M, V, g, H=H, B=8, allow=0.9)
+    few = torch.tensor([0, 1, M // 2, M - 2, M - 1], device=DEV)
+    out = sk.splitk_adjust_logits(x, **how)
+    sync()
+    assert same(out[few], reference(x[few], **{k: v[few] for k, v in how.items()}))
+    allowed = (how["allowed"].long()[:, :, None] >> torch.arange(32, device=DEV) & 1).flatten(1)[:, :V] > 0
+    assert torch.isneginf(out[~allowed]).all()
+    touched = torch.zeros(M, V, dtype=torch.bool, device=DEV).scatter_(1, how["bias_ids"].clamp_min(0), True)
+    if H:
+        touched.scatter_(1, how["history"].clamp(0, V - 1), True)
+    free = allowed & ~touched
+    assert torch.equal(out[free], x[free])
+
+
 def test_past_32_bit_offsets():
     """Logits of more than 2^31 elements: the last rows as the first."""
     M, V = 17000, 131072
