@@ -463,6 +463,27 @@ def test_nan_scales_reach_their_rows_alone(M):
     assert torch.equal(torch.isnan(c), want)
 
 
+@pytest.mark.parametrize("by", ["quantise", "norm"])
+@pytest.mark.parametrize("M", [3, 50, 300])
+@pytest.mark.parametrize("K", [32, 1056, 4128])
+def test_nan_and_infinite_values_reach_their_rows_alone(M, K, by):
+    """What the quantisation and the norm make of them, zeros under a scale that is no
+    number, on both sides; the last 64 of K are half full."""
+    g = gen(M + K)
+    w, x = randn((300, K), g, BF16), randn((M, K), g, BF16)
+    w[17, K - 1], w[129, 0], w[299, K // 2] = float("nan"), float("inf"), float("-inf")
+    x[0, 0], x[1, K - 1], x[M - 1, 5] = float("inf"), float("nan"), float("-inf")
+    a = sk.splitk_quantize_mx4(w)
+    b = sk.splitk_quantize_mx4(x) if by == "quantise" else sk.splitk_rmsnorm_mx4(x, torch.ones(K, device=DEV))[:2]
+    c = sk.splitk_gemm_mx4(*a, *b, out_dtype=F32)
+    sync()
+    assert (a[1] == 255).any(1).sum() == 3 and (b[1] == 255).any(1).sum() == 3
+    want = torch.zeros(M, 300, dtype=torch.bool, device=DEV)
+    want[:, [17, 129, 299]] = True
+    want[[0, 1, M - 1]] = True
+    assert torch.equal(torch.isnan(c), want) and torch.isfinite(c[~want]).all()
+
+
 @pytest.mark.parametrize("M", [1, 8, 33, 129, 700])
 def test_product_runs_the_same_twice(M):
     ops = product_inputs(1, M, 1000, 4096, M)
