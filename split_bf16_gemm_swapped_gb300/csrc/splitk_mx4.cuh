@@ -9,6 +9,8 @@
 // The largest value is then 4 to 8 times its scale (past 6 it is cut off, as the
 // format's standard scale does), the quotient is exact, and no scale leaves
 // 1 .. 252.  A block that holds a NaN or an infinity has scale 255 and codes 0.
+//
+// And the shared memory of the product of such codes (splitk_mx4_gemm.cu).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -9,7 +9,8 @@
 // block of 32, whose largest magnitude two exchanges of lanes give them all.
 // Every byte is read and written once; memory is the bound: codes of 18432 x 7168 bf16
 // 51.0 us and back 51.0 (6.6 TB/s, 98 % of a copy's rate), norm of 2048 x 7168 with an
-// f32 residual 27.5 us (5.6 TB/s), of one row 2.4 us (launch and a chain of latencies).
+// f32 residual 27.5 us (5.6 TB/s), of one row 2.3 us (launch and a chain of latencies).
+// (Rows of 16416 to 32768 with an f32 residual spill some 550 bytes a thread: 512 x 32768 80.6 us.)
 // Issue comes next: with 64-bit places and the largest magnitude in f32, codes took 93
 // instructions a vector and 60 us.
 
@@ -292,8 +293,8 @@ __device__ __forceinline__ FixedSum join_sums(uint32_t units, int shift) {
 // of 8 to 32 squares, which are f32 and the one thing that rounds on the way: the mean
 // does not depend on the order of additions.  By a model of this arithmetic, rows of
 // normal values whose mean is not the exact one rounded to f32, but its neighbour, are 2 in
-// a hundred at 7168 with an f32 residual, 4 to 6 at 1024 and 2048, and 10 to 25 with values
-// of bf16 (28 to 43 above 16384, a thread's 32 squares).  A row is one warp
+// a hundred at 7168 with an f32 residual, 4 to 6 at 1024 and 2048, 8 to 25 up to 512, and 9
+// to 22 with values of bf16 (28 to 43 above 16384, a thread's 32 squares).  A row is one warp
 // (blockDim.x = 32) or the whole CTA, which takes turns between two buffers.  NaN for a row
 // whose sum passes f32.
 __device__ __forceinline__ float row_factor(const NormParams& p, float own, int turn) {
